@@ -210,6 +210,79 @@ dsa_status dsa_sparse_attn_mxfp4(const uint16_t* q, int64_t T, int H, int D, con
                                         static_cast<cudaStream_t>(stream)));
 }
 
+dsa_status dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens, int B, int block_size,
+                            const int32_t* free_blocks, int n_free, int64_t num_blocks, int32_t* block_table,
+                            int64_t bt_stride, int64_t max_tokens, int32_t* context_lens, int32_t* query_start,
+                            int64_t* slot_mapping, int32_t* positions, int32_t* blocks_used, void* stream) {
+  if (B < 0 || block_size < 1 || n_free < 0 || num_blocks < 0 || max_tokens < 0) return DSA_ERR_INVALID_ARG;
+  if (B > 65536 || max_tokens > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (query_start == nullptr || blocks_used == nullptr) return DSA_ERR_INVALID_ARG;
+  if (B > 0 && (cached_lens == nullptr || new_lens == nullptr || context_lens == nullptr || block_table == nullptr ||
+                bt_stride < 1))
+    return DSA_ERR_INVALID_ARG;
+  if (n_free > 0 && free_blocks == nullptr) return DSA_ERR_INVALID_ARG;
+  if (max_tokens > 0 && (slot_mapping == nullptr || positions == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (!aligned(cached_lens, 4) || !aligned(new_lens, 4) || !aligned(free_blocks, 4) || !aligned(block_table, 4) ||
+      !aligned(context_lens, 4) || !aligned(query_start, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 4) ||
+      !aligned(blocks_used, 4))
+    return DSA_ERR_INVALID_ARG;
+  // every CTA reads all lengths while others write their results
+  const void* out[] = {block_table, context_lens, query_start, slot_mapping, positions, blocks_used};
+  const void* in[] = {cached_lens, new_lens, free_blocks};
+  for (int i = 0; i < 6; ++i) {
+    if (out[i] == nullptr) continue;
+    for (int j = 0; j < 3; ++j)
+      if (out[i] == in[j]) return DSA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[i] == out[j]) return DSA_ERR_INVALID_ARG;
+  }
+  return cuda_status(launch_assign_slots(cached_lens, new_lens, B, block_size, free_blocks, n_free, num_blocks,
+                                         block_table, bt_stride, max_tokens, context_lens, query_start, slot_mapping,
+                                         positions, blocks_used, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
+                                float eps, int64_t T, int D, dsa_real type, void* residual_out, void* y,
+                                uint8_t* y_fp8, int64_t ldy, float* y_scale, int pow2_scale, void* stream) {
+  if (type != DSA_REAL_BF16 && type != DSA_REAL_F32) return DSA_ERR_INVALID_ARG;
+  if (T < 0 || D < 1 || !(eps > 0.f) || !std::isfinite(eps)) return DSA_ERR_INVALID_ARG;
+  if (D > add_rmsnorm_max_dim() || T > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (T == 0) return DSA_OK;
+  if (x == nullptr || gamma == nullptr || ldx < D) return DSA_ERR_INVALID_ARG;
+  if ((y_fp8 == nullptr) != (y_scale == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (residual_out == nullptr && y == nullptr && y_fp8 == nullptr) return DSA_ERR_INVALID_ARG;
+  if ((residual != nullptr || residual_out != nullptr) && ldr < D) return DSA_ERR_INVALID_ARG;
+  if ((y != nullptr || y_fp8 != nullptr) && ldy < D) return DSA_ERR_INVALID_ARG;
+  const uintptr_t el = type == DSA_REAL_F32 ? 4 : 2;
+  if (!aligned(x, el) || !aligned(residual, el) || !aligned(residual_out, el) || !aligned(y, el) ||
+      !aligned(gamma, 4) || !aligned(y_scale, 4))
+    return DSA_ERR_INVALID_ARG;
+  // in place only where a thread writes the elements it has read
+  if (residual_out == x && ldr != ldx) return DSA_ERR_INVALID_ARG;
+  if (y == x && ldy != ldx) return DSA_ERR_INVALID_ARG;
+  if (y != nullptr && (y == residual || y == residual_out)) return DSA_ERR_INVALID_ARG;
+  return cuda_status(launch_add_rmsnorm_e4m3(x, ldx, residual, ldr, gamma, eps, T, D, type == DSA_REAL_F32,
+                                             residual_out, y, y_fp8, ldy, y_scale, pow2_scale != 0,
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* w, int64_t ldw,
+                         const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, dsa_real out_type,
+                         void* stream) {
+  if (out_type != DSA_REAL_BF16 && out_type != DSA_REAL_F32) return DSA_ERR_INVALID_ARG;
+  if (M < 0 || N < 0 || K < 1) return DSA_ERR_INVALID_ARG;
+  if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return DSA_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return DSA_OK;
+  if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)
+    return DSA_ERR_INVALID_ARG;
+  if (lda < K || ldw < K || ldo < N || lda % 16 != 0 || ldw % 16 != 0) return DSA_ERR_INVALID_ARG;
+  if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
+      !aligned(out, out_type == DSA_REAL_F32 ? 4 : 2))
+    return DSA_ERR_INVALID_ARG;
+  return cuda_status(launch_gemm_e4m3(a, lda, a_scale, w, ldw, w_scale, M, N, K, out, ldo, out_type == DSA_REAL_F32,
+                                      device_sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
 size_t dsa_workspace_bytes(dsa_op op, dsa_dtype dtype, dsa_queries qs, int topk) {
   if (check_queries(qs) != DSA_OK || topk < 1 || topk > 2048) return 0;
   if (op == DSA_OP_TOPK) return plan_topk(qs, topk).ws_bytes;

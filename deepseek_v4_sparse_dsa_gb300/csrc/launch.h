@@ -103,6 +103,20 @@ cudaError_t launch_q_rope_quant(const uint16_t* q, const int32_t* positions, con
 cudaError_t launch_k_hadamard_mxfp4(const uint16_t* k, const int64_t* slot, int64_t n, uint8_t* fp4, uint8_t* scale,
                                     int64_t num_rows, int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------------------------ input preparation
+// (slots.cu, norm_quant.cu, gemm_e4m3.cu)
+cudaError_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, int B, int bs, const int32_t* free_blocks,
+                                int n_free, int64_t num_blocks, int32_t* table, int64_t bt_stride, int64_t max_tokens,
+                                int32_t* context, int32_t* start, int64_t* slot, int32_t* pos, int32_t* used,
+                                cudaStream_t stream);
+cudaError_t launch_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* res, int64_t ldr, const float* gamma,
+                                    float eps, int64_t T, int D, bool f32, void* res_out, void* y, uint8_t* codes,
+                                    int64_t ldy, float* scale, bool pow2, cudaStream_t stream);
+int add_rmsnorm_max_dim();
+cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* w, int64_t ldw,
+                             const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, bool out_f32,
+                             int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------------------------ sparse attention (sparse_attn.cu)
 // q [T, 64, 128] bf16 (16-byte aligned), sel [T, k], the paged mxfp4 cache, sink [64],
 // out [T, 64, 128] fp32.  One CTA per query row.
@@ -138,6 +152,8 @@ DSA_DECLARE_TU_ERROR_ACCESSORS(indexer_fp8_logits)
 DSA_DECLARE_TU_ERROR_ACCESSORS(topk)
 DSA_DECLARE_TU_ERROR_ACCESSORS(producer)
 DSA_DECLARE_TU_ERROR_ACCESSORS(attn)
+DSA_DECLARE_TU_ERROR_ACCESSORS(slots)
+DSA_DECLARE_TU_ERROR_ACCESSORS(gemm)
 
 // Every translation unit's accessors, for dsa_device_error / dsa_set_wait_limit_ns.
 struct TuWords {
@@ -149,7 +165,7 @@ inline const TuWords* all_tu_words(int* n) {
   static const TuWords w[] = {DSA_TU_WORDS(gather), DSA_TU_WORDS(indexer), DSA_TU_WORDS(indexer_bf16_topk),
                               DSA_TU_WORDS(indexer_bf16_logits), DSA_TU_WORDS(indexer_fp8_topk),
                               DSA_TU_WORDS(indexer_fp8_logits), DSA_TU_WORDS(topk), DSA_TU_WORDS(producer),
-                              DSA_TU_WORDS(attn)};
+                              DSA_TU_WORDS(attn), DSA_TU_WORDS(slots), DSA_TU_WORDS(gemm)};
   *n = (int)(sizeof(w) / sizeof(w[0]));
   return w;
 }

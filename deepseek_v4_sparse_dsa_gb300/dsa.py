@@ -18,6 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libdsa_gb300.so")
 
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_WORKSPACE = 0, 1, 2, 3, 4
 DSA_BF16, DSA_E4M3, DSA_E4M3_MXFP4K = 0, 1, 2
+DSA_REAL_BF16, DSA_REAL_F32 = 0, 1
 DSA_OP_TOPK, DSA_OP_LOGITS_TOPK = 1, 2
 DSA_DEVERR_INDEX, DSA_DEVERR_TIMEOUT = 1, 2
 
@@ -82,6 +83,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "dsa_sparse_attn_mxfp4": (c_int, [c_void_p, c_int64, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p,
                                           c_int64, c_int, c_void_p, c_int64, c_int, c_void_p, c_float, c_void_p,
                                           c_void_p]),
+        "dsa_assign_slots": (c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_int64, c_void_p, c_int64,
+                                     c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "dsa_add_rmsnorm_e4m3": (c_int, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_float, c_int64, c_int,
+                                         c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p]),
+        "dsa_gemm_e4m3": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_int, c_int,
+                                  c_void_p, c_int64, c_int, c_void_p]),
         "dsa_workspace_bytes": (c_size_t, [c_int, c_int, dsa_queries, c_int]),
         "dsa_status_string": (ctypes.c_char_p, [c_int]),
         "dsa_device_error": (c_int, [c_void_p]),
@@ -186,6 +193,27 @@ def dsa_indexer_k_hadamard_mxfp4(k, slot_mapping, N, D, kv_fp4, kv_scale, num_ro
     _check(load().dsa_indexer_k_hadamard_mxfp4(_ptr(k), _ptr(slot_mapping), int(N), int(D), _ptr(kv_fp4),
                                                _ptr(kv_scale), int(num_rows), _stream(stream)),
            "dsa_indexer_k_hadamard_mxfp4")
+
+
+def dsa_assign_slots(cached_lens, new_lens, B, block_size, free_blocks, n_free, num_blocks, block_table, bt_stride,
+                     max_tokens, context_lens, query_start, slot_mapping, positions, blocks_used, stream=None):
+    _check(load().dsa_assign_slots(_ptr(cached_lens), _ptr(new_lens), int(B), int(block_size), _ptr(free_blocks),
+                                   int(n_free), int(num_blocks), _ptr(block_table), int(bt_stride), int(max_tokens),
+                                   _ptr(context_lens), _ptr(query_start), _ptr(slot_mapping), _ptr(positions),
+                                   _ptr(blocks_used), _stream(stream)), "dsa_assign_slots")
+
+
+def dsa_add_rmsnorm_e4m3(x, ldx, residual, ldr, gamma, eps, T, D, type, residual_out, y, y_fp8, ldy, y_scale,
+                         pow2_scale=False, stream=None):
+    _check(load().dsa_add_rmsnorm_e4m3(_ptr(x), int(ldx), _ptr(residual), int(ldr), _ptr(gamma), float(eps), int(T),
+                                       int(D), int(type), _ptr(residual_out), _ptr(y), _ptr(y_fp8), int(ldy),
+                                       _ptr(y_scale), 1 if pow2_scale else 0, _stream(stream)),
+           "dsa_add_rmsnorm_e4m3")
+
+
+def dsa_gemm_e4m3(a, lda, a_scale, w, ldw, w_scale, M, N, K, out, ldo, out_type, stream=None):
+    _check(load().dsa_gemm_e4m3(_ptr(a), int(lda), _ptr(a_scale), _ptr(w), int(ldw), _ptr(w_scale), int(M), int(N),
+                                int(K), _ptr(out), int(ldo), int(out_type), _stream(stream)), "dsa_gemm_e4m3")
 
 
 def dsa_workspace_bytes(op, dtype, qs, topk) -> int:

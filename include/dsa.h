@@ -65,6 +65,9 @@ typedef enum {
  * forward path", "Status", names; see dsa_keys.scale_e8m0). */
 typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1, DSA_E4M3_MXFP4K = 2 } dsa_dtype;
 
+/* Storage of hidden rows and of a projection's result. */
+typedef enum { DSA_REAL_BF16 = 0, DSA_REAL_F32 = 1 } dsa_real;
+
 typedef enum { DSA_OP_TOPK = 1, DSA_OP_LOGITS_TOPK = 2 } dsa_op;
 
 /* Bits of the per-device error word (see dsa_device_error). */
@@ -272,6 +275,95 @@ dsa_status dsa_sparse_attn_mxfp4(const uint16_t* q, int64_t T, int H, int D, con
                                  const uint8_t* kv_fp4, const uint8_t* kv_scale, int64_t num_blocks,
                                  int block_size, const int32_t* block_table, int64_t bt_stride, int next_n,
                                  const float* sink, float softmax_scale, float* out, void* stream);
+
+/*
+ * The three calls that prepare a step's inputs.  (The pages start from finished queries,
+ * keys, weights, slots and tables; these calls make them in the layouts the calls above
+ * read.)  A layer's step uses them in this order: dsa_assign_slots gives every new token its
+ * cache slot and position; dsa_add_rmsnorm_e4m3 turns the hidden rows into E4M3 codes with
+ * one scale per 128 elements; dsa_gemm_e4m3 projects those to the queries
+ * (dsa_indexer_q_rope_quant), the keys (dsa_indexer_k_hadamard_mxfp4) and the fp32 head
+ * weights (the score calls).
+ *
+ * dsa_assign_slots -- block tables, slot mapping and positions from request lengths.
+ * Request b holds cached_lens[b] tokens in have_b = ceil(cached_lens[b] / block_size) pages
+ * and brings new_lens[b] >= 0 tokens, which need need_b = ceil((cached_lens[b] +
+ * new_lens[b]) / block_size) - have_b more.  With first_b = sum of need over the requests
+ * before b and start_b = sum of new_lens over them:
+ *   block_table[b, have_b + i] = free_blocks[first_b + i] for i < need_b (other entries stay);
+ *   new token t = start_b + i of the step, i < new_lens[b], has positions[t] =
+ *   cached_lens[b] + i and slot_mapping[t] = its pool row, block_table[b, pos / block_size] *
+ *   block_size + pos % block_size: the row dsa_indexer_k_hadamard_mxfp4 writes;
+ *   context_lens[b] = cached_lens[b] + new_lens[b]; query_start[b] = start_b, query_start[B]
+ *   = the step's tokens; blocks_used[0] = the free-list entries the step needs (the caller's
+ *   next step starts behind them).
+ * Entries [step's tokens, max_tokens) of slot_mapping are -1 (the key writer skips them) and
+ * of positions 0, so a captured graph can serve any step of up to max_tokens tokens.
+ *  cached_lens, new_lens [B] int32; free_blocks [n_free] int32 block ids of a pool of
+ *           num_blocks blocks; block_table [B, bt_stride] int32, updated in place.
+ *  context_lens [B], query_start [B + 1], blocks_used [1] int32; slot_mapping [max_tokens]
+ *           int64; positions [max_tokens] int32.  No output may overlap an input or another
+ *           output (the same address is refused).
+ * Flagged with DSA_DEVERR_INDEX, never accessed out of range: a negative length or a sum
+ * past INT32_MAX (the request brings nothing; a negative cached length counts as 0); a page
+ * at or past bt_stride (slot -1, no entry); a free-list rank at or past n_free or a block id
+ * outside [0, num_blocks) (slot -1; a new page's entry is -1); tokens at or past max_tokens
+ * (neither slot nor page).  Counts past INT32_MAX are written as INT32_MAX.
+ * block_size >= 1; B <= 65536.  One launch; the result does not depend on timing.
+ */
+dsa_status dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens, int B, int block_size,
+                            const int32_t* free_blocks, int n_free, int64_t num_blocks, int32_t* block_table,
+                            int64_t bt_stride, int64_t max_tokens, int32_t* context_lens, int32_t* query_start,
+                            int64_t* slot_mapping, int32_t* positions, int32_t* blocks_used, void* stream);
+
+/*
+ * dsa_add_rmsnorm_e4m3 -- residual addition, RMS norm and E4M3 quantisation.  For each of T
+ * rows of D elements:
+ *   r = x + residual, rounded once to `type` (r = x without a residual);
+ *   y = r * gamma / sqrt(mean(r^2) + eps), in fp32;
+ *   per group g of 128 elements (the last may be shorter): y_scale[t, g] = max|y| / 448 (at
+ *   least 2^-126; 1 for an all-zero group), with pow2_scale != 0 rounded up to a power of
+ *   two; y_fp8 = E4M3(y / y_scale), nearest even, saturating at +-448.
+ *  x        [T, D] of `type`, rows ldx elements apart; residual, residual_out [T, D] of
+ *           `type`, rows ldr apart, both nullable (residual_out receives r; it may be
+ *           residual itself, or x where ldr == ldx).
+ *  gamma    [D] fp32.  eps > 0.
+ *  y        [T, D] of `type`, nullable: y rounded to `type`; may be x where ldy == ldx.
+ *  y_fp8    [T, D] E4M3 codes with y_scale [T, ceil(D / 128)] fp32 (row-major), both or
+ *           neither NULL.  y and y_fp8 have rows ldy elements apart.  A ldy that is a
+ *           multiple of 16 makes the codes an operand of dsa_gemm_e4m3.
+ * At least one of residual_out, y and y_fp8 is given.  1 <= D <= 32768.  Any element-aligned
+ * pointers and strides >= D work; with D and the strides multiples of 8 and 16-byte aligned
+ * pointers the rows move in 16-byte accesses.
+ * Arithmetic in fp32: the sum of squares over a fixed order, each product rounded on its own,
+ * the quotient by 448's group scale as a product with its reciprocal, so a code can differ
+ * from the exact quotient's only where that lies within a few fp32 ulps of a rounding
+ * boundary.  A row holding a NaN gives NaN codes; an infinity gives NaN at its place and
+ * zeros elsewhere in the row.
+ */
+dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
+                                float eps, int64_t T, int D, dsa_real type, void* residual_out, void* y,
+                                uint8_t* y_fp8, int64_t ldy, float* y_scale, int pow2_scale, void* stream);
+
+/*
+ * dsa_gemm_e4m3 -- product of E4M3 rows with E4M3 weights under block scales:
+ *   out[m, n] = sum_k a[m,k] a_scale[m, k / 128] * w[n,k] w_scale[n / 128, k / 128].
+ *  a        [M, K] E4M3 codes, rows lda bytes apart; a_scale [M, ceil(K / 128)] fp32 (the
+ *           pair dsa_add_rmsnorm_e4m3 writes).
+ *  w        [N, K] E4M3 codes, rows ldw bytes apart; w_scale [ceil(N / 128), ceil(K / 128)]
+ *           fp32.  Scales are row-major and may be any fp32 values.
+ *  out      [M, N] of `out_type`, rows ldo elements apart.
+ * a and w are 16-byte aligned, lda and ldw multiples of 16 and at least K; K >= 1 (what lies
+ * past K in a row is not read), M and N any.  out may not overlap an input.
+ * Arithmetic: exact products summed in fp32 by the tensor cores within a block of 128, the
+ * block's sum times its two scales (their product rounded to fp32) added in fp32 in the order
+ * of K; with few tiles K is cut into up to 8 parts whose sums are added in order.  One
+ * rounding to bf16 at the end.  The result depends on the device's SM count but not on
+ * timing.  No workspace.  A device-side wait that expires sets DSA_DEVERR_TIMEOUT.
+ */
+dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* w, int64_t ldw,
+                         const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, dsa_real out_type,
+                         void* stream);
 
 /*
  * dsa_indexer_logits_topk_noalloc -- dsa_indexer_logits_topk for callers that cannot
