@@ -16,6 +16,7 @@
 #include <cudaTypedefs.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -39,6 +40,7 @@ struct GemmArgs {
   int out_f32;
   int split;                                 // CTAs per tile (the cluster)
   int stages;
+  int out_vec;                               // out and its rows are 16-byte aligned
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -296,6 +298,344 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
   cluster_sync();
 }
 
+// ------------------------------------------------------------------ many tokens
+// A pair of CTAs (one cluster, cta_group::2) owns a tile of 256 tokens x 256 weight rows: each
+// CTA holds 128 of the tokens and 128 of the weight rows in shared memory (32 KB per block of
+// K), the pair's tensor cores read both, and each CTA's TMEM receives its 128 tokens x 256
+// columns.  Tokens are the MMA's M here, so an epilogue thread owns one token: one activation
+// scale per block.  Two accumulators of 256 columns fill TMEM: the epilogue adds block kb to its
+// registers while block kb + 1 runs.  Warps: producer, MMA issue (the even CTA; the odd CTA's
+// forwards "my copies have landed" to the even one), eight epilogue warps (128 columns each).
+// The pairs walk the tiles in groups of 8 token tiles, so that the tiles in flight share rows.
+constexpr int kPairThreads = 320;
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairStage = 32768u;      // 128 tokens and 128 weight rows of 128 bytes
+constexpr uint32_t kPairStaging = 8u * 4096u;   // a 32 x 128-byte block per epilogue warp
+constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + kPairStaging + 64 * 8;
+
+__device__ __forceinline__ void arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// mbar_wait for a barrier that threads of another CTA of the cluster arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned long long limit_ns,
+                                                  const volatile int* abort) {
+  unsigned long long t0 = 0;
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (abort != nullptr && *abort) return false;
+    const unsigned long long t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    else if (t - t0 > limit_ns) return false;
+  }
+}
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}" ::"r"(
+          tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Arrives on the barrier at this offset in both CTAs once every product issued so far is done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  lo = __uint_as_float(a);
+  hi = __uint_as_float(b);
+}
+// Two independent fp32 fused multiply-adds.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const __grid_constant__ CUtensorMap tma,
+                                                                         const __grid_constant__ CUtensorMap tmw,
+                                                                         const GemmArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t bars = smem_u32(sm + kPairStages * kPairStage + kPairStaging);
+  int* flags = reinterpret_cast<int*>(sm + kPairStages * kPairStage + kPairStaging + 60 * 8);
+  volatile int* abort_flag = flags;                          // [0] abort, [1] TMEM base
+  auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
+  auto pfull = [&](int s) { return bars + 8u * (uint32_t)(8 + s); };   // the odd CTA's stage (even CTA only)
+  auto empty = [&](int s) { return bars + 8u * (uint32_t)(16 + s); };
+  auto afull = [&](int b) { return bars + 8u * (uint32_t)(24 + b); };
+  auto aempty = [&](int b) { return bars + 8u * (uint32_t)(26 + b); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x & 1u;                     // = the CTA's rank in its cluster
+  const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
+  const int mt = (int)((g.M + 255) / 256), nt = (g.N + 255) / 256;
+  const int64_t tiles = (int64_t)mt * nt;
+  const int G = g.G;
+  const unsigned long long limit = wait_limit_ns();
+
+  // token tile and weight tile of tile t: groups of 8 token tiles, tokens fastest
+  auto locate = [&](int64_t t, int64_t& m0, int& n0) {
+    const int64_t per = 8 * (int64_t)nt;
+    const int grp = (int)(t / per);
+    const int h = min(8, mt - 8 * grp);
+    const int r = (int)(t - grp * per);
+    m0 = ((int64_t)8 * grp + r % h) * 256;
+    n0 = r / h * 256;
+  };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(pfull(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(afull(b), 1);
+      mbar_init(aempty(b), 16);
+    }
+    flags[0] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    tma_prefetch_desc(&tma);
+    tma_prefetch_desc(&tmw);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 1)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)flags[1];
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    // ================================ producer ================================
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 1;
+      int64_t issued = 0;
+      bool ok = true;
+      for (int64_t t = pair; ok && t < tiles; t += npairs) {
+        int64_t m0;
+        int n0;
+        locate(t, m0, n0);
+        for (int kb = 0; kb < G; ++kb) {
+          if (!(ok = mbar_wait(empty(s), ph, limit, abort_flag))) break;
+          const uint32_t dst = smem_u32(sm) + (uint32_t)s * kPairStage;
+          mbar_arrive_expect_tx(full(s), kPairStage);
+          tma_load_2d(dst, &tma, full(s), kb * kBlk, (int)m0 + 128 * (int)rank);
+          tma_load_2d(dst + 16384u, &tmw, full(s), kb * kBlk, n0 + 128 * (int)rank);
+          ++issued;
+          if (++s == kPairStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        raise_error(DSA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // before the CTA may leave: every copy has landed, and (unless the call was abandoned)
+      // the products' last signals to this CTA's stages have arrived
+      for (int64_t k = issued > kPairStages ? issued - kPairStages : 0; k < issued; ++k) {
+        const int st = (int)(k % kPairStages);
+        const uint32_t par = (uint32_t)(k / kPairStages) & 1u;
+        mbar_wait(full(st), par, kCleanupWaitNs, nullptr);
+        if (ok) ok = mbar_wait(empty(st), par, limit, abort_flag);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 1) {
+      // ===================== the odd CTA: its stages' copies have landed =====================
+      int s = 0;
+      uint32_t ph = 0;
+      const int64_t n = pair < tiles ? ((tiles - pair + npairs - 1) / npairs) * G : 0;
+      for (int64_t k = 0; k < n; ++k) {
+        if (!mbar_wait(full(s), ph, limit, abort_flag)) {
+          raise_error(DSA_DEVERR_TIMEOUT);
+          *abort_flag = 1;
+          break;
+        }
+        arrive_cluster(map_peer(pfull(s), 0u));
+        if (++s == kPairStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    } else if (lane == 0) {
+      // ================================ MMA issue ================================
+      constexpr uint32_t kIdesc = idesc_e4m3(256, 256);
+      int s = 0, b = 0;
+      uint32_t ph = 0, aph = 1;
+      const int64_t n = pair < tiles ? ((tiles - pair + npairs - 1) / npairs) * G : 0;
+      int64_t k = 0;
+      for (; k < n; ++k) {
+        if (!(mbar_wait_cluster(aempty(b), aph, limit, abort_flag) && mbar_wait(full(s), ph, limit, abort_flag) &&
+              mbar_wait_cluster(pfull(s), ph, limit, abort_flag)))
+          break;
+        tc_fence_after();
+        const uint32_t aa = smem_u32(sm) + (uint32_t)s * kPairStage;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_e4m3_pair(tmem + 256u * (uint32_t)b, smem_desc_sw128(aa + 32u * kk), smem_desc_sw128(aa + 16384u + 32u * kk),
+                        kIdesc, kk > 0 ? 1u : 0u);
+        mma_commit_pair(empty(s));
+        mma_commit_pair(afull(b));
+        if (++s == kPairStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+        if ((b ^= 1) == 0) aph ^= 1u;
+      }
+      if (k < n) {
+        raise_error(DSA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      // the last product has completed before either CTA frees TMEM or leaves
+      if (k > 0) mbar_wait(afull((int)((k - 1) & 1)), (uint32_t)((k - 1) >> 1) & 1u, kCleanupWaitNs, nullptr);
+    }
+    __syncwarp();
+  } else {
+    // ================================ epilogue ================================
+    const int half = (warp - 2) >> 2;                        // columns 128 half .. 128 half + 127
+    const int quarter = warp & 3;                            // TMEM lanes 32 quarter ..
+    const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16) + 128u * (uint32_t)half;
+    uint8_t* stage = sm + kPairStages * kPairStage + (uint32_t)(warp - 2) * 4096u;
+    const uint32_t aempty0 = map_peer(aempty(0), 0u);
+    bool ok = true;
+    int b = 0;
+    uint32_t ph = 0;
+    for (int64_t t = pair; ok && t < tiles; t += npairs) {
+      int64_t m0;
+      int n0;
+      locate(t, m0, n0);
+      m0 += 128 * (int64_t)rank + 32 * quarter;              // the warp's first token
+      n0 += 128 * half;                                      // and first column
+      const int64_t mrow = m0 + lane < g.M ? m0 + lane : g.M - 1;
+      const int nblk = n0 < g.N ? n0 / kBlk : (g.N - 1) / kBlk;
+      const float* as = g.a_scale + mrow * G;
+      const float* ws = g.w_scale + (int64_t)nblk * G;
+      uint64_t acc[64];
+#pragma unroll
+      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      float f = __ldg(as) * __ldg(ws);
+      for (int kb = 0; kb < G; ++kb) {
+        const int kn = kb + 1 < G ? kb + 1 : kb;
+        const float an = __ldg(as + kn), wn = __ldg(ws + kn);
+        ok = mbar_wait(afull(b), ph, limit, abort_flag);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
+        tc_fence_after();
+        const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t d[16];
+          tmem_ld16(tl + 256u * (uint32_t)b + 16u * c, d);
+          tmem_ld16_wait(d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[8 * c + e] = fma2(pack2(d[2 * e], d[2 * e + 1]), f2, acc[8 * c + e]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(aempty0 + 8u * (uint32_t)b);
+        if ((b ^= 1) == 0) ph ^= 1u;
+        f = an * wn;
+      }
+      if (!ok) break;
+      // rows of the warp's 32 tokens, 128 bytes of each at a time through its staging block:
+      // a thread writes its own row's pieces, then 8 lanes write one row's 128 bytes
+      const int rows = g.M - m0 < 32 ? (int)(g.M - m0) : 32;
+      auto put = [&](auto* out, int col0, const uint4 (&v)[8]) {
+        using E = typename std::remove_pointer<decltype(out)>::type;
+        constexpr int kPer = 16 / (int)sizeof(E);
+#pragma unroll
+        for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = v[p];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), p = lane & 7;
+          const int col = col0 + kPer * p;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
+          if (r < rows && col < g.N) {
+            E* o = out + (m0 + r) * g.ldo + col;
+            if (g.out_vec && col + kPer <= g.N) {
+              *reinterpret_cast<uint4*>(o) = w;
+            } else {
+              const E* we = reinterpret_cast<const E*>(&w);
+#pragma unroll
+              for (int e = 0; e < kPer; ++e)
+                if (col + e < g.N) o[e] = we[e];
+            }
+          }
+        }
+        __syncwarp();
+      };
+      if (g.out_f32) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 v[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p)
+            v[p] = make_uint4((uint32_t)acc[16 * q + 2 * p], (uint32_t)(acc[16 * q + 2 * p] >> 32),
+                              (uint32_t)acc[16 * q + 2 * p + 1], (uint32_t)(acc[16 * q + 2 * p + 1] >> 32));
+          put(static_cast<float*>(g.out), n0 + 32 * q, v);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint4 v[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float lo, hi;
+              unpack2(acc[32 * q + 4 * p + e], lo, hi);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+              w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            v[p] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          put(static_cast<uint16_t*>(g.out), n0 + 64 * q, v);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      raise_error(DSA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  // both CTAs are done with each other's barriers, shared memory and TMEM
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
 // ------------------------------------------------------------------ host side
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -361,15 +701,45 @@ cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, in
   return cudaLaunchKernelEx(&cfg, gemm_e4m3_kernel<BT>, tma, tmw, g);
 }
 
+cudaError_t launch_pair(const void* a, int64_t lda, const void* w, int64_t ldw, int64_t K, const GemmArgs& g,
+                        int num_sms, cudaStream_t stream) {
+  CUtensorMap tma, tmw;
+  if (!make_map(&tma, a, K, g.M, lda, 128) || !make_map(&tmw, w, K, g.N, ldw, 128)) return cudaErrorInvalidValue;
+  const cudaError_t e =
+      cudaFuncSetAttribute(gemm_e4m3_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((g.M + 255) / 256) * (int64_t)((g.N + 255) / 256);
+  const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * pairs));
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gemm_e4m3_pair_kernel, tma, tmw, g);
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* w, int64_t ldw,
                              const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, bool out_f32,
                              int num_sms, cudaStream_t stream) {
   if (M <= 0 || N <= 0) return cudaSuccess;
-  GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 1, 2};
+  GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 1, 2, 0};
+  const int64_t es = out_f32 ? 4 : 2;
+  g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
   cudaError_t e;
-  if (M <= 16) e = launch_bt<16>(a, lda, w, ldw, K, g, num_sms, stream);
+  const int64_t pair_tiles = ((M + 255) / 256) * (int64_t)((N + 255) / 256);
+  if (pair_tiles * 4 >= num_sms) e = launch_pair(a, lda, w, ldw, K, g, num_sms, stream);
+  else if (M <= 16) e = launch_bt<16>(a, lda, w, ldw, K, g, num_sms, stream);
   else if (M <= 32) e = launch_bt<32>(a, lda, w, ldw, K, g, num_sms, stream);
   else if (M <= 64) e = launch_bt<64>(a, lda, w, ldw, K, g, num_sms, stream);
   else e = launch_bt<128>(a, lda, w, ldw, K, g, num_sms, stream);

@@ -111,10 +111,28 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_raw_stream = None
+
+
+def _current_stream():
+    """torch's current stream on the current device, as a cudaStream_t integer (read without
+    building a torch.cuda.Stream, which costs more than a small kernel's launch)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            device = torch.cuda.current_device
+            _raw_stream = lambda: raw(device())  # noqa: E731
+    return _raw_stream()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
