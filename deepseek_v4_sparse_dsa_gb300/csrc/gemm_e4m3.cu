@@ -307,34 +307,18 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
 // registers while block kb + 1 runs.  Warps: producer, MMA issue (the even CTA; the odd CTA's
 // forwards "my copies have landed" to the even one), eight epilogue warps (128 columns each).
 // The pairs walk the tiles in groups of 8 token tiles, so that the tiles in flight share rows.
-constexpr int kPairThreads = 320;
+constexpr int kPairThreads = 384;             // warps 0..3: producer, MMA issue, two idle; 4..11: epilogue
 constexpr int kPairStages = 6;
 constexpr uint32_t kPairStage = 32768u;      // 128 tokens and 128 weight rows of 128 bytes
 constexpr uint32_t kPairStaging = 8u * 4096u;   // a 32 x 128-byte block per epilogue warp
 constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + kPairStaging + 64 * 8;
 
+// Arrives on a barrier of a CTA of the cluster, without the cluster-wide release that makes a thread wait
+// for all its memory operations (it took 8192 x 8192 x 4096 from 256 to 508 us).  What it announces is no
+// generic write: TMEM reads whose values are in registers, or copies that the thread's own barrier has
+// seen land in its CTA's shared memory, which that CTA's tensor core reads.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-// mbar_wait for a barrier that threads of another CTA of the cluster arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned long long limit_ns,
-                                                  const volatile int* abort) {
-  unsigned long long t0 = 0;
-  for (;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (abort != nullptr && *abort) return false;
-    const unsigned long long t = globaltimer_ns();
-    if (t0 == 0) t0 = t;
-    else if (t - t0 > limit_ns) return false;
-  }
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 __device__ __forceinline__ void mma_e4m3_pair(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -371,6 +355,31 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return d;
 }
 
+// 32 consecutive 32-bit columns of the thread's own TMEM lane: issue, then completion of every load
+// the thread has issued (the registers count as written only there).
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+        "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+        "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+        "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
 __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const __grid_constant__ CUtensorMap tma,
                                                                          const __grid_constant__ CUtensorMap tmw,
                                                                          const GemmArgs g) {
@@ -389,17 +398,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   const uint32_t rank = blockIdx.x & 1u;                     // = the CTA's rank in its cluster
   const int pair = (int)(blockIdx.x >> 1), npairs = (int)(gridDim.x >> 1);
   const int mt = (int)((g.M + 255) / 256), nt = (g.N + 255) / 256;
-  const int64_t tiles = (int64_t)mt * nt;
+  const int tiles = mt * nt;
   const int G = g.G;
   const unsigned long long limit = wait_limit_ns();
 
   // token tile and weight tile of tile t: groups of 8 token tiles, tokens fastest
-  auto locate = [&](int64_t t, int64_t& m0, int& n0) {
-    const int64_t per = 8 * (int64_t)nt;
-    const int grp = (int)(t / per);
+  auto locate = [&](int t, int& m0, int& n0) {
+    const int per = 8 * nt;
+    const int grp = t / per;
     const int h = min(8, mt - 8 * grp);
-    const int r = (int)(t - grp * per);
-    m0 = ((int64_t)8 * grp + r % h) * 256;
+    const int r = t - grp * per;
+    m0 = (8 * grp + r % h) * 256;
     n0 = r / h * 256;
   };
 
@@ -430,6 +439,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   const uint32_t tmem = (uint32_t)flags[1];
   grid_dependency_wait();
 
+  // The epilogue's 128 sums, 64 columns in flight and their scales need more than the 168 registers
+  // that 12 warps leave each thread: the first four warps hand theirs over
+  // (128 x 56 + 256 x 224 = 384 x 168).
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   if (warp == 0) {
     // ================================ producer ================================
     if (lane == 0) {
@@ -437,15 +450,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
       uint32_t ph = 1;
       int64_t issued = 0;
       bool ok = true;
-      for (int64_t t = pair; ok && t < tiles; t += npairs) {
-        int64_t m0;
-        int n0;
+      for (int t = pair; ok && t < tiles; t += npairs) {
+        int m0, n0;
         locate(t, m0, n0);
         for (int kb = 0; kb < G; ++kb) {
           if (!(ok = mbar_wait(empty(s), ph, limit, abort_flag))) break;
           const uint32_t dst = smem_u32(sm) + (uint32_t)s * kPairStage;
           mbar_arrive_expect_tx(full(s), kPairStage);
-          tma_load_2d(dst, &tma, full(s), kb * kBlk, (int)m0 + 128 * (int)rank);
+          tma_load_2d(dst, &tma, full(s), kb * kBlk, m0 + 128 * (int)rank);
           tma_load_2d(dst + 16384u, &tmw, full(s), kb * kBlk, n0 + 128 * (int)rank);
           ++issued;
           if (++s == kPairStages) {
@@ -494,8 +506,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
       const int64_t n = pair < tiles ? ((tiles - pair + npairs - 1) / npairs) * G : 0;
       int64_t k = 0;
       for (; k < n; ++k) {
-        if (!(mbar_wait_cluster(aempty(b), aph, limit, abort_flag) && mbar_wait(full(s), ph, limit, abort_flag) &&
-              mbar_wait_cluster(pfull(s), ph, limit, abort_flag)))
+        if (!(mbar_wait(aempty(b), aph, limit, abort_flag) && mbar_wait(full(s), ph, limit, abort_flag) &&
+              mbar_wait(pfull(s), ph, limit, abort_flag)))
           break;
         tc_fence_after();
         const uint32_t aa = smem_u32(sm) + (uint32_t)s * kPairStage;
@@ -519,50 +531,59 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
       if (k > 0) mbar_wait(afull((int)((k - 1) & 1)), (uint32_t)((k - 1) >> 1) & 1u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();
-  } else {
+  } else if (warp >= 4) {
     // ================================ epilogue ================================
-    const int half = (warp - 2) >> 2;                        // columns 128 half .. 128 half + 127
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    const int half = (warp - 4) >> 2;                        // columns 128 half .. 128 half + 127
     const int quarter = warp & 3;                            // TMEM lanes 32 quarter ..
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16) + 128u * (uint32_t)half;
-    uint8_t* stage = sm + kPairStages * kPairStage + (uint32_t)(warp - 2) * 4096u;
+    uint8_t* stage = sm + kPairStages * kPairStage + (uint32_t)(warp - 4) * 4096u;
     const uint32_t aempty0 = map_peer(aempty(0), 0u);
     bool ok = true;
     int b = 0;
     uint32_t ph = 0;
-    for (int64_t t = pair; ok && t < tiles; t += npairs) {
-      int64_t m0;
-      int n0;
+    for (int t = pair; ok && t < tiles; t += npairs) {
+      int m0, n0;
       locate(t, m0, n0);
-      m0 += 128 * (int64_t)rank + 32 * quarter;              // the warp's first token
+      m0 += 128 * (int)rank + 32 * quarter;                  // the warp's first token
       n0 += 128 * half;                                      // and first column
-      const int64_t mrow = m0 + lane < g.M ? m0 + lane : g.M - 1;
+      const int64_t mrow = min((int64_t)m0 + lane, g.M - 1);
       const int nblk = n0 < g.N ? n0 / kBlk : (g.N - 1) / kBlk;
       const float* as = g.a_scale + mrow * G;
       const float* ws = g.w_scale + (int64_t)nblk * G;
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0ull;
-      float f = __ldg(as) * __ldg(ws);
+      // scales of block kb, and of the two after it in flight
+      float a0 = __ldg(as), w0 = __ldg(ws), a1 = __ldg(as + min(1, G - 1)), w1 = __ldg(ws + min(1, G - 1));
       for (int kb = 0; kb < G; ++kb) {
-        const int kn = kb + 1 < G ? kb + 1 : kb;
-        const float an = __ldg(as + kn), wn = __ldg(ws + kn);
+        const float f = a0 * w0;
+        const int kn = min(kb + 2, G - 1);
+        a0 = a1, w0 = w1;
+        a1 = __ldg(as + kn);
+        w1 = __ldg(ws + kn);
         ok = mbar_wait(afull(b), ph, limit, abort_flag);
         if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
         tc_fence_after();
         const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
+        const uint32_t ta = tl + 256u * (uint32_t)b;
+        uint32_t d[2][32];                                   // a load of 32 columns runs behind the sums of the last
+        tmem_ld32_issue(ta, d[0]);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t d[16];
-          tmem_ld16(tl + 256u * (uint32_t)b + 16u * c, d);
-          tmem_ld16_wait(d);
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld32_wait(d[c & 1]);
+          if (c < 3) {
+            tmem_ld32_issue(ta + 32u * (c + 1), d[(c + 1) & 1]);
+          } else {                                           // all columns read: the accumulator is free
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(aempty0 + 8u * (uint32_t)b);
+          }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) acc[8 * c + e] = fma2(pack2(d[2 * e], d[2 * e + 1]), f2, acc[8 * c + e]);
+          for (int e = 0; e < 16; ++e)
+            acc[16 * c + e] = fma2(pack2(d[c & 1][2 * e], d[c & 1][2 * e + 1]), f2, acc[16 * c + e]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(aempty0 + 8u * (uint32_t)b);
         if ((b ^= 1) == 0) ph ^= 1u;
-        f = an * wn;
       }
       if (!ok) break;
       // rows of the warp's 32 tokens, 128 bytes of each at a time through its staging block:
@@ -580,7 +601,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
           const int col = col0 + kPer * p;
           const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
           if (r < rows && col < g.N) {
-            E* o = out + (m0 + r) * g.ldo + col;
+            E* o = out + (int64_t)(m0 + r) * g.ldo + col;
             if (g.out_vec && col + kPer <= g.N) {
               *reinterpret_cast<uint4*>(o) = w;
             } else {
