@@ -337,24 +337,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       : "memory");
 }
 
-__device__ __forceinline__ uint64_t pack2(uint32_t lo, uint32_t hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-// Two independent fp32 fused multiply-adds.
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
 // 32 consecutive 32-bit columns of the thread's own TMEM lane: issue, then completion of every load
 // the thread has issued (the registers count as written only there).
 __device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
@@ -551,9 +533,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
       const int nblk = n0 < g.N ? n0 / kBlk : (g.N - 1) / kBlk;
       const float* as = g.a_scale + mrow * G;
       const float* ws = g.w_scale + (int64_t)nblk * G;
-      uint64_t acc[64];
+      float acc[128];
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0ull;
+      for (int i = 0; i < 128; ++i) acc[i] = 0.f;
       // scales of block kb, and of the two after it in flight
       float a0 = __ldg(as), w0 = __ldg(ws), a1 = __ldg(as + min(1, G - 1)), w1 = __ldg(ws + min(1, G - 1));
       for (int kb = 0; kb < G; ++kb) {
@@ -565,7 +547,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
         ok = mbar_wait(afull(b), ph, limit, abort_flag);
         if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
         tc_fence_after();
-        const uint64_t f2 = pack2(__float_as_uint(f), __float_as_uint(f));
         const uint32_t ta = tl + 256u * (uint32_t)b;
         uint32_t d[2][32];                                   // a load of 32 columns runs behind the sums of the last
         tmem_ld32_issue(ta, d[0]);
@@ -580,8 +561,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
             if (lane == 0) arrive_cluster(aempty0 + 8u * (uint32_t)b);
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            acc[16 * c + e] = fma2(pack2(d[c & 1][2 * e], d[c & 1][2 * e + 1]), f2, acc[16 * c + e]);
+          for (int e = 0; e < 32; ++e) acc[32 * c + e] = fmaf(__uint_as_float(d[c & 1][e]), f, acc[32 * c + e]);
         }
         if ((b ^= 1) == 0) ph ^= 1u;
       }
@@ -620,8 +600,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
           uint4 v[8];
 #pragma unroll
           for (int p = 0; p < 8; ++p)
-            v[p] = make_uint4((uint32_t)acc[16 * q + 2 * p], (uint32_t)(acc[16 * q + 2 * p] >> 32),
-                              (uint32_t)acc[16 * q + 2 * p + 1], (uint32_t)(acc[16 * q + 2 * p + 1] >> 32));
+            v[p] = make_uint4(__float_as_uint(acc[32 * q + 4 * p]), __float_as_uint(acc[32 * q + 4 * p + 1]),
+                              __float_as_uint(acc[32 * q + 4 * p + 2]), __float_as_uint(acc[32 * q + 4 * p + 3]));
           put(static_cast<float*>(g.out), n0 + 32 * q, v);
         }
       } else {
@@ -633,9 +613,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float lo, hi;
-              unpack2(acc[32 * q + 4 * p + e], lo, hi);
-              const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(acc[64 * q + 8 * p + 2 * e], acc[64 * q + 8 * p + 2 * e + 1]);
               w[e] = *reinterpret_cast<const uint32_t*>(&h);
             }
             v[p] = make_uint4(w[0], w[1], w[2], w[3]);
