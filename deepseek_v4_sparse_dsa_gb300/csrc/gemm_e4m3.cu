@@ -304,11 +304,12 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
 // K), the pair's tensor cores read both, and each CTA's TMEM receives its 128 tokens x 256
 // columns.  Tokens are the MMA's M here, so an epilogue thread owns one token: one activation
 // scale per block.  Two accumulators of 256 columns fill TMEM: the epilogue adds block kb to its
-// registers while block kb + 1 runs.  Warps: producer, MMA issue (the even CTA; the odd CTA's
-// forwards "my copies have landed" to the even one), eight epilogue warps (128 columns each).
+// registers while block kb + 1 runs.  Warps: producer, two MMA
+// issuers (the even CTA's), one that tells the even CTA that this CTA's copies have landed, eight
+// epilogue warps (128 columns each).
 // The pairs walk the tiles in groups of 8 token tiles, so that the tiles in flight share rows.
-constexpr int kPairThreads = 384;             // warps 0..3: producer, MMA issue, two idle; 4..11: epilogue
-constexpr int kPairStages = 6;
+constexpr int kPairThreads = 384;             // warps 0..3: producer, two MMA issuers, forwarder; 4..11: epilogue
+constexpr int kPairStages = 6;               // even: block k and its accumulator k % 2 keep to stages of one parity
 constexpr uint32_t kPairStage = 32768u;      // 128 tokens and 128 weight rows of 128 bytes
 constexpr uint32_t kPairStaging = 8u * 4096u;   // a 32 x 128-byte block per epilogue warp
 constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + kPairStaging + 64 * 8;
@@ -371,7 +372,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   int* flags = reinterpret_cast<int*>(sm + kPairStages * kPairStage + kPairStaging + 60 * 8);
   volatile int* abort_flag = flags;                          // [0] abort, [1] TMEM base
   auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
-  auto pfull = [&](int s) { return bars + 8u * (uint32_t)(8 + s); };   // the odd CTA's stage (even CTA only)
+  auto ready = [&](int s) { return bars + 8u * (uint32_t)(8 + s); };   // even CTA: both CTAs' copies have landed
   auto empty = [&](int s) { return bars + 8u * (uint32_t)(16 + s); };
   auto afull = [&](int b) { return bars + 8u * (uint32_t)(24 + b); };
   auto aempty = [&](int b) { return bars + 8u * (uint32_t)(26 + b); };
@@ -397,7 +398,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairStages; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(pfull(s), 1);
+      mbar_init(ready(s), 2);
       mbar_init(empty(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 1;
-      int64_t issued = 0;
+      int issued = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += npairs) {
         int m0, n0;
@@ -454,63 +455,64 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
       }
       // before the CTA may leave: every copy has landed, and (unless the call was abandoned)
       // the products' last signals to this CTA's stages have arrived
-      for (int64_t k = issued > kPairStages ? issued - kPairStages : 0; k < issued; ++k) {
-        const int st = (int)(k % kPairStages);
+      for (int k = issued > kPairStages ? issued - kPairStages : 0; k < issued; ++k) {
+        const int st = k % kPairStages;
         const uint32_t par = (uint32_t)(k / kPairStages) & 1u;
         mbar_wait(full(st), par, kCleanupWaitNs, nullptr);
         if (ok) ok = mbar_wait(empty(st), par, limit, abort_flag);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 1) {
-      // ===================== the odd CTA: its stages' copies have landed =====================
+  } else if (warp < 4) {
+    const int n = pair < tiles ? (tiles - pair + npairs - 1) / npairs * G : 0;   // the pair's blocks, over all its tiles
+    if (lane == 0 && warp == 3) {
+      // ================ tells the MMA issuers that this CTA's copies have landed ================
       int s = 0;
       uint32_t ph = 0;
-      const int64_t n = pair < tiles ? ((tiles - pair + npairs - 1) / npairs) * G : 0;
-      for (int64_t k = 0; k < n; ++k) {
+      for (int k = 0; k < n; ++k) {
         if (!mbar_wait(full(s), ph, limit, abort_flag)) {
           raise_error(DSA_DEVERR_TIMEOUT);
           *abort_flag = 1;
           break;
         }
-        arrive_cluster(map_peer(pfull(s), 0u));
+        arrive_cluster(map_peer(ready(s), 0u));
         if (++s == kPairStages) {
           s = 0;
           ph ^= 1u;
         }
       }
-    } else if (lane == 0) {
+    } else if (lane == 0 && rank == 0) {
       // ================================ MMA issue ================================
+      // Warp 1 issues the even blocks, warp 2 the odd ones, each into its own accumulator: a thread
+      // is held while the tensor core takes its products, and its waits and signals for the next
+      // block run behind the other's products.
       constexpr uint32_t kIdesc = idesc_e4m3(256, 256);
-      int s = 0, b = 0;
+      const int b = warp - 1;
+      const uint32_t acc = tmem + 256u * (uint32_t)b;
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(sm));
+      int s = b, k = b;
       uint32_t ph = 0, aph = 1;
-      const int64_t n = pair < tiles ? ((tiles - pair + npairs - 1) / npairs) * G : 0;
-      int64_t k = 0;
-      for (; k < n; ++k) {
-        if (!(mbar_wait(aempty(b), aph, limit, abort_flag) && mbar_wait(full(s), ph, limit, abort_flag) &&
-              mbar_wait(pfull(s), ph, limit, abort_flag)))
-          break;
+      for (; k < n; k += 2) {
+        if (!(mbar_wait(ready(s), ph, limit, abort_flag) && mbar_wait(aempty(b), aph, limit, abort_flag))) break;
         tc_fence_after();
-        const uint32_t aa = smem_u32(sm) + (uint32_t)s * kPairStage;
+        const uint64_t da = desc0 + (uint64_t)(s * (int)(kPairStage >> 4));
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_e4m3_pair(tmem + 256u * (uint32_t)b, smem_desc_sw128(aa + 32u * kk), smem_desc_sw128(aa + 16384u + 32u * kk),
-                        kIdesc, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 4; ++kk)                       // 32 bytes of K along the rows; the weights 16 KB on
+          mma_e4m3_pair(acc, da + 2u * kk, da + 1024u + 2u * kk, kIdesc, kk > 0 ? 1u : 0u);
         mma_commit_pair(empty(s));
         mma_commit_pair(afull(b));
-        if (++s == kPairStages) {
-          s = 0;
+        aph ^= 1u;
+        if ((s += 2) >= kPairStages) {
+          s -= kPairStages;
           ph ^= 1u;
         }
-        if ((b ^= 1) == 0) aph ^= 1u;
       }
       if (k < n) {
         raise_error(DSA_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
       // the last product has completed before either CTA frees TMEM or leaves
-      if (k > 0) mbar_wait(afull((int)((k - 1) & 1)), (uint32_t)((k - 1) >> 1) & 1u, kCleanupWaitNs, nullptr);
+      if (k > b) mbar_wait(afull(b), (uint32_t)((k - 2) >> 1) & 1u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -548,20 +550,18 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
         if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
         tc_fence_after();
         const uint32_t ta = tl + 256u * (uint32_t)b;
-        uint32_t d[2][32];                                   // a load of 32 columns runs behind the sums of the last
-        tmem_ld32_issue(ta, d[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld32_wait(d[c & 1]);
-          if (c < 3) {
-            tmem_ld32_issue(ta + 32u * (c + 1), d[(c + 1) & 1]);
-          } else {                                           // all columns read: the accumulator is free
+        for (int c = 0; c < 2; ++c) {
+          uint32_t d[64];
+          tmem_ld64_issue(ta + 64u * c, d);
+          tmem_ld64_wait(d);
+          if (c == 1) {                                      // all columns read: the accumulator is free
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(aempty0 + 8u * (uint32_t)b);
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) acc[32 * c + e] = fmaf(__uint_as_float(d[c & 1][e]), f, acc[32 * c + e]);
+          for (int e = 0; e < 64; ++e) acc[64 * c + e] = fmaf(__uint_as_float(d[e]), f, acc[64 * c + e]);
         }
         if ((b ^= 1) == 0) ph ^= 1u;
       }
