@@ -25,9 +25,10 @@ namespace dsa {
 namespace {
 
 constexpr int kBlk = 128;                    // K per block, weight rows per tile
-constexpr int kGemmThreads = 192;            // producer warp, MMA warp, four epilogue warps
 constexpr int kScaleChunk = 16;              // K blocks whose scales are staged at a time
 constexpr int kMaxStages = 12;
+constexpr size_t kSmemOne = 232448;          // dynamic shared memory of the one CTA of an SM
+constexpr size_t kSmemTwo = 115712;          // of each of two (228 KB per SM, 1 KB reserved per CTA)
 
 struct GemmArgs {
   const float* a_scale;                      // [M, G]
@@ -53,13 +54,16 @@ __device__ __forceinline__ uint32_t map_peer(uint32_t addr, uint32_t rank) {
   return a;
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-// NC consecutive 32-bit columns of the thread's own TMEM lane (completed by tcgen05.wait::ld).
+// 16 consecutive 32-bit columns of the thread's own TMEM lane (completed by the wait).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -77,35 +81,86 @@ __device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
                : "memory");
 }
 
-__device__ __forceinline__ void store_out(const GemmArgs& g, int64_t m, int n, float v) {
-  if (g.out_f32) static_cast<float*>(g.out)[m * g.ldo + n] = v;
-  else static_cast<__nv_bfloat16*>(g.out)[m * g.ldo + n] = __float2bfloat16_rn(v);
+// 32 consecutive 32-bit columns of the thread's own TMEM lane: issue, then completion of every load
+// the thread has issued (the registers count as written only there).
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+        "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+        "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+        "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
 }
 
-// Shared memory, from a 1024-byte aligned base: the stages (weights 16 KB, tokens BT * 128
-// bytes each), the staged scales [kScaleChunk][BT], the barriers and flags.  The partial sums
-// [BT][128] of a split tile reuse the stages once every product has completed.
-template <int BT>
-__host__ __device__ constexpr uint32_t stage_bytes() { return 16384u + (uint32_t)BT * 128u; }
-
-template <int BT>
-size_t gemm_smem(int stages) {
-  return 1024 + (size_t)stages * stage_bytes<BT>() + kScaleChunk * BT * 4 + (2 * kMaxStages + 8) * 8 + 16;
+// Four consecutive outputs of row m from column n.
+__device__ __forceinline__ void store_out4(const GemmArgs& g, int64_t m, int n, float4 v) {
+  const int64_t at = m * g.ldo + n;
+  if (g.out_vec && n + 4 <= g.N) {
+    if (g.out_f32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(g.out) + at) = v;
+    } else {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    }
+    return;
+  }
+  const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (n + i >= g.N) break;
+    if (g.out_f32) static_cast<float*>(g.out)[at + i] = e[i];
+    else static_cast<__nv_bfloat16*>(g.out)[at + i] = __float2bfloat16_rn(e[i]);
+  }
 }
 
+// Shapes of the kernel with BT tokens per tile.  Four epilogue warps (one per TMEM lane quarter) take
+// up to 64 columns; 128 columns are shared by eight.
 template <int BT>
-__global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tma,
-                                                                 const __grid_constant__ CUtensorMap tmw,
-                                                                 const GemmArgs g) {
-  constexpr uint32_t kStage = stage_bytes<BT>();
-  constexpr int kBufs = BT <= 64 ? 4 : 2;                    // TMEM accumulators
-  constexpr uint32_t kCols = BT * kBufs < 32 ? 32 : BT * kBufs;
+struct FewShape {
+  static constexpr int kEpi = BT == 128 ? 256 : 128;         // epilogue threads
+  static constexpr int kThreads = 64 + kEpi;                 // + producer warp, MMA warp
+  static constexpr int kCols = BT == 128 ? 64 : BT;          // columns per epilogue warp
+  static constexpr int kBufs = BT <= 64 ? 4 : 2;             // TMEM accumulators
+  static constexpr uint32_t kTmem = BT * kBufs;              // 64, 128 or 256 columns
+  static constexpr uint32_t kStage = 16384u + (uint32_t)BT * 128u;   // weights, tokens
+  static constexpr uint32_t kScales = 2u * kScaleChunk * BT * 4u;    // two chunks of staged scales
+  static constexpr size_t smem(int stages) {
+    return 1024 + (size_t)stages * kStage + kScales + (2 * kMaxStages + 8) * 8 + 16;
+  }
+};
+
+// Shared memory, from a 1024-byte aligned base: the stages, the staged scales [2][kScaleChunk][BT],
+// the barriers and flags.  The finished sums [BT][128] reuse the stages once every product has
+// completed.
+template <int BT>
+__global__ void __launch_bounds__(FewShape<BT>::kThreads) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tma,
+                                                                           const __grid_constant__ CUtensorMap tmw,
+                                                                           const GemmArgs g) {
+  using Sh = FewShape<BT>;
+  constexpr uint32_t kStage = Sh::kStage;
+  constexpr int kBufs = Sh::kBufs, kEpi = Sh::kEpi, kCols = Sh::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int S = g.split, stages = g.stages;
   float* sc = reinterpret_cast<float*>(sm + (size_t)stages * kStage);
-  const uint32_t bars = smem_u32(sc + kScaleChunk * BT);
-  int* flags = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(sc + kScaleChunk * BT) + (2 * kMaxStages + 8) * 8);
+  uint8_t* ctl = sm + (size_t)stages * kStage + Sh::kScales;
+  const uint32_t bars = smem_u32(ctl);
+  int* flags = reinterpret_cast<int*>(ctl + (2 * kMaxStages + 8) * 8);
   volatile int* abort_flag = flags;                          // [0] abort, [1] TMEM base
   auto full = [&](int s) { return bars + 8u * (uint32_t)s; };
   auto empty = [&](int s) { return bars + 8u * (uint32_t)(kMaxStages + s); };
@@ -115,9 +170,9 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntiles = (g.N + kBlk - 1) / kBlk;
   const int rank = (int)(blockIdx.x % (unsigned)S);          // = the CTA's rank in its cluster
-  const int64_t tile = blockIdx.x / (unsigned)S;
-  const int nt = (int)(tile % ntiles);
-  const int64_t m0 = tile / ntiles * BT;
+  const int tile = (int)(blockIdx.x / (unsigned)S);
+  const int nt = tile % ntiles;
+  const int64_t m0 = (int64_t)(tile / ntiles) * BT;
   const int mv = g.M - m0 < BT ? (int)(g.M - m0) : BT;       // tokens of this tile
   const int kb0 = (int)((int64_t)g.G * rank / S);
   const int nkb = (int)((int64_t)g.G * (rank + 1) / S) - kb0;
@@ -130,23 +185,20 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(afull(b), 1);
-      mbar_init(aempty(b), 4);
+      mbar_init(aempty(b), kEpi / 32);
     }
     flags[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     tma_prefetch_desc(&tma);
     tma_prefetch_desc(&tmw);
   }
-  if (warp == 1) tmem_alloc(smem_u32(flags + 1), kCols);
+  if (warp == 1) tmem_alloc(smem_u32(flags + 1), Sh::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)flags[1];
+  grid_launch_dependents();                                  // TMEM is held: the next kernel's set-up may begin
   grid_dependency_wait();
-
-  float acc[BT];
-#pragma unroll
-  for (int i = 0; i < BT; ++i) acc[i] = 0.f;
 
   if (warp == 0) {
     // ================================ producer ================================
@@ -182,10 +234,9 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
       constexpr uint32_t kIdesc = idesc_e4m3(128, BT);
       int s = 0, b = 0;
       uint32_t ph = 0, aph = 1;
-      bool ok = true;
-      int last = -1;
-      for (int i = 0; i < nkb; ++i) {
-        if (!(ok = mbar_wait(aempty(b), aph, limit, abort_flag) && mbar_wait(full(s), ph, limit, abort_flag))) break;
+      int i = 0;
+      for (; i < nkb; ++i) {
+        if (!(mbar_wait(aempty(b), aph, limit, abort_flag) && mbar_wait(full(s), ph, limit, abort_flag))) break;
         tc_fence_after();
         const uint32_t wa = smem_u32(sm) + (uint32_t)s * kStage;
 #pragma unroll
@@ -194,7 +245,6 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
                    kIdesc, kk > 0 ? 1u : 0u);
         mma_commit(empty(s));
         mma_commit(afull(b));
-        last = i;
         if (++s == stages) {
           s = 0;
           ph ^= 1u;
@@ -204,54 +254,80 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
           aph ^= 1u;
         }
       }
-      if (!ok) {
+      if (i < nkb) {
         raise_error(DSA_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
       // the last product issued has completed before TMEM is freed or the stages are reused
-      if (last >= 0) mbar_wait(afull(last % kBufs), (uint32_t)(last / kBufs) & 1u, kCleanupWaitNs, nullptr);
+      if (i > 0) mbar_wait(afull((i - 1) % kBufs), (uint32_t)((i - 1) / kBufs) & 1u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();
-  } else {
+  }
+
+  const int gt = threadIdx.x - 64;                           // epilogue thread
+  const int nrow = 32 * (warp & 3) + lane;                   // its weight row in the tile
+  const int c0 = kCols * (gt >> 7);                          // and its first column (token)
+  float acc[kCols];
+  if (warp >= 2) {
     // ================================ epilogue ================================
-    const int gt = threadIdx.x - 64;
-    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    const float* wsc = g.w_scale + (int64_t)nt * g.G + kb0;
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c0;
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
+    // Scales of kScaleChunk blocks at a time, both factors multiplied: thread gt fetches block
+    // gt % kScaleChunk of every (kEpi / kScaleChunk)-th token (neighbouring addresses), one chunk
+    // ahead, and leaves them in the chunk's half of `sc`.
+    constexpr int kPer = BT * kScaleChunk / kEpi, kStep = kEpi / kScaleChunk;
+    const int sk = gt % kScaleChunk, sm0 = gt / kScaleChunk;
+    const float* as = g.a_scale + m0 * g.G + kb0;
+    const float* ws = g.w_scale + (int64_t)nt * g.G + kb0;
+    float pa[kPer], pw;
+    auto fetch = [&](int i0) {
+      pw = i0 + sk < nkb ? __ldg(ws + i0 + sk) : 0.f;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int m = sm0 + u * kStep;
+        pa[u] = (m < mv && i0 + sk < nkb) ? __ldg(as + (int64_t)m * g.G + i0 + sk) : 0.f;
+      }
+    };
+    fetch(0);
     bool ok = true;
     int b = 0;
     uint32_t ph = 0;
-    for (int i0 = 0; i0 < nkb; i0 += kScaleChunk) {
+    for (int i0 = 0, half = 0; i0 < nkb; i0 += kScaleChunk, half ^= 1) {
+      float* dst = sc + half * kScaleChunk * BT;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) dst[sk * BT + sm0 + u * kStep] = pa[u] * pw;
+      group_sync<kEpi>();                                    // the other half is free once all have passed here
+      if (i0 + kScaleChunk < nkb) fetch(i0 + kScaleChunk);
       const int nc = min(kScaleChunk, nkb - i0);
-      group_sync<128>();                                     // the chunk before has been used
-      for (int e = gt; e < BT * kScaleChunk; e += 128) {     // kb fastest: neighbouring addresses
-        const int m = e / kScaleChunk, k = e - m * kScaleChunk;
-        if (k < nc)
-          sc[k * BT + m] = m < mv ? __ldg(g.a_scale + (m0 + m) * g.G + kb0 + i0 + k) * __ldg(wsc + i0 + k) : 0.f;
-      }
-      group_sync<128>();
       for (int i = 0; i < nc; ++i) {
         if (ok) ok = mbar_wait(afull(b), ph, limit, abort_flag);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (ok) {
           tc_fence_after();
-          const float* f = sc + i * BT;
-#pragma unroll
-          for (int c = 0; c < BT; c += 16) {
-            uint32_t d[16];
-            tmem_ld16(tl + (uint32_t)(b * BT + c), d);
+          const float4* f = reinterpret_cast<const float4*>(dst + i * BT + c0);
+          uint32_t d[kCols];
+          if constexpr (kCols == 16) {
+            tmem_ld16(tl + (uint32_t)(b * BT), d);
             tmem_ld16_wait(d);
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 f4 = *reinterpret_cast<const float4*>(f + c + e);
-              acc[c + e] = fmaf(__uint_as_float(d[e]), f4.x, acc[c + e]);
-              acc[c + e + 1] = fmaf(__uint_as_float(d[e + 1]), f4.y, acc[c + e + 1]);
-              acc[c + e + 2] = fmaf(__uint_as_float(d[e + 2]), f4.z, acc[c + e + 2]);
-              acc[c + e + 3] = fmaf(__uint_as_float(d[e + 3]), f4.w, acc[c + e + 3]);
-            }
+          } else if constexpr (kCols == 32) {
+            tmem_ld32_issue(tl + (uint32_t)(b * BT), d);
+            tmem_ld32_wait(d);
+          } else {
+            tmem_ld64_issue(tl + (uint32_t)(b * BT), d);
+            tmem_ld64_wait(d);
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(aempty(b));
+#pragma unroll
+          for (int e = 0; e < kCols; e += 4) {
+            const float4 f4 = f[e / 4];
+            acc[e] = fmaf(__uint_as_float(d[e]), f4.x, acc[e]);
+            acc[e + 1] = fmaf(__uint_as_float(d[e + 1]), f4.y, acc[e + 1]);
+            acc[e + 2] = fmaf(__uint_as_float(d[e + 2]), f4.z, acc[e + 2]);
+            acc[e + 3] = fmaf(__uint_as_float(d[e + 3]), f4.w, acc[e + 3]);
+          }
         }
         if (++b == kBufs) {
           b = 0;
@@ -267,35 +343,53 @@ __global__ void __launch_bounds__(kGemmThreads) gemm_e4m3_kernel(const __grid_co
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem, kCols);
-  const int nrow = 32 * (warp & 3) + lane;                   // the epilogue thread's weight row in the tile
-  const int n = nt * kBlk + nrow;
-  if (S == 1) {
-    if (warp >= 2 && n < g.N) {
-#pragma unroll
-      for (int m = 0; m < BT; ++m)
-        if (m < mv) store_out(g, m0 + m, n, acc[m]);
-    }
-    return;
-  }
-  // Split tile: each CTA leaves its part [BT][128] in its own shared memory, CTA r adds up the
-  // tokens r, r + S, ... from all parts in rank order.  Every thread passes both cluster
-  // barriers once; the second keeps each CTA's memory alive until its peers have read it.
+  if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
+  // Each CTA leaves its sums [token][weight row] in its own shared memory; CTA r of the cluster adds
+  // up the tokens r, r + S, ... from all parts in rank order, four neighbouring outputs per thread.
+  // Every thread passes both cluster barriers once; the second keeps each CTA's memory alive until
+  // its peers have read it.
   float* part = reinterpret_cast<float*>(sm);
   if (warp >= 2) {
 #pragma unroll
-    for (int m = 0; m < BT; ++m)
-      if (m < mv) part[m * kBlk + nrow] = acc[m];
+    for (int e = 0; e < kCols; ++e)
+      if (c0 + e < mv) part[(c0 + e) * kBlk + nrow] = acc[e];
   }
-  cluster_sync();
+  if (S > 1) cluster_sync();
+  else __syncthreads();
+  const int n = nt * kBlk + 4 * lane;
   if (warp >= 2 && n < g.N) {
-    for (int m = rank; m < mv; m += S) {
-      float v = 0.f;
-      for (int r = 0; r < S; ++r) v += ld_cluster_f32(map_peer(smem_u32(part + m * kBlk + nrow), (uint32_t)r));
-      store_out(g, m0 + m, n, v);
+    constexpr int kRows = kEpi / 32, kFly = 8;               // rows of a step, and rows in flight per thread
+    const uint32_t base = smem_u32(part) + 16u * (uint32_t)lane;
+    for (int j = gt >> 5; rank + S * j < mv; j += kRows * kFly) {
+      float4 v[kFly];
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < S; ++r) {
+        const uint32_t from = S > 1 ? map_peer(base, (uint32_t)r) : base;
+        float4 t[kFly];
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+          const int m = rank + S * (j + u * kRows);
+          if (m < mv) t[u] = ld_cluster_f32x4(from + (uint32_t)m * (kBlk * 4u));
+        }
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+          if (rank + S * (j + u * kRows) < mv) {
+            v[u].x += t[u].x;
+            v[u].y += t[u].y;
+            v[u].z += t[u].z;
+            v[u].w += t[u].w;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        const int m = rank + S * (j + u * kRows);
+        if (m < mv) store_out4(g, m0 + m, n, v[u]);
+      }
     }
   }
-  cluster_sync();
+  if (S > 1) cluster_sync();
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -336,31 +430,6 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
-}
-
-// 32 consecutive 32-bit columns of the thread's own TMEM lane: issue, then completion of every load
-// the thread has issued (the registers count as written only there).
-__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-        "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-        "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-        "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
 }
 
 __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const __grid_constant__ CUtensorMap tma,
@@ -420,6 +489,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)flags[1];
+  grid_launch_dependents();                                  // TMEM is held: the next kernel's set-up may begin
   grid_dependency_wait();
 
   // The epilogue's 128 sums, 64 columns in flight and their scales need more than the 168 registers
@@ -669,23 +739,25 @@ cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, in
   CUtensorMap tma, tmw;
   if (!make_map(&tma, a, K, g.M, lda, BT) || !make_map(&tmw, w, K, g.N, ldw, kBlk)) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)((g.N + kBlk - 1) / kBlk) * ((g.M + BT - 1) / BT);
-  // split K over a cluster while the tiles leave SMs idle and each part keeps two blocks
+  // Split K over a cluster of S CTAs while the tiles leave CTA slots free (two per SM, which the
+  // shared memory below allows up to 64 tokens per tile) and each part keeps two blocks.
+  const int64_t slots = (int64_t)num_sms * (BT == 128 ? 1 : 2);
   int S = 1;
-  while (S < 8 && tiles * S * 2 <= num_sms && 4 * S <= g.G) S *= 2;
+  while (S < 8 && tiles * S * 2 <= slots && 4 * S <= g.G) S *= 2;
   g.split = S;
   const int nkb = (g.G + S - 1) / S;
-  int st = 8;
-  if (BT == 128) st = 6;
-  if (st > nkb) st = nkb < 2 ? 2 : nkb;
-  // the partial sums reuse the stages
-  while (S > 1 && (size_t)st * stage_bytes<BT>() < (size_t)BT * kBlk * 4) ++st;
+  // as many stages as shared memory holds, and no more than there are blocks; the sums reuse them
+  int st = 2;
+  const size_t room = BT == 128 ? kSmemOne : kSmemTwo;
+  while (st < kMaxStages && st < nkb && FewShape<BT>::smem(st + 1) <= room) ++st;
+  while ((size_t)st * FewShape<BT>::kStage < (size_t)BT * kBlk * 4) ++st;
   g.stages = st;
-  const size_t smem = gemm_smem<BT>(st);
+  const size_t smem = FewShape<BT>::smem(st);
   cudaError_t e = cudaFuncSetAttribute(gemm_e4m3_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * S));
-  cfg.blockDim = dim3(kGemmThreads);
+  cfg.blockDim = dim3(FewShape<BT>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
