@@ -39,7 +39,7 @@ struct GemmArgs {
   void* out;
   int64_t ldo;
   int out_f32;
-  int split;                                 // CTAs per tile (the cluster)
+  int split_log2;                            // log2 of the CTAs per tile (the cluster)
   int stages;
   int out_vec;                               // out and its rows are 16-byte aligned
 };
@@ -54,14 +54,14 @@ __device__ __forceinline__ uint32_t map_peer(uint32_t addr, uint32_t rank) {
   return a;
 }
 
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+
+// Half of a cluster barrier each: every thread arrives when it starts, and waits for the others'
+// arrivals before it touches a peer's shared memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // 16 consecutive 32-bit columns of the thread's own TMEM lane (completed by the wait).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -139,16 +139,16 @@ struct FewShape {
   static constexpr uint32_t kTmem = BT * kBufs;              // 64, 128 or 256 columns
   static constexpr uint32_t kStage = 16384u + (uint32_t)BT * 128u;   // weights, tokens
   static constexpr uint32_t kScales = 2u * kScaleChunk * BT * 4u;    // two chunks of staged scales
+  static constexpr uint32_t kIn = (uint32_t)BT * kBlk * 4u;  // sums of the CTA's tokens from every part
   static constexpr size_t smem(int stages) {
-    return 1024 + (size_t)stages * kStage + kScales + (2 * kMaxStages + 8) * 8 + 16;
+    return 1024 + (size_t)stages * kStage + kIn + kScales + (2 * kMaxStages + 8) * 8 + 16;
   }
 };
 
-// Shared memory, from a 1024-byte aligned base: the stages, the staged scales [2][kScaleChunk][BT],
-// the barriers and flags.  The finished sums [BT][128] reuse the stages once every product has
-// completed.
+// Shared memory, from a 1024-byte aligned base: the stages, the sums that the CTA adds up, the staged
+// scales [2][kScaleChunk][BT], the barriers and flags.
 template <int BT>
-__global__ void __launch_bounds__(FewShape<BT>::kThreads) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tma,
+__global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tma,
                                                                            const __grid_constant__ CUtensorMap tmw,
                                                                            const GemmArgs g) {
   using Sh = FewShape<BT>;
@@ -156,9 +156,11 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads) gemm_e4m3_kernel(const
   constexpr int kBufs = Sh::kBufs, kEpi = Sh::kEpi, kCols = Sh::kCols;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const int S = g.split, stages = g.stages;
-  float* sc = reinterpret_cast<float*>(sm + (size_t)stages * kStage);
-  uint8_t* ctl = sm + (size_t)stages * kStage + Sh::kScales;
+  const int lg = g.split_log2, S = 1 << lg, stages = g.stages;
+  uint8_t* in_s = sm + (size_t)stages * kStage;
+  const uint32_t in = smem_u32(in_s);
+  float* sc = reinterpret_cast<float*>(in_s + Sh::kIn);
+  uint8_t* ctl = in_s + Sh::kIn + Sh::kScales;
   const uint32_t bars = smem_u32(ctl);
   int* flags = reinterpret_cast<int*>(ctl + (2 * kMaxStages + 8) * 8);
   volatile int* abort_flag = flags;                          // [0] abort, [1] TMEM base
@@ -169,8 +171,8 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads) gemm_e4m3_kernel(const
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntiles = (g.N + kBlk - 1) / kBlk;
-  const int rank = (int)(blockIdx.x % (unsigned)S);          // = the CTA's rank in its cluster
-  const int tile = (int)(blockIdx.x / (unsigned)S);
+  const int rank = (int)(blockIdx.x & (unsigned)(S - 1));         // = the CTA's rank in its cluster
+  const int tile = (int)(blockIdx.x >> lg);
   const int nt = tile % ntiles;
   const int64_t m0 = (int64_t)(tile / ntiles) * BT;
   const int mv = g.M - m0 < BT ? (int)(g.M - m0) : BT;       // tokens of this tile
@@ -192,6 +194,7 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads) gemm_e4m3_kernel(const
     tma_prefetch_desc(&tma);
     tma_prefetch_desc(&tmw);
   }
+  if (S > 1) cluster_arrive();
   if (warp == 1) tmem_alloc(smem_u32(flags + 1), Sh::kTmem);
   tc_fence_before();
   __syncthreads();
@@ -344,52 +347,41 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads) gemm_e4m3_kernel(const
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
-  // Each CTA leaves its sums [token][weight row] in its own shared memory; CTA r of the cluster adds
-  // up the tokens r, r + S, ... from all parts in rank order, four neighbouring outputs per thread.
-  // Every thread passes both cluster barriers once; the second keeps each CTA's memory alive until
-  // its peers have read it.
-  float* part = reinterpret_cast<float*>(sm);
+  // Sums [token][weight row] to shared memory: token m goes to CTA m % S of the cluster, row m / S of
+  // its block from this rank (`in`, apart from the stages, so that nobody waits for a peer's
+  // products).  Behind one cluster barrier a CTA adds its tokens' parts in rank order from its own
+  // memory, four neighbouring outputs per thread, and no CTA reads another's.
+  const int per = BT >> lg;                                  // tokens of a CTA
+  if (S > 1) cluster_wait();                                 // the peers run: their memory may be written
   if (warp >= 2) {
+    const uint32_t at = in + 4u * (uint32_t)(rank * per * kBlk + nrow);
+    if (S > 1) {
 #pragma unroll
-    for (int e = 0; e < kCols; ++e)
-      if (c0 + e < mv) part[(c0 + e) * kBlk + nrow] = acc[e];
+      for (int e = 0; e < kCols; ++e) {
+        const int m = c0 + e;
+        if (m < mv) st_cluster_f32(map_peer(at + 512u * (uint32_t)(m >> lg), (uint32_t)(m & (S - 1))), acc[e]);
+      }
+    } else {
+      float* mine = reinterpret_cast<float*>(in_s) + nrow;
+#pragma unroll
+      for (int e = 0; e < kCols; ++e)
+        if (c0 + e < mv) mine[(c0 + e) * kBlk] = acc[e];
+    }
   }
   if (S > 1) cluster_sync();
   else __syncthreads();
   const int n = nt * kBlk + 4 * lane;
   if (warp >= 2 && n < g.N) {
-    constexpr int kRows = kEpi / 32, kFly = 8;               // rows of a step, and rows in flight per thread
-    const uint32_t base = smem_u32(part) + 16u * (uint32_t)lane;
-    for (int j = gt >> 5; rank + S * j < mv; j += kRows * kFly) {
-      float4 v[kFly];
-#pragma unroll
-      for (int u = 0; u < kFly; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int r = 0; r < S; ++r) {
-        const uint32_t from = S > 1 ? map_peer(base, (uint32_t)r) : base;
-        float4 t[kFly];
-#pragma unroll
-        for (int u = 0; u < kFly; ++u) {
-          const int m = rank + S * (j + u * kRows);
-          if (m < mv) t[u] = ld_cluster_f32x4(from + (uint32_t)m * (kBlk * 4u));
-        }
-#pragma unroll
-        for (int u = 0; u < kFly; ++u) {
-          if (rank + S * (j + u * kRows) < mv) {
-            v[u].x += t[u].x;
-            v[u].y += t[u].y;
-            v[u].z += t[u].z;
-            v[u].w += t[u].w;
-          }
-        }
+    for (int j = gt >> 5; rank + S * j < mv; j += kEpi / 32) {
+      const float4* from = reinterpret_cast<const float4*>(in_s) + j * 32 + lane;
+      float4 v = from[0];
+      for (int r = 1; r < S; ++r) {
+        const float4 t = from[r * per * 32];
+        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
       }
-#pragma unroll
-      for (int u = 0; u < kFly; ++u) {
-        const int m = rank + S * (j + u * kRows);
-        if (m < mv) store_out4(g, m0 + m, n, v[u]);
-      }
+      store_out4(g, m0 + rank + S * j, n, v);
     }
   }
-  if (S > 1) cluster_sync();
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -742,15 +734,15 @@ cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, in
   // Split K over a cluster of S CTAs while the tiles leave CTA slots free (two per SM, which the
   // shared memory below allows up to 64 tokens per tile) and each part keeps two blocks.
   const int64_t slots = (int64_t)num_sms * (BT == 128 ? 1 : 2);
-  int S = 1;
-  while (S < 8 && tiles * S * 2 <= slots && 4 * S <= g.G) S *= 2;
-  g.split = S;
+  int lg = 0;
+  while (lg < 3 && (tiles << (lg + 1)) <= slots && (4 << lg) <= g.G) ++lg;
+  const int S = 1 << lg;
+  g.split_log2 = lg;
   const int nkb = (g.G + S - 1) / S;
-  // as many stages as shared memory holds, and no more than there are blocks; the sums reuse them
+  // as many stages as shared memory holds, and no more than there are blocks
   int st = 2;
   const size_t room = BT == 128 ? kSmemOne : kSmemTwo;
   while (st < kMaxStages && st < nkb && FewShape<BT>::smem(st + 1) <= room) ++st;
-  while ((size_t)st * FewShape<BT>::kStage < (size_t)BT * kBlk * 4) ++st;
   g.stages = st;
   const size_t smem = FewShape<BT>::smem(st);
   cudaError_t e = cudaFuncSetAttribute(gemm_e4m3_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -804,7 +796,7 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
                              const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, bool out_f32,
                              int num_sms, cudaStream_t stream) {
   if (M <= 0 || N <= 0) return cudaSuccess;
-  GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 1, 2, 0};
+  GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 0, 2, 0};
   const int64_t es = out_f32 ? 4 : 2;
   g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
   cudaError_t e;
