@@ -7,8 +7,9 @@
 // epilogue warps multiply it by its two scales and add it to fp32 registers while the next
 // block's product runs.
 //
-// Weight rows are the MMA's M (128 rows: one weight scale per tile and block), BT tokens its N,
-// so a decode batch of a few tokens pads to 16 columns instead of 128 rows.  A cluster of S CTAs
+// Few tokens: a tile is 128 weight rows (one weight scale per tile and block) and BT tokens; up to 64
+// tokens the weight rows are the MMA's M and the tokens its N, so a decode batch of a few tokens pads
+// to 16 columns instead of 128 rows.  A cluster of S CTAs
 // shares a tile, each with its part of K; the parts are added in the order of K through
 // distributed shared memory, so that a product with few tiles still streams its weights on
 // every SM, and the result does not depend on timing.
@@ -58,10 +59,20 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
 // Half of a cluster barrier each: every thread arrives when it starts, and waits for the others'
 // arrivals before it touches a peer's shared memory.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_prefetch_l2_2d(const void* tmap, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y)
+               : "memory");
+}
 
 // 16 consecutive 32-bit columns of the thread's own TMEM lane (completed by the wait).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -133,13 +144,25 @@ __device__ __forceinline__ void store_out4(const GemmArgs& g, int64_t m, int n, 
 template <int BT>
 struct FewShape {
   static constexpr int kEpi = BT == 128 ? 256 : 128;         // epilogue threads
-  static constexpr int kThreads = 64 + kEpi;                 // + producer warp, MMA warp
+  static constexpr int kIssue = BT == 128 ? 2 : 1;           // MMA issuers (warps 1 ..)
+  static constexpr int kEpi0 = BT == 128 ? 128 : 64;         // first epilogue thread
+  static constexpr int kThreads = kEpi0 + kEpi;
   static constexpr int kCols = BT == 128 ? 64 : BT;          // columns per epilogue warp
-  static constexpr int kBufs = BT <= 64 ? 4 : 2;             // TMEM accumulators
-  static constexpr uint32_t kTmem = BT * kBufs;              // 64, 128 or 256 columns
+  // Up to 64 tokens the weight rows are the MMA's M, and an epilogue thread holds one weight row of
+  // every token: its factors, one per token and block, are read from shared memory.  Reading 128 of them
+  // takes the SM's shared-memory bandwidth longer than a block's products (256 x 8192 x 4096: 17.7 us,
+  // 515 of 940 cycles per block), so with 128 tokens these are the M and the weight rows the N: a thread
+  // holds one token, and one factor per block.
+  static constexpr bool kTok = BT == 128;
+  static constexpr int kBufs = 4;                            // TMEM accumulators
+  static constexpr uint32_t kTmem = BT * kBufs;              // 64 to 512 columns
   static constexpr uint32_t kStage = 16384u + (uint32_t)BT * 128u;   // weights, tokens
-  static constexpr uint32_t kScales = 2u * kScaleChunk * BT * 4u;    // two chunks of staged scales
-  static constexpr uint32_t kIn = (uint32_t)BT * kBlk * 4u;  // sums of the CTA's tokens from every part
+  static constexpr uint32_t kScales = BT == 128 ? 0u : 2u * kScaleChunk * BT * 4u;   // two chunks of staged scales
+  // The sums of the CTA's tokens from every part: BT * 512 bytes, apart from the stages, so that a CTA
+  // need not wait for its peers' products.  128 tokens' 64 KB lie over the first two stages instead
+  // (six stages, not four).
+  static constexpr bool kOver = BT == 128;
+  static constexpr uint32_t kIn = kOver ? 0u : (uint32_t)BT * kBlk * 4u;
   static constexpr size_t smem(int stages) {
     return 1024 + (size_t)stages * kStage + kIn + kScales + (2 * kMaxStages + 8) * 8 + 16;
   }
@@ -157,10 +180,10 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lg = g.split_log2, S = 1 << lg, stages = g.stages;
-  uint8_t* in_s = sm + (size_t)stages * kStage;
+  uint8_t* in_s = Sh::kOver ? sm : sm + (size_t)stages * kStage;
   const uint32_t in = smem_u32(in_s);
-  float* sc = reinterpret_cast<float*>(in_s + Sh::kIn);
-  uint8_t* ctl = in_s + Sh::kIn + Sh::kScales;
+  float* sc = reinterpret_cast<float*>(sm + (size_t)stages * kStage + Sh::kIn);
+  uint8_t* ctl = sm + (size_t)stages * kStage + Sh::kIn + Sh::kScales;
   const uint32_t bars = smem_u32(ctl);
   int* flags = reinterpret_cast<int*>(ctl + (2 * kMaxStages + 8) * 8);
   volatile int* abort_flag = flags;                          // [0] abort, [1] TMEM base
@@ -194,13 +217,18 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
     tma_prefetch_desc(&tma);
     tma_prefetch_desc(&tmw);
   }
-  if (S > 1) cluster_arrive();
+  if (S > 1 && !Sh::kOver) cluster_arrive();
   if (warp == 1) tmem_alloc(smem_u32(flags + 1), Sh::kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)flags[1];
   grid_launch_dependents();                                  // TMEM is held: the next kernel's set-up may begin
+  // While the kernel before this one ends, the weights are brought into L2 (only there: what that
+  // kernel may still write to them is seen by the loads behind the wait).  1 x 8192 x 2048 6.3 -> 5.7 us;
+  // from 64 tokens on the weights are read by more than one CTA or the loads have other company, and
+  // it costs up to 10 %.
+  if (BT <= 32 && warp == 0 && lane < nkb) tma_prefetch_l2_2d(&tmw, (kb0 + lane) * kBlk, nt * kBlk);
   grid_dependency_wait();
 
   if (warp == 0) {
@@ -231,29 +259,32 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
         mbar_wait(full(k % stages), (uint32_t)(k / stages) & 1u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp <= Sh::kIssue) {
     // ================================ MMA issue ================================
+    // With 128 tokens a block's products take the tensor core 256 cycles, less than a thread needs
+    // for its waits, products and signals: two issuers take the blocks in turn.
     if (lane == 0) {
       constexpr uint32_t kIdesc = idesc_e4m3(128, BT);
-      int s = 0, b = 0;
+      constexpr int kIssue = Sh::kIssue;
+      int i = warp - 1, s = i, b = i;
       uint32_t ph = 0, aph = 1;
-      int i = 0;
-      for (; i < nkb; ++i) {
+      for (; i < nkb; i += kIssue) {
         if (!(mbar_wait(aempty(b), aph, limit, abort_flag) && mbar_wait(full(s), ph, limit, abort_flag))) break;
         tc_fence_after();
-        const uint32_t wa = smem_u32(sm) + (uint32_t)s * kStage;
+        const uint32_t wa = smem_u32(sm) + (uint32_t)s * kStage, ta = wa + 16384u;
+        const uint32_t ra = Sh::kTok ? ta : wa, ca = Sh::kTok ? wa : ta;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_e4m3(tmem + (uint32_t)(b * BT), smem_desc_sw128(wa + 32u * kk), smem_desc_sw128(wa + 16384u + 32u * kk),
-                   kIdesc, kk > 0 ? 1u : 0u);
+          mma_e4m3(tmem + (uint32_t)(b * BT), smem_desc_sw128(ra + 32u * kk), smem_desc_sw128(ca + 32u * kk), kIdesc,
+                   kk > 0 ? 1u : 0u);
         mma_commit(empty(s));
         mma_commit(afull(b));
-        if (++s == stages) {
-          s = 0;
+        if ((s += kIssue) >= stages) {
+          s -= stages;
           ph ^= 1u;
         }
-        if (++b == kBufs) {
-          b = 0;
+        if ((b += kIssue) >= kBufs) {
+          b -= kBufs;
           aph ^= 1u;
         }
       }
@@ -261,68 +292,97 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
         raise_error(DSA_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
-      // the last product issued has completed before TMEM is freed or the stages are reused
-      if (i > 0) mbar_wait(afull((i - 1) % kBufs), (uint32_t)((i - 1) / kBufs) & 1u, kCleanupWaitNs, nullptr);
+      // its last product has completed before TMEM is freed
+      const int last = i - kIssue;
+      if (last >= 0) mbar_wait(afull(last % kBufs), (uint32_t)(last / kBufs) & 1u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();
   }
 
-  const int gt = threadIdx.x - 64;                           // epilogue thread
-  const int nrow = 32 * (warp & 3) + lane;                   // its weight row in the tile
-  const int c0 = kCols * (gt >> 7);                          // and its first column (token)
+  const int gt = threadIdx.x - Sh::kEpi0;                          // epilogue thread
+  const int row = 32 * (warp & 3) + lane;                    // its weight row (kTok: token) in the tile
+  const int c0 = kCols * (gt >> 7);                          // and its first token (kTok: weight row)
   float acc[kCols];
-  if (warp >= 2) {
+  if (gt >= 0) {
     // ================================ epilogue ================================
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c0;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
-    // Scales of kScaleChunk blocks at a time, both factors multiplied: thread gt fetches block
-    // gt % kScaleChunk of every (kEpi / kScaleChunk)-th token (neighbouring addresses), one chunk
-    // ahead, and leaves them in the chunk's half of `sc`.
-    constexpr int kPer = BT * kScaleChunk / kEpi, kStep = kEpi / kScaleChunk;
-    const int sk = gt % kScaleChunk, sm0 = gt / kScaleChunk;
-    const float* as = g.a_scale + m0 * g.G + kb0;
-    const float* ws = g.w_scale + (int64_t)nt * g.G + kb0;
-    float pa[kPer], pw;
-    auto fetch = [&](int i0) {
-      pw = i0 + sk < nkb ? __ldg(ws + i0 + sk) : 0.f;
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int m = sm0 + u * kStep;
-        pa[u] = (m < mv && i0 + sk < nkb) ? __ldg(as + (int64_t)m * g.G + i0 + sk) : 0.f;
-      }
-    };
-    fetch(0);
     bool ok = true;
     int b = 0;
     uint32_t ph = 0;
-    for (int i0 = 0, half = 0; i0 < nkb; i0 += kScaleChunk, half ^= 1) {
-      float* dst = sc + half * kScaleChunk * BT;
+    const float* ws = g.w_scale + (int64_t)nt * g.G + kb0;
+    // waits for a block's accumulator, reads the warp's columns and hands it back
+    auto take = [&](uint32_t (&d)[kCols]) {
+      if (ok) ok = mbar_wait(afull(b), ph, limit, abort_flag);
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      if (ok) {
+        tc_fence_after();
+        const uint32_t from = tl + (uint32_t)(b * BT);
+        if constexpr (kCols == 16) {
+          tmem_ld16(from, d);
+          tmem_ld16_wait(d);
+        } else if constexpr (kCols == 32) {
+          tmem_ld32_issue(from, d);
+          tmem_ld32_wait(d);
+        } else {
+          tmem_ld64_issue(from, d);
+          tmem_ld64_wait(d);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(aempty(b));
+      }
+      if (++b == kBufs) {
+        b = 0;
+        ph ^= 1u;
+      }
+    };
+    if constexpr (Sh::kTok) {
+      // the token's factor of block i, and of the two blocks after it in flight
+      const float* as = g.a_scale + (m0 + min(row, mv - 1)) * g.G + kb0;
+      float a0 = __ldg(as), w0 = __ldg(ws), a1 = __ldg(as + min(1, nkb - 1)), w1 = __ldg(ws + min(1, nkb - 1));
+      for (int i = 0; i < nkb; ++i) {
+        const float f = a0 * w0;
+        const int kn = min(i + 2, nkb - 1);
+        a0 = a1, w0 = w1;
+        a1 = __ldg(as + kn);
+        w1 = __ldg(ws + kn);
+        uint32_t d[kCols];
+        take(d);
+        if (!ok) break;
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) dst[sk * BT + sm0 + u * kStep] = pa[u] * pw;
-      group_sync<kEpi>();                                    // the other half is free once all have passed here
-      if (i0 + kScaleChunk < nkb) fetch(i0 + kScaleChunk);
-      const int nc = min(kScaleChunk, nkb - i0);
-      for (int i = 0; i < nc; ++i) {
-        if (ok) ok = mbar_wait(afull(b), ph, limit, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok) {
-          tc_fence_after();
-          const float4* f = reinterpret_cast<const float4*>(dst + i * BT + c0);
+        for (int e = 0; e < kCols; ++e) acc[e] = fmaf(__uint_as_float(d[e]), f, acc[e]);
+      }
+    } else {
+      // Factors of kScaleChunk blocks at a time, both scales multiplied: thread gt fetches block
+      // gt % kScaleChunk of every (kEpi / kScaleChunk)-th token (neighbouring addresses), one chunk
+      // ahead, and leaves them in the chunk's half of `sc`.
+      constexpr int kPer = BT * kScaleChunk / kEpi, kStep = kEpi / kScaleChunk;
+      const int sk = gt % kScaleChunk, sm0 = gt / kScaleChunk;
+      const float* as = g.a_scale + m0 * g.G + kb0;
+      float pa[kPer], pw;
+      auto fetch = [&](int i0) {
+        pw = i0 + sk < nkb ? __ldg(ws + i0 + sk) : 0.f;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          const int m = sm0 + u * kStep;
+          pa[u] = (m < mv && i0 + sk < nkb) ? __ldg(as + (int64_t)m * g.G + i0 + sk) : 0.f;
+        }
+      };
+      fetch(0);
+      for (int i0 = 0, half = 0; i0 < nkb; i0 += kScaleChunk, half ^= 1) {
+        float* dst = sc + half * kScaleChunk * BT;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) dst[sk * BT + sm0 + u * kStep] = pa[u] * pw;
+        group_sync<kEpi>();                                  // the other half is free once all have passed here
+        if (i0 + kScaleChunk < nkb) fetch(i0 + kScaleChunk);
+        const int nc = min(kScaleChunk, nkb - i0);
+        for (int i = 0; i < nc; ++i) {
           uint32_t d[kCols];
-          if constexpr (kCols == 16) {
-            tmem_ld16(tl + (uint32_t)(b * BT), d);
-            tmem_ld16_wait(d);
-          } else if constexpr (kCols == 32) {
-            tmem_ld32_issue(tl + (uint32_t)(b * BT), d);
-            tmem_ld32_wait(d);
-          } else {
-            tmem_ld64_issue(tl + (uint32_t)(b * BT), d);
-            tmem_ld64_wait(d);
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(aempty(b));
+          take(d);
+          if (!ok) continue;                                 // every warp still passes the chunks' barriers
+          const float4* f = reinterpret_cast<const float4*>(dst + i * BT + c0);
 #pragma unroll
           for (int e = 0; e < kCols; e += 4) {
             const float4 f4 = f[e / 4];
@@ -331,10 +391,6 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
             acc[e + 2] = fmaf(__uint_as_float(d[e + 2]), f4.z, acc[e + 2]);
             acc[e + 3] = fmaf(__uint_as_float(d[e + 3]), f4.w, acc[e + 3]);
           }
-        }
-        if (++b == kBufs) {
-          b = 0;
-          ph ^= 1u;
         }
       }
     }
@@ -348,38 +404,48 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
   // Sums [token][weight row] to shared memory: token m goes to CTA m % S of the cluster, row m / S of
-  // its block from this rank (`in`, apart from the stages, so that nobody waits for a peer's
-  // products).  Behind one cluster barrier a CTA adds its tokens' parts in rank order from its own
+  // its block from this rank.  Behind one cluster barrier a CTA adds its tokens' parts in rank order from its own
   // memory, four neighbouring outputs per thread, and no CTA reads another's.
   const int per = BT >> lg;                                  // tokens of a CTA
-  if (S > 1) cluster_wait();                                 // the peers run: their memory may be written
-  if (warp >= 2) {
-    const uint32_t at = in + 4u * (uint32_t)(rank * per * kBlk + nrow);
-    if (S > 1) {
+  if (S > 1) {                                               // the peers run, and where the sums lie over
+    if (Sh::kOver) cluster_arrive();                         // the stages their products are done
+    cluster_wait();
+  }
+  if (gt >= 0) {
+    if constexpr (Sh::kTok) {
+      // 16-byte pieces of the token's row, piece p at p ^ (token & 7): eight lanes' pieces fall into
+      // different banks
+      const uint32_t at = in + 512u * (uint32_t)(rank * per + (row >> lg));
+      if (row < mv) {
+#pragma unroll
+        for (int p = 0; p < kCols / 4; ++p) {
+          const uint32_t to = at + 16u * (uint32_t)((c0 / 4 + p) ^ (row & 7));
+          st_cluster_f32x4(map_peer(to, (uint32_t)(row & (S - 1))), acc[4 * p], acc[4 * p + 1], acc[4 * p + 2],
+                           acc[4 * p + 3]);
+        }
+      }
+    } else {
+      const uint32_t at = in + 4u * (uint32_t)(rank * per * kBlk + row);
 #pragma unroll
       for (int e = 0; e < kCols; ++e) {
         const int m = c0 + e;
         if (m < mv) st_cluster_f32(map_peer(at + 512u * (uint32_t)(m >> lg), (uint32_t)(m & (S - 1))), acc[e]);
       }
-    } else {
-      float* mine = reinterpret_cast<float*>(in_s) + nrow;
-#pragma unroll
-      for (int e = 0; e < kCols; ++e)
-        if (c0 + e < mv) mine[(c0 + e) * kBlk] = acc[e];
     }
   }
   if (S > 1) cluster_sync();
   else __syncthreads();
   const int n = nt * kBlk + 4 * lane;
-  if (warp >= 2 && n < g.N) {
+  if (gt >= 0 && n < g.N) {
     for (int j = gt >> 5; rank + S * j < mv; j += kEpi / 32) {
-      const float4* from = reinterpret_cast<const float4*>(in_s) + j * 32 + lane;
+      const int m = rank + S * j;
+      const float4* from = reinterpret_cast<const float4*>(in_s) + j * 32 + (Sh::kTok ? lane ^ (m & 7) : lane);
       float4 v = from[0];
       for (int r = 1; r < S; ++r) {
         const float4 t = from[r * per * 32];
         v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
       }
-      store_out4(g, m0 + rank + S * j, n, v);
+      store_out4(g, m0 + m, n, v);
     }
   }
 }
@@ -732,10 +798,12 @@ cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, in
   if (!make_map(&tma, a, K, g.M, lda, BT) || !make_map(&tmw, w, K, g.N, ldw, kBlk)) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)((g.N + kBlk - 1) / kBlk) * ((g.M + BT - 1) / BT);
   // Split K over a cluster of S CTAs while the tiles leave CTA slots free (two per SM, which the
-  // shared memory below allows up to 64 tokens per tile) and each part keeps two blocks.
+  // shared memory below allows up to 64 tokens per tile) and each part keeps two blocks.  Clusters of 8
+  // leave SMs of a GPC over, so they may ask for three quarters of the slots only (16 clusters of 8,
+  // one CTA per SM, ran in two waves: 128 x 2048 x 2048 11.4 us).
   const int64_t slots = (int64_t)num_sms * (BT == 128 ? 1 : 2);
   int lg = 0;
-  while (lg < 3 && (tiles << (lg + 1)) <= slots && (4 << lg) <= g.G) ++lg;
+  while (lg < 3 && (tiles << (lg + 1)) <= (lg == 2 ? slots * 3 / 4 : slots) && (4 << lg) <= g.G) ++lg;
   const int S = 1 << lg;
   g.split_log2 = lg;
   const int nkb = (g.G + S - 1) / S;
@@ -799,9 +867,12 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
   GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 0, 2, 0};
   const int64_t es = out_f32 ? 4 : 2;
   g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
+  // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 19 us
+  // against 36 us, while at 256 x 8192 x 4096 (one wave) the two are level (19.0 and 18.4 us) and below
+  // that the clusters win (128 x 8192 x 4096: 18.6 and 12.4 us).
+  const int64_t tiles = ((M + 127) / 128) * (int64_t)((N + 127) / 128);
   cudaError_t e;
-  const int64_t pair_tiles = ((M + 255) / 256) * (int64_t)((N + 255) / 256);
-  if (pair_tiles * 4 >= num_sms) e = launch_pair(a, lda, w, ldw, K, g, num_sms, stream);
+  if (tiles > num_sms) e = launch_pair(a, lda, w, ldw, K, g, num_sms, stream);
   else if (M <= 16) e = launch_bt<16>(a, lda, w, ldw, K, g, num_sms, stream);
   else if (M <= 32) e = launch_bt<32>(a, lda, w, ldw, K, g, num_sms, stream);
   else if (M <= 64) e = launch_bt<64>(a, lda, w, ldw, K, g, num_sms, stream);
