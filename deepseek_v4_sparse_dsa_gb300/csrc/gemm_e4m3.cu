@@ -59,8 +59,9 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float4 v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
 // Half of a cluster barrier each: every thread arrives when it starts, and waits for the others'
@@ -159,8 +160,8 @@ struct FewShape {
   static constexpr uint32_t kStage = 16384u + (uint32_t)BT * 128u;   // weights, tokens
   static constexpr uint32_t kScales = BT == 128 ? 0u : 2u * kScaleChunk * BT * 4u;   // two chunks of staged scales
   // The sums of the CTA's tokens from every part: BT * 512 bytes, apart from the stages, so that a CTA
-  // need not wait for its peers' products.  128 tokens' 64 KB lie over the first two stages instead
-  // (six stages, not four).
+  // need not wait for its peers' products.  128 tokens' 64 KB, and the CTA's own sums as much again,
+  // lie over the stages instead.
   static constexpr bool kOver = BT == 128;
   static constexpr uint32_t kIn = kOver ? 0u : (uint32_t)BT * kBlk * 4u;
   static constexpr size_t smem(int stages) {
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int lg = g.split_log2, S = 1 << lg, stages = g.stages;
-  uint8_t* in_s = Sh::kOver ? sm : sm + (size_t)stages * kStage;
+  uint8_t* in_s = Sh::kOver ? sm + BT * kBlk * 4 : sm + (size_t)stages * kStage;
   const uint32_t in = smem_u32(in_s);
   float* sc = reinterpret_cast<float*>(sm + (size_t)stages * kStage + Sh::kIn);
   uint8_t* ctl = sm + (size_t)stages * kStage + Sh::kIn + Sh::kScales;
@@ -403,49 +404,67 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
   __syncthreads();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, Sh::kTmem);
-  // Sums [token][weight row] to shared memory: token m goes to CTA m % S of the cluster, row m / S of
-  // its block from this rank.  Behind one cluster barrier a CTA adds its tokens' parts in rank order from its own
-  // memory, four neighbouring outputs per thread, and no CTA reads another's.
+  // The sums of token m go to CTA m % S of the cluster, as rows of 128 weight rows' sums: row
+  // rank * per + m / S of its `in`.  Behind a cluster barrier each CTA adds its tokens' parts in rank
+  // order from its own memory, four neighbouring outputs per thread, and no CTA reads another's.
+  // A warp writes whole rows (32 lanes, neighbouring addresses): with the lanes' 16-byte pieces spread
+  // over rows and CTAs the writes to the peers took 2.6 us instead of 1.
   const int per = BT >> lg;                                  // tokens of a CTA
   if (S > 1) {                                               // the peers run, and where the sums lie over
     if (Sh::kOver) cluster_arrive();                         // the stages their products are done
     cluster_wait();
   }
-  if (gt >= 0) {
-    if constexpr (Sh::kTok) {
-      // 16-byte pieces of the token's row, piece p at p ^ (token & 7): eight lanes' pieces fall into
-      // different banks
-      const uint32_t at = in + 512u * (uint32_t)(rank * per + (row >> lg));
-      if (row < mv) {
+  if constexpr (Sh::kTok) {
+    // The CTA's own sums first: 16-byte pieces of the token's row, piece p at p ^ (token & 7), so that
+    // eight lanes' pieces fall into different banks.
+    if (gt >= 0) {
+      float4* own = reinterpret_cast<float4*>(sm + 512 * row);
 #pragma unroll
-        for (int p = 0; p < kCols / 4; ++p) {
-          const uint32_t to = at + 16u * (uint32_t)((c0 / 4 + p) ^ (row & 7));
-          st_cluster_f32x4(map_peer(to, (uint32_t)(row & (S - 1))), acc[4 * p], acc[4 * p + 1], acc[4 * p + 2],
-                           acc[4 * p + 3]);
+      for (int p = 0; p < kCols / 4; ++p)
+        own[(c0 / 4 + p) ^ (row & 7)] = make_float4(acc[4 * p], acc[4 * p + 1], acc[4 * p + 2], acc[4 * p + 3]);
+      group_sync<kEpi>();
+      if (S > 1) {
+#pragma unroll 4
+        for (int m = gt >> 5; m < mv; m += kEpi / 32) {
+          const int r = m & (S - 1);
+          const float4 v = reinterpret_cast<const float4*>(sm)[32 * m + lane];
+          if (r != rank) st_cluster_f32x4(map_peer(in + 512u * (uint32_t)(rank * per + (m >> lg)) + 16u * lane, (uint32_t)r), v);
         }
       }
-    } else {
-      const uint32_t at = in + 4u * (uint32_t)(rank * per * kBlk + row);
+    }
+  } else if (gt >= 0) {
+    const uint32_t at = in + 4u * (uint32_t)(rank * per * kBlk + row);
 #pragma unroll
-      for (int e = 0; e < kCols; ++e) {
-        const int m = c0 + e;
-        if (m < mv) st_cluster_f32(map_peer(at + 512u * (uint32_t)(m >> lg), (uint32_t)(m & (S - 1))), acc[e]);
-      }
+    for (int e = 0; e < kCols; ++e) {
+      const int m = c0 + e;
+      if (m < mv) st_cluster_f32(map_peer(at + 512u * (uint32_t)(m >> lg), (uint32_t)(m & (S - 1))), acc[e]);
     }
   }
   if (S > 1) cluster_sync();
   else __syncthreads();
   const int n = nt * kBlk + 4 * lane;
   if (gt >= 0 && n < g.N) {
-    for (int j = gt >> 5; rank + S * j < mv; j += kEpi / 32) {
-      const int m = rank + S * j;
-      const float4* from = reinterpret_cast<const float4*>(in_s) + j * 32 + (Sh::kTok ? lane ^ (m & 7) : lane);
-      float4 v = from[0];
-      for (int r = 1; r < S; ++r) {
-        const float4 t = from[r * per * 32];
-        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+    constexpr int kRows = kEpi / 32, kFly = 4;               // warps, and rows in flight per warp
+    for (int j0 = gt >> 5; rank + S * j0 < mv; j0 += kRows * kFly) {
+      float4 v[kFly];
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int r = 0; r < S; ++r) {
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+          const int j = j0 + u * kRows, m = rank + S * j;
+          if (m < mv) {
+            const uint8_t* from = Sh::kTok && r == rank ? sm + 512 * m : in_s + 512 * (r * per + j);
+            const float4 t = reinterpret_cast<const float4*>(from)[Sh::kTok ? lane ^ (m & 7) : lane];
+            v[u].x += t.x, v[u].y += t.y, v[u].z += t.z, v[u].w += t.w;
+          }
+        }
       }
-      store_out4(g, m0 + m, n, v);
+#pragma unroll
+      for (int u = 0; u < kFly; ++u) {
+        const int m = rank + S * (j0 + u * kRows);
+        if (m < mv) store_out4(g, m0 + m, n, v[u]);
+      }
     }
   }
 }
@@ -811,6 +830,7 @@ cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, in
   int st = 2;
   const size_t room = BT == 128 ? kSmemOne : kSmemTwo;
   while (st < kMaxStages && st < nkb && FewShape<BT>::smem(st + 1) <= room) ++st;
+  if (FewShape<BT>::kOver && S > 1 && st < 4) st = 4;        // 128 KB of sums
   g.stages = st;
   const size_t smem = FewShape<BT>::smem(st);
   cudaError_t e = cudaFuncSetAttribute(gemm_e4m3_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
