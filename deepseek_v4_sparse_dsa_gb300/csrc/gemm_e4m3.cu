@@ -428,7 +428,8 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
         for (int m = gt >> 5; m < mv; m += kEpi / 32) {
           const int r = m & (S - 1);
           const float4 v = reinterpret_cast<const float4*>(sm)[32 * m + lane];
-          if (r != rank) st_cluster_f32x4(map_peer(in + 512u * (uint32_t)(rank * per + (m >> lg)) + 16u * lane, (uint32_t)r), v);
+          if (r != rank && nt * kBlk + 4 * (lane ^ (m & 7)) < g.N)
+            st_cluster_f32x4(map_peer(in + 512u * (uint32_t)(rank * per + (m >> lg)) + 16u * lane, (uint32_t)r), v);
         }
       }
     }
@@ -888,14 +889,15 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
   const int64_t es = out_f32 ? 4 : 2;
   g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
   // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 19 us
-  // against 36 us, while at 256 x 8192 x 4096 (one wave) the two are level (19.0 and 18.4 us) and below
-  // that the clusters win (128 x 8192 x 4096: 18.6 and 12.4 us).
-  const int64_t tiles = ((M + 127) / 128) * (int64_t)((N + 127) / 128);
+  // against 36 us, while at 256 x 8192 x 4096 (one wave) the clusters win (14.7 and 19.0 us).
+  // Tiles of 32 tokens pay while there are few of them, for more CTAs share the work (128 x 512 x 8192
+  // 6.8 us against 8.0 with 128 tokens, 500 x 128 x 4096 5.3 and 6.4); past half the SMs they lose
+  // (333 x 1000 x 1808 7.3 and 6.8 us).  Up to 16 tokens 16 columns suffice.
+  const int64_t nt = (N + 127) / 128;
   cudaError_t e;
-  if (tiles > num_sms) e = launch_pair(a, lda, w, ldw, K, g, num_sms, stream);
+  if ((M + 127) / 128 * nt > num_sms) e = launch_pair(a, lda, w, ldw, K, g, num_sms, stream);
   else if (M <= 16) e = launch_bt<16>(a, lda, w, ldw, K, g, num_sms, stream);
-  else if (M <= 32) e = launch_bt<32>(a, lda, w, ldw, K, g, num_sms, stream);
-  else if (M <= 64) e = launch_bt<64>(a, lda, w, ldw, K, g, num_sms, stream);
+  else if (M <= 32 || (M + 31) / 32 * nt * 2 <= num_sms) e = launch_bt<32>(a, lda, w, ldw, K, g, num_sms, stream);
   else e = launch_bt<128>(a, lda, w, ldw, K, g, num_sms, stream);
   note_launch();
   if (e != cudaSuccess) return e;
