@@ -262,7 +262,7 @@ dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual
   if (y == x && ldy != ldx) return DSA_ERR_INVALID_ARG;
   if (y != nullptr && (y == residual || y == residual_out)) return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_add_rmsnorm_e4m3(x, ldx, residual, ldr, gamma, eps, T, D, type == DSA_REAL_F32,
-                                             residual_out, y, y_fp8, ldy, y_scale, pow2_scale != 0,
+                                             residual_out, y, y_fp8, ldy, y_scale, pow2_scale != 0, device_sm_count(),
                                              static_cast<cudaStream_t>(stream)));
 }
 

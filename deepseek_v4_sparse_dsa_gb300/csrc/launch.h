@@ -111,7 +111,7 @@ cudaError_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, int
                                 cudaStream_t stream);
 cudaError_t launch_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* res, int64_t ldr, const float* gamma,
                                     float eps, int64_t T, int D, bool f32, void* res_out, void* y, uint8_t* codes,
-                                    int64_t ldy, float* scale, bool pow2, cudaStream_t stream);
+                                    int64_t ldy, float* scale, bool pow2, int num_sms, cudaStream_t stream);
 int add_rmsnorm_max_dim();
 cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* w, int64_t ldw,
                              const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, bool out_f32,
