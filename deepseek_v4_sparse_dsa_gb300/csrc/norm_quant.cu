@@ -135,9 +135,11 @@ __device__ __forceinline__ float next_pow2_f32(float s) {
 // VPT pieces of 8 elements per thread: piece j of thread t of a row is j * tpr + t.  A CTA walks the rows
 // with a stride of the grid; in 16-byte accesses with one or two pieces the next row's loads are in flight
 // while this one is worked on, and gamma stays in registers.  Four pieces leave no room for either, and
-// element-wise accesses need the registers for more warps (4096 x 4097 bf16: 79 us with one CTA an SM).
+// element-wise accesses need the registers for more warps (4096 x 4097 bf16: 79 us with one CTA an SM,
+// 45 us so).  bf16 rows are held to 64 registers (8192 x 7168: 88 -> 76 us), fp32 rows lose by that
+// (4096 x 4096: 35 -> 43 us).
 template <typename T, int VPT, bool VEC>
-__global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, !VEC && VPT < 4 ? 2 : 1) add_rmsnorm_e4m3_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2) && VPT < 4 ? 2 : 1) add_rmsnorm_e4m3_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   __shared__ float s_sum[2][32];
   const int rpc = blockDim.x / a.tpr;                  // rows per CTA

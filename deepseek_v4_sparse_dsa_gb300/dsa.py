@@ -106,9 +106,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
 def _ptr(x):
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:                # an integer address
+        return int(x)
 
 
 _raw_stream = None
@@ -132,7 +133,7 @@ def _current_stream():
 
 def _stream(s):
     if s is None:
-        return _current_stream()
+        return _raw_stream() if _raw_stream is not None else _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
