@@ -272,6 +272,8 @@ dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, co
   if (out_type != DSA_REAL_BF16 && out_type != DSA_REAL_F32) return DSA_ERR_INVALID_ARG;
   if (M < 0 || N < 0 || K < 1) return DSA_ERR_INVALID_ARG;
   if (M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256) return DSA_ERR_UNSUPPORTED;
+  if ((M + 127) / 128 * (((int64_t)N + 127) / 128) > INT32_MAX) return DSA_ERR_UNSUPPORTED;   // tiles are counted in int32
+  if (lda >= (int64_t)1 << 40 || ldw >= (int64_t)1 << 40) return DSA_ERR_UNSUPPORTED;          // tensor-map strides
   if (M == 0 || N == 0) return DSA_OK;
   if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)
     return DSA_ERR_INVALID_ARG;

@@ -332,14 +332,16 @@ dsa_status dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens,
  *  y_fp8    [T, D] E4M3 codes with y_scale [T, ceil(D / 128)] fp32 (row-major), both or
  *           neither NULL.  y and y_fp8 have rows ldy elements apart.  A ldy that is a
  *           multiple of 16 makes the codes an operand of dsa_gemm_e4m3.
- * At least one of residual_out, y and y_fp8 is given.  1 <= D <= 32768.  Any element-aligned
+ * At least one of residual_out, y and y_fp8 is given; no other overlap of outputs with inputs
+ * or with one another.  1 <= D <= 32768.  Any element-aligned
  * pointers and strides >= D work; with D and the strides multiples of 8 and 16-byte aligned
  * pointers the rows move in 16-byte accesses.
- * Arithmetic in fp32: the sum of squares over a fixed order, each product rounded on its own,
- * the quotient by 448's group scale as a product with its reciprocal, so a code can differ
- * from the exact quotient's only where that lies within a few fp32 ulps of a rounding
- * boundary.  A row holding a NaN gives NaN codes; an infinity gives NaN at its place and
- * zeros elsewhere in the row.
+ * Arithmetic in fp32: the sum of squares in an order that D and T fix, 1 / rms by the hardware's
+ * reciprocal root (2 ulps), each product rounded on its own; y / y_scale is formed as
+ * (r gamma) (448 / max|r gamma|), without the row's common factor, so a code can differ from
+ * the exact quotient's only where that lies within a few fp32 ulps of a rounding boundary.
+ * r * gamma must be finite.  A row holding a NaN gives NaN codes; an infinity gives NaN at its
+ * place and zeros elsewhere in the row.
  */
 dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
                                 float eps, int64_t T, int D, dsa_real type, void* residual_out, void* y,
@@ -354,12 +356,14 @@ dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual
  *           fp32.  Scales are row-major and may be any fp32 values.
  *  out      [M, N] of `out_type`, rows ldo elements apart.
  * a and w are 16-byte aligned, lda and ldw multiples of 16 and at least K; K >= 1 (what lies
- * past K in a row is not read), M and N any.  out may not overlap an input.
+ * past K in a row is not part of the product), M and N any; any element-aligned out and ldo
+ * >= N (16-byte aligned rows are stored in 16-byte accesses).  out may not overlap an input.
  * Arithmetic: exact products summed in fp32 by the tensor cores within a block of 128, the
  * block's sum times its two scales (their product rounded to fp32) added in fp32 in the order
- * of K; with few tiles K is cut into up to 8 parts whose sums are added in order.  One
- * rounding to bf16 at the end.  The result depends on the device's SM count but not on
- * timing.  No workspace.  A device-side wait that expires sets DSA_DEVERR_TIMEOUT.
+ * of K; with few tiles K is cut into 2, 4 or 8 parts whose sums are added in order.  One
+ * rounding to bf16 at the end.  The result depends on the sizes and the device's SM count (a
+ * row's sums may be cut differently in another batch) but not on timing.  No workspace.  A
+ * device-side wait that expires sets DSA_DEVERR_TIMEOUT.
  */
 dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* w, int64_t ldw,
                          const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, dsa_real out_type,

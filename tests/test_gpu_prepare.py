@@ -101,6 +101,26 @@ def test_assign_slots_batches(B, bs, ctx, most):
     Slots(rng.integers(0, ctx, B), np.full(B, most), bs, seed=B + 1).check(torch.cuda.Stream())
 
 
+def test_assign_slots_largest_batch_and_offsets_past_32_bits():
+    # 65536 requests with table rows of 40000 entries: 2.6e9 entries, the last rows past 2^31
+    B, stride, bs = 65536, 40000, 16
+    table = torch.full((B, stride), -1, dtype=torch.int32, device="cuda")
+    cached = torch.zeros(B, dtype=torch.int32, device="cuda")
+    new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    new[0], new[-1], new[-2], cached[-2] = 1, 2, 3, 30
+    table[-2, :2] = torch.tensor([3, 4], dtype=torch.int32)
+    free = torch.arange(10, 20, dtype=torch.int32, device="cuda")
+    ctx, start, used = torch.empty_like(cached), torch.empty(B + 1, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+    slot, pos = torch.empty(8, dtype=torch.int64, device="cuda"), torch.empty(8, dtype=torch.int32, device="cuda")
+    dsa.dsa_assign_slots(cached, new, B, bs, free, 10, 100, table, stride, 8, ctx, start, slot, pos, used)
+    assert dsa.dsa_device_error() == 0
+    assert slot.tolist() == [160, 4 * 16 + 14, 4 * 16 + 15, 11 * 16, 12 * 16, 12 * 16 + 1, -1, -1]
+    assert pos.tolist() == [0, 30, 31, 32, 0, 1, 0, 0] and int(used) == 3
+    assert table[-2, :4].tolist() == [3, 4, 11, -1] and table[-1, :2].tolist() == [12, -1] and int(table[0, 0]) == 10
+    assert int((table != -1).sum()) == 5
+    assert start[:3].tolist() == [0, 1, 1] and start[-3:].tolist() == [1, 4, 6] and torch.equal(ctx, cached + new)
+
+
 def test_assign_slots_no_requests():
     err, table, ctx, start, slot, pos, used = Slots([], [], 64, 9, 1).run()
     assert err == 0 and start.tolist() == [0] and used == 0
@@ -235,6 +255,27 @@ def test_add_rmsnorm_zero_rows_and_non_finite():
     assert (c[3, 200] & 0x7F) == 0x7F and (np.delete(c[3], 200) & 0x7F == 0).all()
 
 
+def test_add_rmsnorm_bf16_subnormals_and_offsets_past_32_bits():
+    # sums of bf16 subnormals are exact and kept
+    x = torch.full((2, 256), 9.2e-41, device="cuda").to(torch.bfloat16)
+    res = torch.full((2, 256), 1.8e-40, device="cuda").to(torch.bfloat16)
+    assert x[0, 0] > 0 and res[0, 0] > 0
+    ro, g = torch.empty_like(x), torch.ones(256, device="cuda")
+    dsa.dsa_add_rmsnorm_e4m3(x, 256, res, 256, g, 1e-6, 2, 256, BF16, ro, None, None, 0, None)
+    assert np.array_equal(f64(ro), f64(x) + f64(res))
+    # 2.3e9 elements: the last rows against the same rows alone
+    T, D = 70000, 32768
+    x = torch.zeros(T, D, dtype=torch.bfloat16, device="cuda")
+    x[-40:] = torch.randn(40, D, device="cuda").to(torch.bfloat16)
+    g = torch.rand(D, device="cuda") + 0.5
+    codes, scale = torch.empty(T, D, dtype=torch.uint8, device="cuda"), torch.empty(T, D // 128, device="cuda")
+    dsa.dsa_add_rmsnorm_e4m3(x, D, None, 0, g, 1e-6, T, D, BF16, None, None, codes, D, scale)
+    assert dsa.dsa_device_error() == 0
+    _, y64 = ref.add_rmsnorm(f64(x[-40:]), None, f64(g), float(np.float32(1e-6)), True)
+    ref.check_quantised(y64, codes[-40:].cpu().numpy(), scale[-40:].cpu().numpy(), False)
+    assert not codes[:-40].any() and bool((scale[:-40] == 1).all())
+
+
 def test_add_rmsnorm_rows_do_not_depend_on_the_batch():
     x = torch.randn(300, 1536, device="cuda").to(torch.bfloat16)
     g = torch.rand(1536, device="cuda")
@@ -317,6 +358,46 @@ def test_gemm_large_product():
     assert (np.abs(f64(out)[rows] - want) <= tol + 2.0 ** -8 * (np.abs(want) + tol)).all()
     # the same call twice: the same bits
     assert torch.equal(out, gemm_call(a, asc, w, wsc, K, BF16))
+
+
+@pytest.mark.parametrize("M,N,K,ldo", [(2000, 2304, 384, 2304), (2304, 2000, 1000, 2008), (1500, 2600, 4112, 2601),
+                                       (129, 19500, 160, 19500), (19500, 129, 160, 136)])
+@pytest.mark.parametrize("typ", [BF16, F32])
+def test_gemm_many_tiles(M, N, K, ldo, typ):
+    # whole and ragged tiles in both directions, K past its last whole block, stores of 16 bytes and less
+    gemm_check(M, N, K, typ, ldo=ldo, signed=True)
+
+
+def test_gemm_offsets_past_32_bits():
+    # rows 1 MiB apart: the last rows of a and out lie past 4 GiB and 2^32 elements
+    M, N, K, ld = 4500, 128, 256, 1 << 20
+    a, asc, w, wsc = gemm_inputs(M, N, K)
+    want = gemm_call(a, asc, w, wsc, K, BF16)
+    big = torch.zeros(M, ld, dtype=torch.uint8, device="cuda")
+    big[:, :K] = dev(a)
+    out = torch.zeros(M, ld, dtype=torch.bfloat16, device="cuda")
+    d = [dev(v) for v in (asc, w, wsc)]
+    dsa.dsa_gemm_e4m3(big, ld, d[0], d[1], K, d[2], M, N, K, out, ld, BF16)
+    assert dsa.dsa_device_error() == 0
+    assert torch.equal(out[:, :N], want) and not out[:, N:].any()
+
+
+def test_gemm_on_two_streams_at_once():
+    # products of different shapes in flight together, each repeated: every result as when run alone
+    cases = [(gemm_inputs(m, n, k), k) for m, n, k in ((3, 700, 2048), (300, 900, 1024), (2300, 2100, 512))]
+    want = [gemm_call(*c, k, BF16) for c, k in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    data = [[dev(v) for v in c] for c, _ in cases]
+    outs = [[torch.empty_like(w) for _ in range(10)] for w in want]
+    torch.cuda.synchronize()
+    for i in range(10):
+        for (a, asc, w, wsc), (_, k), st, o in zip(data, cases, streams, outs):
+            dsa.dsa_gemm_e4m3(a, a.shape[1], asc, w, w.shape[1], wsc, a.shape[0], w.shape[0], k, o[i], w.shape[0], BF16, st)
+    for st in streams:
+        assert dsa.dsa_device_error(st) == 0
+    for w, o in zip(want, outs):
+        assert all(torch.equal(w, x) for x in o)
 
 
 def test_gemm_non_finite_stays_in_its_row_and_column():

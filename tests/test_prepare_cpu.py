@@ -66,7 +66,8 @@ def gemm(a=_p(1), lda=256, asc=_p(2), w=_p(3), ldw=256, wsc=_p(4), M=4, N=128, K
     (dict(wsc=None), INVALID), (dict(out=None), INVALID), (dict(lda=240), INVALID), (dict(ldw=240), INVALID),
     (dict(lda=264), INVALID), (dict(ldw=264), INVALID), (dict(ldo=127), INVALID), (dict(a=_p(1) + 8), INVALID),
     (dict(w=_p(3) + 8), INVALID), (dict(out=_p(5) + 1), INVALID), (dict(out=_p(5) + 2, typ=dsa.DSA_REAL_F32), INVALID),
-    (dict(asc=_p(2) + 1), INVALID),
+    (dict(asc=_p(2) + 1), INVALID), (dict(lda=1 << 40), UNSUPPORTED), (dict(ldw=1 << 40), UNSUPPORTED),
+    (dict(M=2**31 - 300, N=2**31 - 300, ldo=2**31), UNSUPPORTED),
 ])
 def test_gemm_refusals(lib, bad, status):  # noqa: F811
     before = dsa.dsa_launch_count()
