@@ -16,6 +16,7 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -811,6 +812,20 @@ bool make_map(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Lets a kernel ask for up to kSmemOne bytes of shared memory on the current device: once per kernel and
+// device (`devices` has a bit for each), not on every call.
+template <typename K>
+cudaError_t allow_smem(K* kernel, std::atomic<uint64_t>& devices) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (dev < 64 && (devices.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemOne);
+  if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <int BT>
 cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, int64_t K, GemmArgs g, int num_sms,
                       cudaStream_t stream) {
@@ -834,7 +849,8 @@ cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, in
   if (FewShape<BT>::kOver && S > 1 && st < 4) st = 4;        // 128 KB of sums
   g.stages = st;
   const size_t smem = FewShape<BT>::smem(st);
-  cudaError_t e = cudaFuncSetAttribute(gemm_e4m3_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e = allow_smem(gemm_e4m3_kernel<BT>, devices);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles * S));
@@ -857,8 +873,8 @@ cudaError_t launch_pair(const void* a, int64_t lda, const void* w, int64_t ldw, 
                         int num_sms, cudaStream_t stream) {
   CUtensorMap tma, tmw;
   if (!make_map(&tma, a, K, g.M, lda, 128) || !make_map(&tmw, w, K, g.N, ldw, 128)) return cudaErrorInvalidValue;
-  const cudaError_t e =
-      cudaFuncSetAttribute(gemm_e4m3_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPairSmem);
+  static std::atomic<uint64_t> devices{0};
+  const cudaError_t e = allow_smem(gemm_e4m3_pair_kernel, devices);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((g.M + 255) / 256) * (int64_t)((g.N + 255) / 256);
   const int64_t pairs = tiles < num_sms / 2 ? tiles : num_sms / 2;
