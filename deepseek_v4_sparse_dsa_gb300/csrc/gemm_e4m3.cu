@@ -119,10 +119,15 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
                : "memory");
 }
 
-// Four consecutive outputs of row m from column n.
+__device__ __forceinline__ void store_out(const GemmArgs& g, int64_t at, float v) {
+  if (g.out_f32) static_cast<float*>(g.out)[at] = v;
+  else static_cast<__nv_bfloat16*>(g.out)[at] = __float2bfloat16_rn(v);
+}
+
+// Four consecutive outputs of row m from column n (a multiple of 4), rows 16-byte aligned.
 __device__ __forceinline__ void store_out4(const GemmArgs& g, int64_t m, int n, float4 v) {
   const int64_t at = m * g.ldo + n;
-  if (g.out_vec && n + 4 <= g.N) {
+  if (n + 4 <= g.N) {
     if (g.out_f32) {
       *reinterpret_cast<float4*>(static_cast<float*>(g.out) + at) = v;
     } else {
@@ -134,11 +139,8 @@ __device__ __forceinline__ void store_out4(const GemmArgs& g, int64_t m, int n, 
   }
   const float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (n + i >= g.N) break;
-    if (g.out_f32) static_cast<float*>(g.out)[at + i] = e[i];
-    else static_cast<__nv_bfloat16*>(g.out)[at + i] = __float2bfloat16_rn(e[i]);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (n + i < g.N) store_out(g, at + i, e[i]);
 }
 
 // Shapes of the kernel with BT tokens per tile.  Four epilogue warps (one per TMEM lane quarter) take
@@ -444,9 +446,14 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
   }
   if (S > 1) cluster_sync();
   else __syncthreads();
-  const int n = nt * kBlk + 4 * lane;
-  if (gt >= 0 && n < g.N) {
-    constexpr int kRows = kEpi / 32, kFly = 4;               // warps, and rows in flight per warp
+  if (gt < 0) return;
+  constexpr int kRows = kEpi / 32;                           // warps, a row each
+  // row of part r of the CTA's token j
+  const auto part = [&](int r, int j) { return Sh::kTok && r == rank ? sm + 512 * (rank + S * j) : in_s + 512 * (r * per + j); };
+  if (g.out_vec) {
+    const int n = nt * kBlk + 4 * lane;
+    if (n >= g.N) return;
+    constexpr int kFly = 4;                                  // rows in flight per warp
     for (int j0 = gt >> 5; rank + S * j0 < mv; j0 += kRows * kFly) {
       float4 v[kFly];
 #pragma unroll
@@ -456,8 +463,7 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
         for (int u = 0; u < kFly; ++u) {
           const int j = j0 + u * kRows, m = rank + S * j;
           if (m < mv) {
-            const uint8_t* from = Sh::kTok && r == rank ? sm + 512 * m : in_s + 512 * (r * per + j);
-            const float4 t = reinterpret_cast<const float4*>(from)[Sh::kTok ? lane ^ (m & 7) : lane];
+            const float4 t = reinterpret_cast<const float4*>(part(r, j))[Sh::kTok ? lane ^ (m & 7) : lane];
             v[u].x += t.x, v[u].y += t.y, v[u].z += t.z, v[u].w += t.w;
           }
         }
@@ -466,6 +472,24 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
       for (int u = 0; u < kFly; ++u) {
         const int m = rank + S * (j0 + u * kRows);
         if (m < mv) store_out4(g, m0 + m, n, v[u]);
+      }
+    }
+  } else {                                                   // rows at any alignment: neighbouring elements
+    for (int j = gt >> 5; rank + S * j < mv; j += kRows) {
+      const int m = rank + S * j;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < S; ++r) {
+        const float* from = reinterpret_cast<const float*>(part(r, j));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = lane + 32 * q;
+          v[q] += from[Sh::kTok ? c ^ ((m & 7) << 2) : c];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = nt * kBlk + lane + 32 * q;
+        if (n < g.N) store_out(g, (m0 + m) * g.ldo + n, v[q]);
       }
     }
   }
@@ -724,20 +748,41 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
 #pragma unroll
         for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = v[p];
         __syncwarp();
+        if (g.out_vec) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + (lane >> 3), p = lane & 7;
-          const int col = col0 + kPer * p;
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
-          if (r < rows && col < g.N) {
-            E* o = out + (int64_t)(m0 + r) * g.ldo + col;
-            if (g.out_vec && col + kPer <= g.N) {
-              *reinterpret_cast<uint4*>(o) = w;
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), p = lane & 7;
+            const int col = col0 + kPer * p;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
+            if (r < rows && col < g.N) {
+              E* o = out + (int64_t)(m0 + r) * g.ldo + col;
+              if (col + kPer <= g.N) {
+                *reinterpret_cast<uint4*>(o) = w;
+              } else {
+                const E* we = reinterpret_cast<const E*>(&w);
+#pragma unroll
+                for (int e = 0; e < kPer; ++e)
+                  if (col + e < g.N) o[e] = we[e];
+              }
+            }
+          }
+        } else {
+          // rows at any alignment: the warp stores one row at a time, neighbouring words (a bf16 row that
+          // starts at 2 mod 4 has its first and last element apart)
+          const int cols = min(128 / (int)sizeof(E), g.N - col0);
+          const auto at = [&](int r, int e) { return stage + r * 128 + (((e / kPer) ^ (r & 7)) << 4) + (e % kPer) * (int)sizeof(E); };
+#pragma unroll 4
+          for (int r = 0; r < rows; ++r) {
+            E* o = out + (int64_t)(m0 + r) * g.ldo + col0;
+            if constexpr (sizeof(E) == 4) {
+              if (lane < cols) o[lane] = *reinterpret_cast<const E*>(at(r, lane));
             } else {
-              const E* we = reinterpret_cast<const E*>(&w);
-#pragma unroll
-              for (int e = 0; e < kPer; ++e)
-                if (col + e < g.N) o[e] = we[e];
+              const int odd = (int)(reinterpret_cast<uintptr_t>(o) >> 1) & 1, e = 2 * lane + odd;
+              const uint32_t lo = e < 64 ? *reinterpret_cast<const uint16_t*>(at(r, e)) : 0u;
+              const uint32_t hi = e < 63 ? *reinterpret_cast<const uint16_t*>(at(r, e + 1)) : 0u;
+              if (e + 1 < cols) *reinterpret_cast<uint32_t*>(o + e) = lo | hi << 16;
+              else if (e < cols) o[e] = (E)lo;
+              if (odd && lane == 0 && cols > 0) o[0] = *reinterpret_cast<const uint16_t*>(at(r, 0));
             }
           }
         }
@@ -826,19 +871,22 @@ cudaError_t allow_smem(K* kernel, std::atomic<uint64_t>& devices) {
   return e;
 }
 
+// log2 of the CTAs that share a tile's K: twice as many while the tiles leave CTA slots free and each part
+// keeps two blocks, up to 8.  Clusters of 8 leave SMs of a GPC over, so they may ask for three quarters of
+// the slots only (16 clusters of 8, one CTA per SM, ran in two waves: 128 x 2048 x 2048 11.4 us).
+int split_log2(int64_t tiles, int G, int64_t slots) {
+  int lg = 0;
+  while (lg < 3 && (tiles << (lg + 1)) <= (lg == 2 ? slots * 3 / 4 : slots) && (4 << lg) <= G) ++lg;
+  return lg;
+}
+
 template <int BT>
 cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, int64_t K, GemmArgs g, int num_sms,
                       cudaStream_t stream) {
   CUtensorMap tma, tmw;
   if (!make_map(&tma, a, K, g.M, lda, BT) || !make_map(&tmw, w, K, g.N, ldw, kBlk)) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)((g.N + kBlk - 1) / kBlk) * ((g.M + BT - 1) / BT);
-  // Split K over a cluster of S CTAs while the tiles leave CTA slots free (two per SM, which the
-  // shared memory below allows up to 64 tokens per tile) and each part keeps two blocks.  Clusters of 8
-  // leave SMs of a GPC over, so they may ask for three quarters of the slots only (16 clusters of 8,
-  // one CTA per SM, ran in two waves: 128 x 2048 x 2048 11.4 us).
-  const int64_t slots = (int64_t)num_sms * (BT == 128 ? 1 : 2);
-  int lg = 0;
-  while (lg < 3 && (tiles << (lg + 1)) <= (lg == 2 ? slots * 3 / 4 : slots) && (4 << lg) <= g.G) ++lg;
+  const int lg = split_log2(tiles, g.G, (int64_t)num_sms * (BT == 128 ? 1 : 2));   // two CTAs per SM up to 32 tokens
   const int S = 1 << lg;
   g.split_log2 = lg;
   const int nkb = (g.G + S - 1) / S;
@@ -906,14 +954,15 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
   g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
   // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 19 us
   // against 36 us, while at 256 x 8192 x 4096 (one wave) the clusters win (14.7 and 19.0 us).
-  // Tiles of 32 tokens pay while there are few of them, for more CTAs share the work (128 x 512 x 8192
-  // 6.8 us against 8.0 with 128 tokens, 500 x 128 x 4096 5.3 and 6.4); past half the SMs they lose
-  // (333 x 1000 x 1808 7.3 and 6.8 us).  Up to 16 tokens 16 columns suffice.
+  // Tiles of 32 tokens pay where those of 128, split over K, leave half the SMs idle (128 x 512 x 8192 6.8 us
+  // against 8.0 with 128 tokens, 500 x 128 x 4096 5.3 and 6.4); elsewhere they read the weights too often
+  // (333 x 1000 x 1808 7.3 and 6.8 us, 95 x 2816 x 6704 13.6 and 9.9).  Up to 16 tokens 16 columns suffice.
   const int64_t nt = (N + 127) / 128;
   cudaError_t e;
   if ((M + 127) / 128 * nt > num_sms) e = launch_pair(a, lda, w, ldw, K, g, num_sms, stream);
   else if (M <= 16) e = launch_bt<16>(a, lda, w, ldw, K, g, num_sms, stream);
-  else if (M <= 32 || (M + 31) / 32 * nt * 2 <= num_sms) e = launch_bt<32>(a, lda, w, ldw, K, g, num_sms, stream);
+  else if (M <= 32 || ((M + 127) / 128 * nt << split_log2((M + 127) / 128 * nt, g.G, num_sms)) * 2 < num_sms)
+    e = launch_bt<32>(a, lda, w, ldw, K, g, num_sms, stream);
   else e = launch_bt<128>(a, lda, w, ldw, K, g, num_sms, stream);
   note_launch();
   if (e != cudaSuccess) return e;

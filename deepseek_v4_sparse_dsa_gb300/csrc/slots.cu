@@ -67,16 +67,30 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
   bool bad = false;
   int64_t tok = 0, pg = 0;                               // running sums before this step's requests
   const int steps = (a.B + kSlotTile - 1) / kSlotTile;
+  int32_t n_next[kSlotPer], old_next[kSlotPer];          // the next step's lengths, in flight
+  auto fetch = [&](int c) {
+#pragma unroll
+    for (int i = 0; i < kSlotPer; ++i) {
+      const int b = c * kSlotTile + tid * kSlotPer + i;
+      n_next[i] = b < a.B ? __ldg(a.fresh + b) : 0;
+      old_next[i] = b < a.B ? __ldg(a.cached + b) : 0;
+    }
+  };
+  fetch(0);
   for (int c = 0; c < steps; ++c) {
     int32_t n[kSlotPer], old[kSlotPer], need[kSlotPer];
     int64_t ts = 0, ps = 0;
 #pragma unroll
     for (int i = 0; i < kSlotPer; ++i) {
+      n[i] = n_next[i];
+      old[i] = old_next[i];
+    }
+    if (c + 1 < steps) fetch(c + 1);
+#pragma unroll
+    for (int i = 0; i < kSlotPer; ++i) {
       const int b = c * kSlotTile + tid * kSlotPer + i;
-      n[i] = old[i] = need[i] = 0;
+      need[i] = 0;
       if (b < a.B) {
-        n[i] = __ldg(a.fresh + b);
-        old[i] = __ldg(a.cached + b);
         if (n[i] < 0 || old[i] < 0 || (int64_t)old[i] + n[i] > INT32_MAX) {
           bad = true;                                    // such a request brings nothing
           n[i] = 0;
