@@ -767,22 +767,31 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
             }
           }
         } else {
-          // rows at any alignment: the warp stores one row at a time, neighbouring words (a bf16 row that
-          // starts at 2 mod 4 has its first and last element apart)
+          // rows at any alignment: the warp stores one row at a time, neighbouring words; a bf16 row that
+          // starts at 2 mod 4 has its words shifted by one element, and its first and last element apart
           const int cols = min(128 / (int)sizeof(E), g.N - col0);
-          const auto at = [&](int r, int e) { return stage + r * 128 + (((e / kPer) ^ (r & 7)) << 4) + (e % kPer) * (int)sizeof(E); };
-#pragma unroll 4
-          for (int r = 0; r < rows; ++r) {
-            E* o = out + (int64_t)(m0 + r) * g.ldo + col0;
-            if constexpr (sizeof(E) == 4) {
-              if (lane < cols) o[lane] = *reinterpret_cast<const E*>(at(r, lane));
-            } else {
-              const int odd = (int)(reinterpret_cast<uintptr_t>(o) >> 1) & 1, e = 2 * lane + odd;
-              const uint32_t lo = e < 64 ? *reinterpret_cast<const uint16_t*>(at(r, e)) : 0u;
-              const uint32_t hi = e < 63 ? *reinterpret_cast<const uint16_t*>(at(r, e + 1)) : 0u;
-              if (e + 1 < cols) *reinterpret_cast<uint32_t*>(o + e) = lo | hi << 16;
-              else if (e < cols) o[e] = (E)lo;
-              if (odd && lane == 0 && cols > 0) o[0] = *reinterpret_cast<const uint16_t*>(at(r, 0));
+          constexpr int kFly = 8;
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += kFly) {
+            uint32_t w[kFly];
+#pragma unroll
+            for (int u = 0; u < kFly; ++u)
+              w[u] = *reinterpret_cast<const uint32_t*>(stage + (r0 + u) * 128 + (((lane >> 2) ^ ((r0 + u) & 7)) << 4) + 4 * (lane & 3));
+#pragma unroll
+            for (int u = 0; u < kFly; ++u) {
+              E* o = out + (int64_t)(m0 + r0 + u) * g.ldo + col0;
+              const bool live = r0 + u < rows;
+              if constexpr (sizeof(E) == 4) {
+                if (live && lane < cols) *reinterpret_cast<uint32_t*>(o + lane) = w[u];
+              } else {
+                const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[u], 1);
+                const int odd = (int)(reinterpret_cast<uintptr_t>(o) >> 1) & 1, e = 2 * lane + odd;
+                const uint32_t x = odd ? __funnelshift_r(w[u], next, 16) : w[u];
+                const bool whole = e + 1 < cols;
+                if (live && whole) *reinterpret_cast<uint32_t*>(o + e) = x;
+                if (live && !whole && e < cols) o[e] = (E)x;
+                if (live && odd && lane == 0 && cols > 0) o[0] = (E)w[u];
+              }
             }
           }
         }
