@@ -17,6 +17,7 @@
 #include <cudaTypedefs.h>
 
 #include <atomic>
+#include <cstring>
 #include <mutex>
 #include <type_traits>
 
@@ -44,6 +45,7 @@ struct GemmArgs {
   int split_log2;                            // log2 of the CTAs per tile (the cluster)
   int stages;
   int out_vec;                               // out and its rows are 16-byte aligned
+  int out_tma;                               // and end on 16 bytes (a bulk tensor store writes whole 16-byte words)
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -69,6 +71,14 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float4 v) {
 // arrivals before it touches a peer's shared memory.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// 2-D tiled store of a box in shared memory to (x = inner element, y = row), in the thread's bulk group.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
 
 __device__ __forceinline__ void tma_prefetch_l2_2d(const void* tmap, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(tmap)),
@@ -506,9 +516,9 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
 // epilogue warps (128 columns each).
 // The pairs walk the tiles in groups of 8 token tiles, so that the tiles in flight share rows.
 constexpr int kPairThreads = 384;             // warps 0..3: producer, two MMA issuers, forwarder; 4..11: epilogue
-constexpr int kPairStages = 6;               // even: block k and its accumulator k % 2 keep to stages of one parity
+constexpr int kPairStages = 5;
 constexpr uint32_t kPairStage = 32768u;      // 128 tokens and 128 weight rows of 128 bytes
-constexpr uint32_t kPairStaging = 8u * 4096u;   // a 32 x 128-byte block per epilogue warp
+constexpr uint32_t kPairStaging = 8u * 8192u;   // two blocks of 32 x 128 bytes per epilogue warp
 constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + kPairStaging + 64 * 8;
 
 // Arrives on a barrier of a CTA of the cluster, without the cluster-wide release that makes a thread wait
@@ -537,6 +547,7 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
 
 __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const __grid_constant__ CUtensorMap tma,
                                                                          const __grid_constant__ CUtensorMap tmw,
+                                                                         const __grid_constant__ CUtensorMap tmo,
                                                                          const GemmArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -597,8 +608,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
 
   // The epilogue's 128 sums, 64 columns in flight and their scales need more than the 168 registers
   // that 12 warps leave each thread: the first four warps hand theirs over
-  // (128 x 56 + 256 x 224 = 384 x 168).
-  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+  // (128 x 64 + 256 x 216 <= 384 x 168).
+  if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
   if (warp == 0) {
     // ================================ producer ================================
     if (lane == 0) {
@@ -690,11 +701,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
     __syncwarp();
   } else if (warp >= 4) {
     // ================================ epilogue ================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int half = (warp - 4) >> 2;                        // columns 128 half .. 128 half + 127
     const int quarter = warp & 3;                            // TMEM lanes 32 quarter ..
     const uint32_t tl = tmem + ((uint32_t)(32 * quarter) << 16) + 128u * (uint32_t)half;
-    uint8_t* stage = sm + kPairStages * kPairStage + (uint32_t)(warp - 4) * 4096u;
+    uint8_t* staging = sm + kPairStages * kPairStage + (uint32_t)(warp - 4) * 8192u;
     const uint32_t aempty0 = map_peer(aempty(0), 0u);
     bool ok = true;
     int b = 0;
@@ -739,38 +750,33 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
         if ((b ^= 1) == 0) ph ^= 1u;
       }
       if (!ok) break;
-      // rows of the warp's 32 tokens, 128 bytes of each at a time through its staging block:
-      // a thread writes its own row's pieces, then 8 lanes write one row's 128 bytes
+      // The warp's 32 tokens x 128 columns leave through its two staging blocks, 128 bytes of each row at a
+      // time: a thread writes its own row's pieces in the 128-byte swizzle, then one lane hands the block
+      // to a bulk tensor store (which leaves out what lies past M and N) and the warp goes on; or, where
+      // out's rows do not start and end on 16 bytes, the warp stores the rows itself.
       const int rows = g.M - m0 < 32 ? (int)(g.M - m0) : 32;
-      auto put = [&](auto* out, int col0, const uint4 (&v)[8]) {
+      auto put = [&](auto* out, int col0, int block, const uint4 (&v)[8]) {
         using E = typename std::remove_pointer<decltype(out)>::type;
-        constexpr int kPer = 16 / (int)sizeof(E);
+        uint8_t* stage = staging + 4096 * block;
+        if (g.out_tma) {                                     // the block's last store has been read
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+          __syncwarp();
+        }
 #pragma unroll
         for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = v[p];
-        __syncwarp();
-        if (g.out_vec) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = 4 * i + (lane >> 3), p = lane & 7;
-            const int col = col0 + kPer * p;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + ((p ^ (r & 7)) << 4));
-            if (r < rows && col < g.N) {
-              E* o = out + (int64_t)(m0 + r) * g.ldo + col;
-              if (col + kPer <= g.N) {
-                *reinterpret_cast<uint4*>(o) = w;
-              } else {
-                const E* we = reinterpret_cast<const E*>(&w);
-#pragma unroll
-                for (int e = 0; e < kPer; ++e)
-                  if (col + e < g.N) o[e] = we[e];
-              }
-            }
+        if (g.out_tma) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (rows > 0 && col0 < g.N) tma_store_2d(&tmo, smem_u32(stage), col0, m0);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         } else {
           // rows at any alignment: the warp stores one row at a time, neighbouring words; a bf16 row that
           // starts at 2 mod 4 has its words shifted by one element, and its first and last element apart
           const int cols = min(128 / (int)sizeof(E), g.N - col0);
           constexpr int kFly = 8;
+          __syncwarp();
 #pragma unroll 1
           for (int r0 = 0; r0 < rows; r0 += kFly) {
             uint32_t w[kFly];
@@ -794,8 +800,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
               }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
       };
       if (g.out_f32) {
 #pragma unroll
@@ -805,7 +811,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
           for (int p = 0; p < 8; ++p)
             v[p] = make_uint4(__float_as_uint(acc[32 * q + 4 * p]), __float_as_uint(acc[32 * q + 4 * p + 1]),
                               __float_as_uint(acc[32 * q + 4 * p + 2]), __float_as_uint(acc[32 * q + 4 * p + 3]));
-          put(static_cast<float*>(g.out), n0 + 32 * q, v);
+          put(static_cast<float*>(g.out), n0 + 32 * q, q & 1, v);
         }
       } else {
 #pragma unroll
@@ -821,10 +827,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
             }
             v[p] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          put(static_cast<uint16_t*>(g.out), n0 + 64 * q, v);
+          put(static_cast<uint16_t*>(g.out), n0 + 64 * q, q, v);
         }
       }
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
     if (!ok && lane == 0) {
       raise_error(DSA_DEVERR_TIMEOUT);
       *abort_flag = 1;
@@ -863,6 +871,20 @@ bool make_map(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The result in boxes of 32 rows x 128 bytes, in the 128-byte swizzle.
+bool make_out_map(CUtensorMap* m, const GemmArgs& g) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint32_t es = g.out_f32 ? 4u : 2u;
+  const cuuint64_t dims[2] = {(cuuint64_t)g.N, (cuuint64_t)g.M};
+  const cuuint64_t strides[1] = {(cuuint64_t)g.ldo * es};
+  const cuuint32_t box[2] = {128u / es, 32u};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, g.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, g.out, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -928,8 +950,13 @@ cudaError_t launch_bt(const void* a, int64_t lda, const void* w, int64_t ldw, in
 
 cudaError_t launch_pair(const void* a, int64_t lda, const void* w, int64_t ldw, int64_t K, const GemmArgs& g,
                         int num_sms, cudaStream_t stream) {
-  CUtensorMap tma, tmw;
+  CUtensorMap tma, tmw, tmo;
   if (!make_map(&tma, a, K, g.M, lda, 128) || !make_map(&tmw, w, K, g.N, ldw, 128)) return cudaErrorInvalidValue;
+  if (!g.out_tma) {
+    memset(&tmo, 0, sizeof(tmo));                            // rows are stored without it
+  } else if (!make_out_map(&tmo, g)) {
+    return cudaErrorInvalidValue;
+  }
   static std::atomic<uint64_t> devices{0};
   const cudaError_t e = allow_smem(gemm_e4m3_pair_kernel, devices);
   if (e != cudaSuccess) return e;
@@ -949,7 +976,7 @@ cudaError_t launch_pair(const void* a, int64_t lda, const void* w, int64_t ldw, 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gemm_e4m3_pair_kernel, tma, tmw, g);
+  return cudaLaunchKernelEx(&cfg, gemm_e4m3_pair_kernel, tma, tmw, tmo, g);
 }
 
 }  // namespace
@@ -958,9 +985,10 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
                              const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, bool out_f32,
                              int num_sms, cudaStream_t stream) {
   if (M <= 0 || N <= 0) return cudaSuccess;
-  GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 0, 2, 0};
+  GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 0, 2, 0, 0};
   const int64_t es = out_f32 ? 4 : 2;
   g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
+  g.out_tma = g.out_vec && N * es % 16 == 0 && ldo * es < (int64_t)1 << 40 ? 1 : 0;
   // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 19 us
   // against 36 us, while at 256 x 8192 x 4096 (one wave) the clusters win (14.7 and 19.0 us).
   // Tiles of 32 tokens pay where those of 128, split over K, leave half the SMs idle (128 x 512 x 8192 6.8 us
