@@ -34,12 +34,20 @@ struct SlotArgs {
   int64_t* slot;
   int32_t* pos;
   int32_t* used;
+  uint32_t mul, shift;          // division by bs (div_page)
 };
 
 __device__ __forceinline__ int32_t clamp_i32(int64_t v) { return v > INT32_MAX ? INT32_MAX : (int32_t)v; }
 
-// Pages that hold n tokens (n and bs below 2^31, so their sum fits 32 bits unsigned).
-__device__ __forceinline__ int pages(int n, int bs) { return (int)(((uint32_t)n + (uint32_t)bs - 1u) / (uint32_t)bs); }
+// Division of 0 <= n < 2^31 by the page size as a product and a shift (division by an invariant integer,
+// Granlund and Montgomery): with 2^(s-1) < bs <= 2^s and mul = ceil(2^(31 + s) / bs) <= 2^32 - 1 for
+// bs > 1, n mul / 2^(31 + s) exceeds n / bs by less than n / 2^31 < 1 / bs, so its floor is n / bs.
+__device__ __forceinline__ int div_page(const SlotArgs& a, int n) {
+  return a.bs == 1 ? n : (int)(((uint64_t)(uint32_t)n * a.mul) >> a.shift);
+}
+
+// Pages that hold n tokens.
+__device__ __forceinline__ int pages(const SlotArgs& a, int n) { return n > 0 ? div_page(a, n - 1) + 1 : 0; }
 
 __device__ __forceinline__ int64_t warp_incl_sum(int64_t v, int lane) {
 #pragma unroll
@@ -96,7 +104,7 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
           n[i] = 0;
           old[i] = old[i] < 0 ? 0 : old[i];
         }
-        need[i] = pages(old[i] + n[i], a.bs) - pages(old[i], a.bs);
+        need[i] = pages(a, old[i] + n[i]) - pages(a, old[i]);
       }
       ts += n[i];
       ps += need[i];
@@ -165,35 +173,45 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
 #pragma unroll
   for (int i = 0; i < kSlotPer; ++i) s_head[tid * kSlotPer + i] = max(before, h[i]);
   __syncthreads();
+  // each token's position and where its block id stands; then all block ids, then all results
+  const int32_t* from[kSlotPer];
+  int32_t* entry[kSlotPer];
+  int32_t pos[kSlotPer], off[kSlotPer];
+#pragma unroll
+  for (int i = 0; i < kSlotPer; ++i) {
+    const int64_t t = t0 + i * kSlotThreads + tid;
+    from[i] = nullptr;
+    entry[i] = nullptr;
+    pos[i] = off[i] = 0;
+    if (t < t1 && t < tok) {
+      const int p = s_head[i * kSlotThreads + tid];
+      const int old = s_old[p];
+      pos[i] = old + (int32_t)(t - s_start[p]);
+      const int page = div_page(a, pos[i]), have = pages(a, old);
+      off[i] = pos[i] - page * a.bs;
+      if (page < a.bt_stride) {
+        int32_t* e = a.table + (int64_t)s_b[p] * a.bt_stride + page;
+        const int64_t f = s_first[p] + (page - have);
+        if (page < have) from[i] = e;
+        else if (f < a.n_free) from[i] = a.free_blocks + f;
+        if (page >= have && off[i] == 0) entry[i] = e;
+      }
+    }
+  }
+  int32_t blk[kSlotPer];
+#pragma unroll
+  for (int i = 0; i < kSlotPer; ++i) blk[i] = from[i] != nullptr ? *from[i] : -1;
 #pragma unroll
   for (int i = 0; i < kSlotPer; ++i) {
     const int64_t t = t0 + i * kSlotThreads + tid;
     if (t >= t1) continue;
-    int64_t row = -1;
-    int32_t pos = 0;
-    if (t < tok) {
-      const int p = s_head[i * kSlotThreads + tid];
-      const int b = s_b[p], old = s_old[p];
-      pos = old + (int32_t)(t - s_start[p]);
-      const int page = pos / a.bs, off = pos - page * a.bs;
-      const int have = pages(old, a.bs);
-      int32_t blk = -1;
-      if (page < a.bt_stride) {
-        int32_t* entry = a.table + (int64_t)b * a.bt_stride + page;
-        if (page < have) {
-          blk = *entry;
-        } else {
-          const int64_t f = s_first[p] + (page - have);
-          if (f < a.n_free) blk = __ldg(a.free_blocks + f);
-        }
-        if (blk < 0 || blk >= a.num_blocks) blk = -1;
-        if (page >= have && off == 0) *entry = blk;
-      }
-      if (blk >= 0) row = (int64_t)blk * a.bs + off;
-      else bad = true;
+    if (blk[i] < 0 || blk[i] >= a.num_blocks) {
+      blk[i] = -1;
+      if (t < tok) bad = true;
     }
-    a.slot[t] = row;
-    a.pos[t] = pos;
+    if (entry[i] != nullptr) *entry[i] = blk[i];
+    a.slot[t] = blk[i] >= 0 ? (int64_t)blk[i] * a.bs + off[i] : -1;
+    a.pos[t] = pos[i];
   }
   if (bad) raise_error(DSA_DEVERR_INDEX);
 }
@@ -206,7 +224,11 @@ cudaError_t launch_assign_slots(const int32_t* cached, const int32_t* fresh, int
                                 cudaStream_t stream) {
   const int64_t tiles = (max_tokens + kSlotTile - 1) / kSlotTile;
   SlotArgs a{cached, fresh, B, bs, free_blocks, n_free, num_blocks, table, bt_stride, max_tokens,
-             context, start, slot, pos, used};
+             context, start, slot, pos, used, 0, 0};
+  uint32_t s = 0;
+  while ((uint64_t(1) << s) < (uint64_t)bs) ++s;
+  a.shift = 31 + s;
+  a.mul = bs == 1 ? 0u : (uint32_t)(((uint64_t(1) << a.shift) + (uint64_t)bs - 1) / (uint64_t)bs);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tiles > 0 ? tiles : 1));
   cfg.blockDim = dim3(kSlotThreads);
