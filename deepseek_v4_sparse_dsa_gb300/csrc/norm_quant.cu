@@ -132,6 +132,12 @@ __device__ __forceinline__ float next_pow2_f32(float s) {
   return (u & 0x7FFFFFu) == 0u ? s : __uint_as_float((u & 0x7F800000u) + 0x800000u);
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // VPT pieces of 8 elements per thread: piece j of thread t of a row is j * tpr + t.  A CTA walks the rows
 // with a stride of the grid; in 16-byte accesses with one or two pieces the next row's loads are in flight
 // while this one is worked on, and gamma stays in registers.  Four pieces leave no room for either, and
@@ -139,12 +145,14 @@ __device__ __forceinline__ float next_pow2_f32(float s) {
 // 45 us so).  bf16 rows are held to 64 registers (8192 x 7168: 88 -> 76 us), fp32 rows lose by that
 // (4096 x 4096: 35 -> 43 us).
 template <typename T, int VPT, bool VEC>
-__global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2) && VPT < 4 ? 2 : 1) add_rmsnorm_e4m3_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2) && VPT < 4 ? 2 : 1)
+    add_rmsnorm_e4m3_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   __shared__ float s_sum[2][32];
-  const int rpc = blockDim.x / a.tpr;                  // rows per CTA
-  const int sub = threadIdx.x / a.tpr;
-  const int t = threadIdx.x - sub * a.tpr;
+  const int tpr = a.tpr;
+  const int rpc = blockDim.x / tpr;                    // rows per CTA
+  const int sub = threadIdx.x / tpr;
+  const int t = threadIdx.x - sub * tpr;
   const int groups = (a.D + 127) >> 7;
   const int64_t step = (int64_t)gridDim.x * rpc;
   int64_t row = (int64_t)blockIdx.x * rpc + sub;
@@ -157,7 +165,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
   auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int v = j * a.tpr + t, D = r < a.T ? a.D : 0;    // nothing past the last row
+      const int v = j * tpr + t, D = r < a.T ? a.D : 0;    // nothing past the last row
       x[j].load(static_cast<const T*>(a.x) + r * a.ldx, v, D);
       if (kAhead && a.res != nullptr) res[j].load(static_cast<const T*>(a.res) + r * a.ldr, v, D);
     }
@@ -166,7 +174,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
   if constexpr (kAhead) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      gm[j].load(a.gamma, j * a.tpr + t, a.D);
+      gm[j].load(a.gamma, j * tpr + t, a.D);
     }
   }
   for (int it = 0; row - sub < a.T; row += step, it ^= 1) {
@@ -177,10 +185,10 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
     for (int j = 0; j < VPT; ++j) {
       if (a.res != nullptr) {
         if constexpr (!kAhead)
-          res[0].load(static_cast<const T*>(a.res) + row * a.ldr, j * a.tpr + t, live ? a.D : 0);
+          res[0].load(static_cast<const T*>(a.res) + row * a.ldr, j * tpr + t, live ? a.D : 0);
         x[j].add(res[kAhead ? j : 0]);
       }
-      if (a.res_out != nullptr && live) x[j].store(static_cast<T*>(a.res_out) + row * a.ldr, j * a.tpr + t, a.D);
+      if (a.res_out != nullptr && live) x[j].store(static_cast<T*>(a.res_out) + row * a.ldr, j * tpr + t, a.D);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         r[j][i] = x[j].get(i);
@@ -190,17 +198,17 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
     if (kAhead && row + step - sub < a.T) fetch(row + step);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-    if (a.tpr > 32) {                                  // the row's warps, summed in their order
+    if (tpr > 32) {                                    // the row's warps, summed in their order
       if ((threadIdx.x & 31) == 0) s_sum[it][threadIdx.x >> 5] = ss;
       __syncthreads();                                 // the other half is free: all have passed the last one
-      const int w0 = (sub * a.tpr) >> 5, nw = a.tpr >> 5;
+      const int w0 = (sub * tpr) >> 5, nw = tpr >> 5;
       ss = 0.f;
       for (int w = 0; w < nw; ++w) ss += s_sum[it][w0 + w];
     }
     const float rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int v = j * a.tpr + t;
+      const int v = j * tpr + t;
       if constexpr (!kAhead) {
         gm[0].load(a.gamma, v, a.D);
       }
@@ -225,15 +233,17 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
         // scale = amax |y| / 448; code = E4M3(y / scale) with y / scale = (r gamma) (448 / amax |r gamma|),
         // one rounding less than by way of y.  The factor is NaN with rstd.
         constexpr float kMin = 1.17549435e-38f;
-        float s = 1.f, f = 0.f;
-        if (amax > 0.f) {
-          s = __fmul_rn(__fmul_rn(amax, rstd), 1.f / 448.f);
-          f = __fdiv_rn(448.f, amax);
-          if (s < kMin || a.pow2) {
-            if (s < kMin) s = kMin;
-            if (a.pow2) s = next_pow2_f32(s);
-            f = __fmul_rn(rstd, __fdiv_rn(1.f, s));
-          }
+        float s = __fmul_rn(__fmul_rn(amax, rstd), 1.f / 448.f), f;
+        if (amax >= 1e-30f && amax <= 1e30f && !(s < kMin) && !a.pow2) {
+          const float r0 = rcp_approx(amax);           // and one Newton step: 1 ulp
+          f = __fmul_rn(448.f, fmaf(fmaf(-amax, r0, 1.f), r0, r0));
+        } else if (amax > 0.f) {
+          if (s < kMin) s = kMin;
+          if (a.pow2) s = next_pow2_f32(s);
+          f = amax < INFINITY ? __fmul_rn(rstd, __fdiv_rn(1.f, s)) : 0.f;   // an infinity times 0 is a NaN code
+        } else {
+          s = 1.f;
+          f = 0.f;
         }
         f = fmaf(0.f, rstd, f);
         if ((v & 15) == 0 && (v >> 4) < groups) a.scale[row * groups + (v >> 4)] = s;
@@ -290,10 +300,11 @@ template <typename T, bool VEC>
 cudaError_t launch_norm_v(NormArgs a, int num_sms, cudaStream_t stream) {
   // Pieces of 8 elements, whole groups of 16.  A row takes as many threads as it has pieces, or half or a
   // quarter as many: with two pieces a thread there is more in flight per thread and a batch of many
-  // rows streams better; few rows are quickest with one piece a thread.
+  // rows streams better, unless one warp holds the row anyway (16384 x 128: 7.4 us with two, 4.4 with one);
+  // few rows are quickest with one piece a thread.
   const int pieces = (a.D + 127) / 128 * 16;
   int vpt = pieces <= 512 ? 1 : (pieces <= 1024 ? 2 : 4);
-  if (vpt == 1 && a.T > 2 * (int64_t)num_sms) vpt = 2;
+  if (vpt == 1 && pieces > 32 && a.T > 2 * (int64_t)num_sms) vpt = 2;
   a.tpr = ((pieces + vpt - 1) / vpt + 31) / 32 * 32;
   const int rpc = a.tpr >= 256 ? 1 : 256 / a.tpr;
   if (vpt == 1) return launch_norm<T, 1, VEC>(a, a.tpr * rpc, rpc, num_sms, stream);
