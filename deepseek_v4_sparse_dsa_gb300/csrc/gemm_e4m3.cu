@@ -3,16 +3,19 @@
 //
 //   out[m, n] = sum_kb sa[m, kb] sw[n / 128, kb] sum_{k in block kb} a[m, k] w[n, k]
 //
-// Each block of 128 along K is one tcgen05 product into its own TMEM accumulator; the
-// epilogue warps multiply it by its two scales and add it to fp32 registers while the next
-// block's product runs.
+// Each block of 128 along K is one tcgen05 product into its own TMEM accumulator; the epilogue warps
+// multiply it by its two scales and add it to fp32 registers while the next block's product runs (the
+// scales are any fp32 values, so they cannot ride along in the block-scaled MMA).
 //
-// Few tokens: a tile is 128 weight rows (one weight scale per tile and block) and BT tokens; up to 64
-// tokens the weight rows are the MMA's M and the tokens its N, so a decode batch of a few tokens pads
-// to 16 columns instead of 128 rows.  A cluster of S CTAs
-// shares a tile, each with its part of K; the parts are added in the order of K through
-// distributed shared memory, so that a product with few tiles still streams its weights on
-// every SM, and the result does not depend on timing.
+// Few tokens are bound by the weights' stream from memory, many by the tensor cores and, at full rate, by
+// the board's power; what lies between, by the fixed costs of a launch.  Two kernels:
+//  * gemm_e4m3_kernel: tiles of 128 weight rows x 16, 32 or 128 tokens.  A cluster of up to 8 CTAs shares a
+//    tile, each with its part of K, so that a product with few tiles still streams its weights on every
+//    SM; the parts are added in the order of K through distributed shared memory, so the result does
+//    not depend on timing and there is no workspace.
+//  * gemm_e4m3_pair_kernel: tiles of 256 x 256 on persistent CTA pairs (cta_group::2).
+// Measured: 1 x 8192 x 2048 5.4 us (weights in L2; 5.9 from memory), 64 x 8192 x 4096 9.4 us, 8192 x 64 x
+// 4096 10.3 us, 8192 x 8192 x 4096 212 us = 2.6 PFLOP/s.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -67,8 +70,9 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float4 v) {
                : "memory");
 }
 
-// Half of a cluster barrier each: every thread arrives when it starts, and waits for the others'
-// arrivals before it touches a peer's shared memory.
+// Half of a cluster barrier each.  A thread's arrival says that its CTA runs, or that products and copies
+// which it has seen complete are done with memory that the peers will write; no generic write is
+// announced, so it is relaxed.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
@@ -154,7 +158,7 @@ __device__ __forceinline__ void store_out4(const GemmArgs& g, int64_t m, int n, 
 }
 
 // Shapes of the kernel with BT tokens per tile.  Four epilogue warps (one per TMEM lane quarter) take
-// up to 64 columns; 128 columns are shared by eight.
+// up to 32 columns; 128 columns are shared by eight.
 template <int BT>
 struct FewShape {
   static constexpr int kEpi = BT == 128 ? 256 : 128;         // epilogue threads
@@ -162,11 +166,12 @@ struct FewShape {
   static constexpr int kEpi0 = BT == 128 ? 128 : 64;         // first epilogue thread
   static constexpr int kThreads = kEpi0 + kEpi;
   static constexpr int kCols = BT == 128 ? 64 : BT;          // columns per epilogue warp
-  // Up to 64 tokens the weight rows are the MMA's M, and an epilogue thread holds one weight row of
-  // every token: its factors, one per token and block, are read from shared memory.  Reading 128 of them
-  // takes the SM's shared-memory bandwidth longer than a block's products (256 x 8192 x 4096: 17.7 us,
-  // 515 of 940 cycles per block), so with 128 tokens these are the M and the weight rows the N: a thread
-  // holds one token, and one factor per block.
+  // Up to 32 tokens the weight rows are the MMA's M and the tokens its N (a few tokens pad to 16 columns, not
+  // to 128 rows), and an epilogue thread holds one weight row of every token: its factors, one per
+  // token and block, are read from shared memory.  Reading 128 of them takes the SM's shared-memory
+  // bandwidth longer than a block's products (515 of 940 cycles per block at 256 x 8192 x 4096, 17.7 us
+  // against 14.7), so with 128 tokens these are the M and the weight rows the N: a thread holds one token,
+  // and one factor per block.  64 tokens per tile, either way, won nowhere.
   static constexpr bool kTok = BT == 128;
   static constexpr int kBufs = 4;                            // TMEM accumulators
   static constexpr uint32_t kTmem = BT * kBufs;              // 64 to 512 columns
@@ -185,9 +190,8 @@ struct FewShape {
 // Shared memory, from a 1024-byte aligned base: the stages, the sums that the CTA adds up, the staged
 // scales [2][kScaleChunk][BT], the barriers and flags.
 template <int BT>
-__global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tma,
-                                                                           const __grid_constant__ CUtensorMap tmw,
-                                                                           const GemmArgs g) {
+__global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
+    gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmw, const GemmArgs g) {
   using Sh = FewShape<BT>;
   constexpr uint32_t kStage = Sh::kStage;
   constexpr int kBufs = Sh::kBufs, kEpi = Sh::kEpi, kCols = Sh::kCols;
@@ -239,9 +243,8 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
   const uint32_t tmem = (uint32_t)flags[1];
   grid_launch_dependents();                                  // TMEM is held: the next kernel's set-up may begin
   // While the kernel before this one ends, the weights are brought into L2 (only there: what that
-  // kernel may still write to them is seen by the loads behind the wait).  1 x 8192 x 2048 6.3 -> 5.7 us;
-  // from 64 tokens on the weights are read by more than one CTA or the loads have other company, and
-  // it costs up to 10 %.
+  // kernel may still write to them is seen by the loads behind the wait).  1 x 8192 x 2048 6.3 -> 5.7 us; with
+  // 128 tokens it costs up to 10 %.
   if (BT <= 32 && warp == 0 && lane < nkb) tma_prefetch_l2_2d(&tmw, (kb0 + lane) * kBlk, nt * kBlk);
   grid_dependency_wait();
 
@@ -511,10 +514,11 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT <= 64 ? 2 : 1) gemm
 // K), the pair's tensor cores read both, and each CTA's TMEM receives its 128 tokens x 256
 // columns.  Tokens are the MMA's M here, so an epilogue thread owns one token: one activation
 // scale per block.  Two accumulators of 256 columns fill TMEM: the epilogue adds block kb to its
-// registers while block kb + 1 runs.  Warps: producer, two MMA
-// issuers (the even CTA's), one that tells the even CTA that this CTA's copies have landed, eight
-// epilogue warps (128 columns each).
+// registers while block kb + 1 runs.  Warps: producer, two MMA issuers (the even CTA's), one that
+// tells the even CTA that this CTA's copies have landed, eight epilogue warps (128 columns each).
 // The pairs walk the tiles in groups of 8 token tiles, so that the tiles in flight share rows.
+// Bound by power: at 2.7 PFLOP/s (16384 x 8192 x 8192) the board draws 1.38 of its 1.4 kW.  Without the sums
+// the products alone reach 3.1 PFLOP/s.
 constexpr int kPairThreads = 384;             // warps 0..3: producer, two MMA issuers, forwarder; 4..11: epilogue
 constexpr int kPairStages = 5;
 constexpr uint32_t kPairStage = 32768u;      // 128 tokens and 128 weight rows of 128 bytes
@@ -522,7 +526,7 @@ constexpr uint32_t kPairStaging = 8u * 8192u;   // two blocks of 32 x 128 bytes 
 constexpr size_t kPairSmem = 1024 + kPairStages * kPairStage + kPairStaging + 64 * 8;
 
 // Arrives on a barrier of a CTA of the cluster, without the cluster-wide release that makes a thread wait
-// for all its memory operations (it took 8192 x 8192 x 4096 from 256 to 508 us).  What it announces is no
+// for all its memory operations (with it 8192 x 8192 x 4096 took 508 us, without 280).  What it announces is no
 // generic write: TMEM reads whose values are in registers, or copies that the thread's own barrier has
 // seen land in its CTA's shared memory, which that CTA's tensor core reads.
 __device__ __forceinline__ void arrive_cluster(uint32_t addr) {
@@ -989,7 +993,7 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
   const int64_t es = out_f32 ? 4 : 2;
   g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
   g.out_tma = g.out_vec && N * es % 16 == 0 && ldo * es < (int64_t)1 << 40 ? 1 : 0;
-  // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 19 us
+  // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 20 us
   // against 36 us, while at 256 x 8192 x 4096 (one wave) the clusters win (14.7 and 19.0 us).
   // Tiles of 32 tokens pay where those of 128, split over K, leave half the SMs idle (128 x 512 x 8192 6.8 us
   // against 8.0 with 128 tokens, 500 x 128 x 4096 5.3 and 6.4); elsewhere they read the weights too often
