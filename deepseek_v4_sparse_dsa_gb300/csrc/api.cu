@@ -261,6 +261,8 @@ dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual
   if (residual_out == x && ldr != ldx) return DSA_ERR_INVALID_ARG;
   if (y == x && ldy != ldx) return DSA_ERR_INVALID_ARG;
   if (y != nullptr && (y == residual || y == residual_out)) return DSA_ERR_INVALID_ARG;
+  if (y_fp8 != nullptr && (y_fp8 == x || y_fp8 == residual || y_fp8 == residual_out || y_fp8 == y))
+    return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_add_rmsnorm_e4m3(x, ldx, residual, ldr, gamma, eps, T, D, type == DSA_REAL_F32,
                                              residual_out, y, y_fp8, ldy, y_scale, pow2_scale != 0, device_sm_count(),
                                              static_cast<cudaStream_t>(stream)));
@@ -278,6 +280,7 @@ dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, co
   if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)
     return DSA_ERR_INVALID_ARG;
   if (lda < K || ldw < K || ldo < N || lda % 16 != 0 || ldw % 16 != 0) return DSA_ERR_INVALID_ARG;
+  if (out == a || out == w || out == a_scale || out == w_scale) return DSA_ERR_INVALID_ARG;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
       !aligned(out, out_type == DSA_REAL_F32 ? 4 : 2))
     return DSA_ERR_INVALID_ARG;

@@ -431,6 +431,40 @@ def test_gemm_other_stream_and_graph():
         assert torch.equal(out, gemm_call(a2, asc2, w, wsc, K, F32))
 
 
+@pytest.mark.parametrize("M,N", [(5, 300), (100, 900), (2100, 2300)])
+def test_calls_behind_copies_and_other_kernels_in_a_graph(M, N):
+    # a captured chain copy -> norm -> product -> norm of the product: each starts early behind a kernel, and
+    # whole behind a copy; replayed on new inputs it gives what the eager calls give
+    K = 512
+    a, asc, w, wsc = gemm_inputs(8, N, K)
+    dw, dws, g, g2 = dev(w), dev(wsc), torch.rand(K, device="cuda") + 0.5, torch.rand(N, device="cuda") + 0.5
+    e = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    src, x = e(M, K, t=torch.bfloat16), e(M, K, t=torch.bfloat16)
+    codes, scale, out, y = e(M, K, t=torch.uint8), e(M, K // 128), e(M, N), e(M, N)
+
+    def chain():
+        x.copy_(src)
+        dsa.dsa_add_rmsnorm_e4m3(x, K, None, 0, g, 1e-6, M, K, BF16, None, None, codes, K, scale)
+        dsa.dsa_gemm_e4m3(codes, K, scale, dw, K, dws, M, N, K, out, N, F32)
+        dsa.dsa_add_rmsnorm_e4m3(out, N, None, 0, g2, 1e-6, M, N, F32, None, y, None, N, None)
+        dsa.dsa_gemm_e4m3(codes, K, scale, dw, K, dws, M, N, K, out, N, F32)
+    src.normal_()
+    chain()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            chain()
+    for _ in range(4):
+        src.normal_()
+        chain()
+        want = (codes.clone(), scale.clone(), out.clone(), y.clone())
+        for t in (codes, scale, out, y):
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip(want, (codes, scale, out, y)))
+    assert dsa.dsa_device_error() == 0
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 256, 4096), (200, 300, 2048), (2000, 2000, 1024)])
 def test_gemm_expired_waits_flag_timeout(M, N, K):
     a, asc, w, wsc = gemm_inputs(M, N, K)

@@ -47,7 +47,7 @@ def norm(x=_p(1), ldx=256, res=_p(2), ldr=256, gamma=_p(3), eps=1e-6, T=4, D=256
     (dict(codes=None), INVALID), (dict(ro=None, y=None, codes=None, scale=None), INVALID), (dict(x=_p(1) + 1), INVALID),
     (dict(typ=dsa.DSA_REAL_F32, x=_p(1) + 2), INVALID), (dict(scale=_p(7) + 2), INVALID),
     (dict(ro=_p(1), ldx=264), INVALID), (dict(y=_p(1), ldx=264), INVALID), (dict(y=_p(2)), INVALID),
-    (dict(y=_p(4)), INVALID),
+    (dict(y=_p(4)), INVALID), (dict(codes=_p(1)), INVALID), (dict(codes=_p(2)), INVALID), (dict(codes=_p(5)), INVALID),
 ])
 def test_add_rmsnorm_refusals(lib, bad, status):  # noqa: F811
     before = dsa.dsa_launch_count()
@@ -66,7 +66,7 @@ def gemm(a=_p(1), lda=256, asc=_p(2), w=_p(3), ldw=256, wsc=_p(4), M=4, N=128, K
     (dict(wsc=None), INVALID), (dict(out=None), INVALID), (dict(lda=240), INVALID), (dict(ldw=240), INVALID),
     (dict(lda=264), INVALID), (dict(ldw=264), INVALID), (dict(ldo=127), INVALID), (dict(a=_p(1) + 8), INVALID),
     (dict(w=_p(3) + 8), INVALID), (dict(out=_p(5) + 1), INVALID), (dict(out=_p(5) + 2, typ=dsa.DSA_REAL_F32), INVALID),
-    (dict(asc=_p(2) + 1), INVALID), (dict(lda=1 << 40), UNSUPPORTED), (dict(ldw=1 << 40), UNSUPPORTED),
+    (dict(asc=_p(2) + 1), INVALID), (dict(out=_p(1)), INVALID), (dict(out=_p(3)), INVALID), (dict(lda=1 << 40), UNSUPPORTED), (dict(ldw=1 << 40), UNSUPPORTED),
     (dict(M=2**31 - 300, N=2**31 - 300, ldo=2**31), UNSUPPORTED),
 ])
 def test_gemm_refusals(lib, bad, status):  # noqa: F811
