@@ -143,9 +143,10 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // VPT pieces of 8 elements per thread: piece j of thread t of a row is j * tpr + t.  A CTA walks the rows
 // with a stride of the grid; in 16-byte accesses with one or two pieces the next row's loads are in flight
-// while this one is worked on, and gamma stays in registers.  Four pieces leave no room for either, and
-// element-wise accesses need the registers for more warps (4096 x 4097 bf16: 79 us with one CTA an SM,
-// 45 us so).  bf16 rows are held to 64 registers (8192 x 7168: 88 -> 76 us), fp32 rows lose by that
+// while this one is worked on, and gamma stays in registers.  Four pieces leave no room for either.
+// Element-wise accesses need the registers for more warps (4096 x 4097 bf16: 79 us with the next row in
+// flight, 38 us without); gamma and the residual are loaded with x where they fit (bf16; fp32 517 x 4999
+// 6.2 us without, 7.9 us with).  bf16 rows are held to 64 registers (8192 x 7168: 88 -> 76 us), fp32 rows lose by that
 // (4096 x 4096: 35 -> 43 us).
 template <typename T, int VPT, bool VEC>
 __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2) && VPT < 4 ? 2 : 1)
@@ -162,19 +163,19 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
   grid_launch_dependents();
   grid_dependency_wait();
   constexpr bool kAhead = VEC && VPT <= 2;
-  constexpr int kHeld = kAhead ? VPT : 1;
-  Piece<float, VEC> gm[kHeld];
-  P x[VPT], res[kHeld];
+  constexpr bool kAll = VPT <= 2 && (VEC || sizeof(T) == 2);   // gamma and the residual's pieces are held too
+  Piece<float, VEC> gm[kAll ? VPT : 1];
+  P x[VPT], res[kAll ? VPT : 1];
   auto fetch = [&](int64_t r) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = j * tpr + t, D = r < a.T ? a.D : 0;    // nothing past the last row
       x[j].load(static_cast<const T*>(a.x) + r * a.ldx, v, D);
-      if (kAhead && a.res != nullptr) res[j].load(static_cast<const T*>(a.res) + r * a.ldr, v, D);
+      if (kAll && a.res != nullptr) res[j].load(static_cast<const T*>(a.res) + r * a.ldr, v, D);
     }
   };
   fetch(row);
-  if constexpr (kAhead) {
+  if constexpr (kAll) {
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       gm[j].load(a.gamma, j * tpr + t, a.D);
@@ -187,9 +188,9 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (a.res != nullptr) {
-        if constexpr (!kAhead)
+        if constexpr (!kAll)
           res[0].load(static_cast<const T*>(a.res) + row * a.ldr, j * tpr + t, live ? a.D : 0);
-        x[j].add(res[kAhead ? j : 0]);
+        x[j].add(res[kAll ? j : 0]);
       }
       if (a.res_out != nullptr && live) x[j].store(static_cast<T*>(a.res_out) + row * a.ldr, j * tpr + t, a.D);
 #pragma unroll
@@ -212,13 +213,13 @@ __global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int v = j * tpr + t;
-      if constexpr (!kAhead) {
+      if constexpr (!kAll) {
         gm[0].load(a.gamma, v, a.D);
       }
       float amax = 0.f;                                // of r * gamma: the row's 1 / rms is a common factor
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        r[j][i] = __fmul_rn(r[j][i], gm[kAhead ? j : 0].get(i));
+        r[j][i] = __fmul_rn(r[j][i], gm[kAll ? j : 0].get(i));
         amax = fmaxf(amax, fabsf(r[j][i]));
       }
 #pragma unroll
