@@ -51,6 +51,11 @@ struct GemmArgs {
   int out_tma;                               // and end on 16 bytes (a bulk tensor store writes whole 16-byte words)
 };
 
+// The wait limit as the host has set it (0: the default); the value is needed only behind the set-up.
+__device__ __forceinline__ unsigned long long wait_limit_word() {
+  return *(volatile unsigned long long*)&g_wait_limit_ns;
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -193,6 +198,7 @@ template <int BT>
 __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
     gemm_e4m3_kernel(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmw, const GemmArgs g) {
   using Sh = FewShape<BT>;
+  const unsigned long long set_limit = wait_limit_word();    // on its way during the set-up
   constexpr uint32_t kStage = Sh::kStage;
   constexpr int kBufs = Sh::kBufs, kEpi = Sh::kEpi, kCols = Sh::kCols;
   extern __shared__ uint8_t smem_raw[];
@@ -219,21 +225,16 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
   const int mv = g.M - m0 < BT ? (int)(g.M - m0) : BT;       // tokens of this tile
   const int kb0 = (int)((int64_t)g.G * rank / S);
   const int nkb = (int)((int64_t)g.G * (rank + 1) / S) - kb0;
-  const unsigned long long limit = wait_limit_ns();
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+  if (warp == 0) {                                           // a barrier per lane: 2 * kMaxStages + 8 of them
+    static_assert(2 * kMaxStages + 2 * kBufs == 32, "a barrier per lane");
+    mbar_init(bars + 8u * (uint32_t)lane, lane < 32 - kBufs ? 1u : (uint32_t)(kEpi / 32));
+    if (lane == 0) {
+      flags[0] = 0;
+      tma_prefetch_desc(&tma);
+      tma_prefetch_desc(&tmw);
     }
-    for (int b = 0; b < kBufs; ++b) {
-      mbar_init(afull(b), 1);
-      mbar_init(aempty(b), kEpi / 32);
-    }
-    flags[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tma_prefetch_desc(&tma);
-    tma_prefetch_desc(&tmw);
   }
   if (S > 1 && !Sh::kOver) cluster_arrive();
   if (warp == 1) tmem_alloc(smem_u32(flags + 1), Sh::kTmem);
@@ -241,6 +242,7 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)flags[1];
+  const unsigned long long limit = set_limit == 0 ? kDefaultWaitNs : set_limit;
   grid_launch_dependents();                                  // TMEM is held: the next kernel's set-up may begin
   // While the kernel before this one ends, the weights are brought into L2 (only there: what that
   // kernel may still write to them is seen by the loads behind the wait).  1 x 8192 x 2048 6.3 -> 5.7 us; with
@@ -553,6 +555,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
                                                                          const __grid_constant__ CUtensorMap tmw,
                                                                          const __grid_constant__ CUtensorMap tmo,
                                                                          const GemmArgs g) {
+  const unsigned long long set_limit = wait_limit_word();    // on its way during the set-up
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t bars = smem_u32(sm + kPairStages * kPairStage + kPairStaging);
@@ -570,7 +573,6 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   const int mt = (int)((g.M + 255) / 256), nt = (g.N + 255) / 256;
   const int tiles = mt * nt;
   const int G = g.G;
-  const unsigned long long limit = wait_limit_ns();
 
   // token tile and weight tile of tile t: groups of 8 token tiles, tokens fastest
   auto locate = [&](int t, int& m0, int& n0) {
@@ -582,20 +584,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
     n0 = r / h * 256;
   };
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(ready(s), 2);
-      mbar_init(empty(s), 1);
+  if (warp == 0) {                                           // a barrier per lane (full, ready, empty: 8 each; 2 + 2)
+    if (lane < 28) mbar_init(bars + 8u * (uint32_t)lane, lane >= 26 ? 16u : (lane >= 8 && lane < 16 ? 2u : 1u));
+    if (lane == 0) {
+      flags[0] = 0;
+      tma_prefetch_desc(&tma);
+      tma_prefetch_desc(&tmw);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(afull(b), 1);
-      mbar_init(aempty(b), 16);
-    }
-    flags[0] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    tma_prefetch_desc(&tma);
-    tma_prefetch_desc(&tmw);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(flags + 1)), "r"(512u)
@@ -607,6 +603,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)flags[1];
+  const unsigned long long limit = set_limit == 0 ? kDefaultWaitNs : set_limit;
   grid_launch_dependents();                                  // TMEM is held: the next kernel's set-up may begin
   grid_dependency_wait();
 
