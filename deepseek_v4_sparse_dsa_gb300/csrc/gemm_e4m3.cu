@@ -14,7 +14,7 @@
 //    SM; the parts are added in the order of K through distributed shared memory, so the result does
 //    not depend on timing and there is no workspace.
 //  * gemm_e4m3_pair_kernel: tiles of 256 x 256 on persistent CTA pairs (cta_group::2).
-// Measured: 1 x 8192 x 2048 5.4 us (weights in L2; 5.9 from memory), 64 x 8192 x 4096 9.4 us, 8192 x 64 x
+// Measured: 1 x 8192 x 2048 5.2 us (weights in L2; 5.9 from memory), 64 x 8192 x 4096 9.4 us, 8192 x 64 x
 // 4096 10.3 us, 8192 x 8192 x 4096 212 us = 2.6 PFLOP/s.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
@@ -490,21 +490,36 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
       }
     }
   } else {                                                   // rows at any alignment: neighbouring elements
-    for (int j = gt >> 5; rank + S * j < mv; j += kRows) {
-      const int m = rank + S * j;
-      float v[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int r = 0; r < S; ++r) {
-        const float* from = reinterpret_cast<const float*>(part(r, j));
+    constexpr int kFly = 4;
+    for (int j0 = gt >> 5; rank + S * j0 < mv; j0 += kRows * kFly) {
+      float v[kFly][4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = lane + 32 * q;
-          v[q] += from[Sh::kTok ? c ^ ((m & 7) << 2) : c];
+      for (int u = 0; u < kFly; ++u)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[u][q] = 0.f;
+      for (int r = 0; r < S; ++r) {
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+          const int j = j0 + u * kRows, m = rank + S * j;
+          if (m < mv) {
+            const float* from = reinterpret_cast<const float*>(part(r, j));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int c = lane + 32 * q;
+              v[u][q] += from[Sh::kTok ? c ^ ((m & 7) << 2) : c];
+            }
+          }
         }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = nt * kBlk + lane + 32 * q;
-        if (n < g.N) store_out(g, (m0 + m) * g.ldo + n, v[q]);
+      for (int u = 0; u < kFly; ++u) {
+        const int m = rank + S * (j0 + u * kRows);
+        if (m < mv) {
+          const int64_t at = (m0 + m) * g.ldo + nt * kBlk + lane;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (nt * kBlk + lane + 32 * q < g.N) store_out(g, at + 32 * q, v[u][q]);
+        }
       }
     }
   }
