@@ -22,7 +22,6 @@
 #include <atomic>
 #include <cstring>
 #include <mutex>
-#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -136,6 +135,22 @@ __device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
         "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
                :
                : "memory");
+}
+
+// Four sums as they are, eight rounded to bf16.
+template <int kN>
+__device__ __forceinline__ uint4 four_f32(const float (&v)[kN], int i) {
+  return make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
+}
+template <int kN>
+__device__ __forceinline__ uint4 eight_bf16(const float (&v)[kN], int i) {
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[i + 2 * e], v[i + 2 * e + 1]);
+    w[e] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ void store_out(const GemmArgs& g, int64_t at, float v) {
@@ -766,84 +781,117 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
         if ((b ^= 1) == 0) ph ^= 1u;
       }
       if (!ok) break;
-      // The warp's 32 tokens x 128 columns leave through its two staging blocks, 128 bytes of each row at a
-      // time: a thread writes its own row's pieces in the 128-byte swizzle, then one lane hands the block
-      // to a bulk tensor store (which leaves out what lies past M and N) and the warp goes on; or, where
-      // out's rows do not start and end on 16 bytes, the warp stores the rows itself.
       const int rows = g.M - m0 < 32 ? (int)(g.M - m0) : 32;
-      auto put = [&](auto* out, int col0, int block, const uint4 (&v)[8]) {
-        using E = typename std::remove_pointer<decltype(out)>::type;
-        uint8_t* stage = staging + 4096 * block;
-        if (g.out_tma) {                                     // the block's last store has been read
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      if (g.out_tma) {
+        // The warp's 32 tokens x 128 columns leave through its two staging blocks, 128 bytes of each row at a
+        // time: a thread writes its own row's pieces in the 128-byte swizzle, one lane hands the block to
+        // a bulk tensor store (which leaves out what lies past M and N), and the warp goes on.
+        auto put = [&](int col0, int block, const uint4 (&v)[8]) {
+          uint8_t* stage = staging + 4096 * block;
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");   // the block's last store is read
           __syncwarp();
-        }
 #pragma unroll
-        for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = v[p];
-        if (g.out_tma) {
+          for (int p = 0; p < 8; ++p) *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = v[p];
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
             if (rows > 0 && col0 < g.N) tma_store_2d(&tmo, smem_u32(stage), col0, m0);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
+        };
+        if (g.out_f32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint4 v[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) v[p] = four_f32(acc, 32 * q + 4 * p);
+            put(n0 + 32 * q, q & 1, v);
+          }
         } else {
-          // rows at any alignment: the warp stores one row at a time, neighbouring words; a bf16 row that
-          // starts at 2 mod 4 has its words shifted by one element, and its first and last element apart
-          const int cols = min(128 / (int)sizeof(E), g.N - col0);
-          constexpr int kFly = 8;
-          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint4 v[8];
+#pragma unroll
+            for (int p = 0; p < 8; ++p) v[p] = eight_bf16(acc, 64 * q + 8 * p);
+            put(n0 + 64 * q, q, v);
+          }
+        }
+      } else {
+        // Rows at any alignment, through the staging blocks. fp32: a row's 128 columns at a time, every store
+        // instruction in one 128-byte line, so that only a row's two ends write part of a 32-byte sector:
+        // 241 us at 6732 x 14163 x 1792, where words stored from each 128-byte piece's own start
+        // took 264. bf16, whose row has half the sectors, keeps to its pieces (207 us; in whole lines 223,
+        // and 280 with the rows' ends stored apart).
+        const int cols = g.N > n0 ? min(128, g.N - n0) : 0;
+        if (g.out_f32) {
+          const uint32_t first = (uint32_t)((reinterpret_cast<uintptr_t>(g.out) >> 2) + (uint64_t)((int64_t)m0 * g.ldo + n0));   // in words
 #pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += kFly) {
-            uint32_t w[kFly];
+          for (int h = 0; h < 2; ++h) {                      // 16 rows of 512 bytes
+            if ((lane >> 4) == h) {
 #pragma unroll
-            for (int u = 0; u < kFly; ++u)
-              w[u] = *reinterpret_cast<const uint32_t*>(stage + (r0 + u) * 128 + (((lane >> 2) ^ ((r0 + u) & 7)) << 4) + 4 * (lane & 3));
+              for (int q = 0; q < 32; ++q)
+                *reinterpret_cast<uint4*>(staging + (lane & 15) * 512 + (((q & 24) | ((q ^ lane) & 7)) << 4)) = four_f32(acc, 4 * q);
+            }
+            __syncwarp();
+#pragma unroll 1
+            for (int r0 = 0; r0 < 16; r0 += 4) {             // four rows in flight, no branches
+              uint32_t x[4][5];
+              int c0[4];
 #pragma unroll
-            for (int u = 0; u < kFly; ++u) {
-              E* o = out + (int64_t)(m0 + r0 + u) * g.ldo + col0;
-              const bool live = r0 + u < rows;
-              if constexpr (sizeof(E) == 4) {
-                if (live && lane < cols) *reinterpret_cast<uint32_t*>(o + lane) = w[u];
-              } else {
+              for (int u = 0; u < 4; ++u) {
+                const int r = r0 + u;
+                const uint32_t at = first + (uint32_t)(16 * h + r) * (uint32_t)g.ldo;
+                c0[u] = lane - (int)(at & 31u);
+#pragma unroll
+                for (int k = 0; k < 5; ++k) {
+                  const int c = (c0[u] + 32 * k) & 127, q = c >> 2;
+                  x[u][k] = *reinterpret_cast<const uint32_t*>(staging + r * 512 + (((q & 24) | ((q ^ r) & 7)) << 4) + 4 * (c & 3));
+                }
+              }
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                uint32_t* o = static_cast<uint32_t*>(g.out) + (int64_t)(m0 + 16 * h + r0 + u) * g.ldo + n0 + c0[u];
+                const int lim = 16 * h + r0 + u < rows ? cols : 0;
+#pragma unroll
+                for (int k = 0; k < 5; ++k)
+                  if ((unsigned)(c0[u] + 32 * k) < (unsigned)lim) o[32 * k] = x[u][k];
+              }
+            }
+            __syncwarp();
+          }
+        } else {
+          // a bf16 row that starts at 2 mod 4 has its words shifted by one element, and its first and last
+          // element apart
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            uint8_t* stage = staging + 4096 * q;
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((p ^ (lane & 7)) << 4)) = eight_bf16(acc, 64 * q + 8 * p);
+            __syncwarp();
+            const int lim = min(64, cols - 64 * q);
+            constexpr int kFly = 8;
+#pragma unroll 1
+            for (int r0 = 0; r0 < rows; r0 += kFly) {
+              uint32_t w[kFly];
+#pragma unroll
+              for (int u = 0; u < kFly; ++u)
+                w[u] = *reinterpret_cast<const uint32_t*>(stage + (r0 + u) * 128 + (((lane >> 2) ^ ((r0 + u) & 7)) << 4) + 4 * (lane & 3));
+#pragma unroll
+              for (int u = 0; u < kFly; ++u) {
+                uint16_t* o = static_cast<uint16_t*>(g.out) + (int64_t)(m0 + r0 + u) * g.ldo + n0 + 64 * q;
+                const bool live = r0 + u < rows;
                 const uint32_t next = __shfl_down_sync(0xFFFFFFFFu, w[u], 1);
                 const int odd = (int)(reinterpret_cast<uintptr_t>(o) >> 1) & 1, e = 2 * lane + odd;
                 const uint32_t x = odd ? __funnelshift_r(w[u], next, 16) : w[u];
-                const bool whole = e + 1 < cols;
+                const bool whole = e + 1 < lim;
                 if (live && whole) *reinterpret_cast<uint32_t*>(o + e) = x;
-                if (live && !whole && e < cols) o[e] = (E)x;
-                if (live && odd && lane == 0 && cols > 0) o[0] = (E)w[u];
+                if (live && !whole && e < lim) o[e] = (uint16_t)x;
+                if (live && odd && lane == 0 && lim > 0) o[0] = (uint16_t)w[u];
               }
             }
+            __syncwarp();
           }
-          __syncwarp();
-        }
-      };
-      if (g.out_f32) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint4 v[8];
-#pragma unroll
-          for (int p = 0; p < 8; ++p)
-            v[p] = make_uint4(__float_as_uint(acc[32 * q + 4 * p]), __float_as_uint(acc[32 * q + 4 * p + 1]),
-                              __float_as_uint(acc[32 * q + 4 * p + 2]), __float_as_uint(acc[32 * q + 4 * p + 3]));
-          put(static_cast<float*>(g.out), n0 + 32 * q, q & 1, v);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint4 v[8];
-#pragma unroll
-          for (int p = 0; p < 8; ++p) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(acc[64 * q + 8 * p + 2 * e], acc[64 * q + 8 * p + 2 * e + 1]);
-              w[e] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            v[p] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          put(static_cast<uint16_t*>(g.out), n0 + 64 * q, q, v);
         }
       }
     }
