@@ -147,9 +147,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // Element-wise accesses need the registers for more warps (4096 x 4097 bf16: 79 us with the next row in
 // flight, 38 us without); gamma and the residual are loaded with x where they fit (bf16; fp32 517 x 4999
 // 6.2 us without, 7.9 us with).  bf16 rows are held to 64 registers (8192 x 7168: 88 -> 76 us), fp32 rows lose by that
-// (4096 x 4096: 35 -> 43 us).
+// (4096 x 4096: 35 -> 43 us; one piece a thread, held to 64, 128 x 4096: 2.2 -> 3.1 us).  The next launch is
+// let in at the start: after the first loads a chain of norm and three products takes 16.5 us for one token, not 15.3.
 template <typename T, int VPT, bool VEC>
-__global__ void __launch_bounds__(VPT == 4 ? 1024 : 512, (!VEC || sizeof(T) == 2) && VPT < 4 ? 2 : 1)
+constexpr int kNormThreads = VPT == 2 ? 512 : (VPT == 1 && VEC && sizeof(T) == 4 ? 768 : 1024);
+template <typename T, int VPT, bool VEC>
+__global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>, VPT == 2 && (!VEC || sizeof(T) == 2) ? 2 : 1)
     add_rmsnorm_e4m3_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   __shared__ float s_sum[2][32];
@@ -305,10 +308,14 @@ cudaError_t launch_norm_v(NormArgs a, int num_sms, cudaStream_t stream) {
   // Pieces of 8 elements, whole groups of 16.  A row takes as many threads as it has pieces, or half or a
   // quarter as many: with two pieces a thread there is more in flight per thread and a batch of many
   // rows streams better, unless one warp holds the row anyway (16384 x 128: 7.4 us with two, 4.4 with one);
-  // few rows are quickest with one piece a thread.
+  // few rows are quickest with one piece a thread (64 x 7168 bf16: 2.5 us, with two 3.8; 304 x 5120: 3.3 and 4.4).
+  // Above 768 pieces an SM holds one such row, so that is for a row per SM at most (304 x 7001: 6.5 us with
+  // one, 5.6 with two), and fp32 pieces of 32 bytes gain nothing by it (64 x 8192: 3.5 and 3.3).
   const int pieces = (a.D + 127) / 128 * 16;
-  int vpt = pieces <= 512 ? 1 : (pieces <= 1024 ? 2 : 4);
-  if (vpt == 1 && pieces > 32 && a.T > 2 * (int64_t)num_sms) vpt = 2;
+  const bool wide = pieces > 768;
+  const int64_t few = wide ? num_sms : 2 * (int64_t)num_sms;       // rows
+  int vpt = pieces <= 32 || (a.T <= few && !(wide && VEC && sizeof(T) == 4)) ? 1 : 2;
+  if (pieces > 1024) vpt = 4;
   a.tpr = ((pieces + vpt - 1) / vpt + 31) / 32 * 32;
   const int rpc = a.tpr >= 256 ? 1 : 256 / a.tpr;
   if (vpt == 1) return launch_norm<T, 1, VEC>(a, a.tpr * rpc, rpc, num_sms, stream);

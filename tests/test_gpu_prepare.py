@@ -200,6 +200,15 @@ def test_add_rmsnorm(T, D, typ):
 
 
 @pytest.mark.parametrize("typ", [BF16, F32])
+@pytest.mark.parametrize("D", [4104, 6143, 6144, 6145, 6152, 8185, 8192])
+@pytest.mark.parametrize("rows", [(0, 31), (1, 0), (1, 1), (2, 0), (2, 1)])
+def test_add_rmsnorm_wide_rows(rows, D, typ):
+    # a row per SM, two, and one more: where a thread's share of a row changes
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    norm_case(rows[0] * sms + rows[1], D, typ)
+
+
+@pytest.mark.parametrize("typ", [BF16, F32])
 @pytest.mark.parametrize("kw", [dict(residual=False), dict(want_y=False), dict(want_codes=False), dict(pow2=True),
                                 dict(pad=1), dict(pad=8, pow2=True), dict(pad=4), dict(scale_x=1e-3), dict(scale_x=100.0)])
 def test_add_rmsnorm_options(typ, kw):
