@@ -150,9 +150,9 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // (4096 x 4096: 35 -> 43 us; one piece a thread, held to 64, 128 x 4096: 2.2 -> 3.1 us).  The next launch is
 // let in at the start: after the first loads a chain of norm and three products takes 16.5 us for one token, not 15.3.
 template <typename T, int VPT, bool VEC>
-constexpr int kNormThreads = VPT == 2 ? 512 : (VPT == 1 && VEC && sizeof(T) == 4 ? 768 : 1024);
+constexpr int kNormThreads = VEC && sizeof(T) == 4 && VPT < 4 ? (VPT == 2 ? 512 : 768) : 1024;   // at most
 template <typename T, int VPT, bool VEC>
-__global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>, VPT == 2 && (!VEC || sizeof(T) == 2) ? 2 : 1)
+__global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>)
     add_rmsnorm_e4m3_kernel(const NormArgs a) {
   using P = Piece<T, VEC>;
   __shared__ float s_sum[2][32];
@@ -315,7 +315,14 @@ cudaError_t launch_norm_v(NormArgs a, int num_sms, cudaStream_t stream) {
   const bool wide = pieces > 768;
   const int64_t few = wide ? num_sms : 2 * (int64_t)num_sms;       // rows
   int vpt = pieces <= 32 || (a.T <= few && !(wide && VEC && sizeof(T) == 4)) ? 1 : 2;
-  if (pieces > 1024) vpt = 4;
+  // Rows of more than 1024 pieces: two a thread for a row per SM at most (64 x 8454 bf16: 4.1 us, with four 7.0), and
+  // for 16-byte rows with a residual that exceed the L2, where the next row's loads count (4000 x 12288: 68 and
+  // 89 us; 1200 x 10240, 86 MB: 18.2 and 17.3; 4000 x 12288 without a residual: 56 and 51).
+  if (pieces > 1024) {
+    const int64_t bytes = a.T * a.D * (int64_t)(sizeof(T) * (2 + (a.res_out != nullptr) + (a.y != nullptr)) + 1);
+    const bool streams = VEC && a.res != nullptr && bytes > (int64_t)96 << 20;
+    vpt = pieces <= 2048 && !(VEC && sizeof(T) == 4) && (a.T <= num_sms || streams) ? 2 : 4;
+  }
   a.tpr = ((pieces + vpt - 1) / vpt + 31) / 32 * 32;
   const int rpc = a.tpr >= 256 ? 1 : 256 / a.tpr;
   if (vpt == 1) return launch_norm<T, 1, VEC>(a, a.tpr * rpc, rpc, num_sms, stream);

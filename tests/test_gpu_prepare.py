@@ -209,6 +209,31 @@ def test_add_rmsnorm_wide_rows(rows, D, typ):
 
 
 @pytest.mark.parametrize("typ", [BF16, F32])
+@pytest.mark.parametrize("D", [8193, 8200, 16383, 16384, 16385])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_add_rmsnorm_widest_rows(more, D, typ):
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    norm_case(sms + more, D, typ, residual=more < 1)
+
+
+def test_add_rmsnorm_wide_rows_past_the_cache():
+    # rows of 12288 that exceed 96 MiB, every output: the last rows, and rows of a small batch, agree with the formula
+    T, D = 1000, 12288
+    x, res = torch.randn(T, D, device="cuda").to(torch.bfloat16), torch.randn(T, D, device="cuda").to(torch.bfloat16)
+    g = torch.rand(D, device="cuda") + 0.5
+    ro, y = torch.empty_like(x), torch.empty_like(x)
+    codes, scale = torch.empty(T, D, dtype=torch.uint8, device="cuda"), torch.empty(T, D // 128, device="cuda")
+    dsa.dsa_add_rmsnorm_e4m3(x, D, res, D, g, 1e-6, T, D, BF16, ro, y, codes, D, scale)
+    at = np.r_[0:8, 148:156, 300:308, T - 8:T]
+    r64, y64 = ref.add_rmsnorm(f64(x[at]), f64(res[at]), f64(g), float(np.float32(1e-6)), True)
+    assert np.array_equal(f64(ro[at]), r64)
+    half = 2.0 ** -8
+    assert (np.abs(f64(y[at]) - y64) <= (ref.Y_REL + half + ref.Y_REL * half) * np.abs(y64) + 2.0 ** -133).all()
+    ref.check_quantised(y64, codes[at].cpu().numpy(), scale[at].cpu().numpy(), False)
+    assert torch.equal(ro, (x.float() + res.float()).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("typ", [BF16, F32])
 @pytest.mark.parametrize("kw", [dict(residual=False), dict(want_y=False), dict(want_codes=False), dict(pow2=True),
                                 dict(pad=1), dict(pad=8, pow2=True), dict(pad=4), dict(scale_x=1e-3), dict(scale_x=100.0)])
 def test_add_rmsnorm_options(typ, kw):
