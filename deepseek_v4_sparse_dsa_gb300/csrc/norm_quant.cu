@@ -242,8 +242,9 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>)
         constexpr float kMin = 1.17549435e-38f;
         float s = __fmul_rn(__fmul_rn(amax, rstd), 1.f / 448.f), f;
         if (amax >= 1e-30f && amax <= 1e30f && !(s < kMin) && !a.pow2) {
-          const float r0 = rcp_approx(amax);           // and one Newton step: 1 ulp
-          f = __fmul_rn(448.f, fmaf(fmaf(-amax, r0, 1.f), r0, r0));
+          const float r0 = rcp_approx(amax);           // and one Newton step on the quotient: half an ulp
+          f = __fmul_rn(448.f, r0);
+          f = fmaf(fmaf(-amax, f, 448.f), r0, f);
         } else if (amax > 0.f) {
           if (s < kMin) s = kMin;
           if (a.pow2) s = next_pow2_f32(s);
