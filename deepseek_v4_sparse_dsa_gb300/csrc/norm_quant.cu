@@ -238,28 +238,35 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>)
       }
       if (a.codes != nullptr) {
         // scale = amax |y| / 448; code = E4M3(y / scale) with y / scale = (r gamma) (448 / amax |r gamma|),
-        // one rounding less than by way of y.  The factor is NaN with rstd.
+        // one rounding less than by way of y.  Where the scale is a power of two or clamped, or 448 / amax may pass fp32,
+        // y comes first and then y / scale: 1 / scale is at most 2^126, while rstd / scale overflows for tiny groups.
+        // (Each way packs its own codes: r changed in place by one of them costs registers, 16384 x 4096 79 -> 83 us.)
         constexpr float kMin = 1.17549435e-38f;
         float s = __fmul_rn(__fmul_rn(amax, rstd), 1.f / 448.f), f;
+        uint32_t p[2] = {0u, 0u};
+        auto put = [&](auto q) {                       // the group's scale and the piece's codes
+          if ((v & 15) == 0 && (v >> 4) < groups) a.scale[row * groups + (v >> 4)] = s;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2)
+            p[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q(r[j][i]), q(r[j][i + 1])), __NV_SATFINITE, __NV_E4M3)
+                         << (8 * (i & 3));
+        };
         if (amax >= 1e-30f && amax <= 1e30f && !(s < kMin) && !a.pow2) {
           const float r0 = rcp_approx(amax);           // and one Newton step on the quotient: half an ulp
           f = __fmul_rn(448.f, r0);
           f = fmaf(fmaf(-amax, f, 448.f), r0, f);
-        } else if (amax > 0.f) {
-          if (s < kMin) s = kMin;
-          if (a.pow2) s = next_pow2_f32(s);
-          f = amax < INFINITY ? __fmul_rn(rstd, __fdiv_rn(1.f, s)) : 0.f;   // an infinity times 0 is a NaN code
+          f = fmaf(0.f, rstd, f);                      // NaN with rstd
+          put([&](float z) { return __fmul_rn(z, f); });
         } else {
-          s = 1.f;
-          f = 0.f;
-        }
-        f = fmaf(0.f, rstd, f);
-        if ((v & 15) == 0 && (v >> 4) < groups) a.scale[row * groups + (v >> 4)] = s;
-        uint32_t p[2] = {0u, 0u};
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 q = make_float2(__fmul_rn(r[j][i], f), __fmul_rn(r[j][i + 1], f));
-          p[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) << (8 * (i & 3));
+          if (amax > 0.f) {
+            if (s < kMin) s = kMin;
+            if (a.pow2) s = next_pow2_f32(s);
+            f = amax < INFINITY ? __fdiv_rn(1.f, s) : 0.f;   // an infinity times 0 is a NaN code
+          } else {
+            s = 1.f;
+            f = 0.f;
+          }
+          put([&](float z) { return __fmul_rn(__fmul_rn(z, rstd), f); });
         }
         uint8_t* c = a.codes + row * a.ldy;
         if constexpr (VEC) {

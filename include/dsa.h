@@ -339,8 +339,9 @@ dsa_status dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens,
  * Arithmetic in fp32: the sum of squares in an order that D, T, the type, the alignment and the
  * device's SM count fix, 1 / rms by the hardware's reciprocal root (2 ulps), each product
  * rounded on its own; y / y_scale is formed as (r gamma) (448 / max|r gamma|), without the row's
- * common factor, so a code can differ from the exact quotient's only where that lies within a
- * few fp32 ulps of a rounding boundary.
+ * common factor (from y itself where pow2_scale is set, y_scale is 2^-126, or max|r gamma| is
+ * outside [1e-30, 1e30]), so a code can differ from the exact quotient's only where that lies
+ * within a few fp32 ulps of a rounding boundary.
  * r * gamma must be finite.  A row holding a NaN gives NaN codes; an infinity gives NaN at its
  * place and zeros elsewhere in the row.
  */

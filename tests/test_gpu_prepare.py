@@ -324,6 +324,37 @@ def test_add_rmsnorm_rows_do_not_depend_on_the_batch():
     assert torch.equal(c[17:18], c1) and torch.equal(s[17:18], s1)
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("typ", [BF16, F32])
+@pytest.mark.parametrize("D", [384, 381])
+def test_add_rmsnorm_tiny_groups(D, typ, pow2):
+    # a group of tiny values with zeros among them, down to subnormals, in an otherwise zero row and beside a
+    # normal group: neither 1 / scale nor 1 / rms times it may overflow.  Powers of two for gamma: r gamma is exact.
+    tiny = [1e-29, 1e-32, 1e-35, 1.2e-36, 1e-36, 3e-37, 1e-38, 1e-39, 9.2e-41]
+    T = 2 * len(tiny)
+    x = torch.zeros(T, D)
+    part = torch.tensor([1.0, 0.5, 0.0, -0.25, -1.0, 0.3, 0.0, 0.001])
+    for i, t in enumerate(tiny):
+        x[2 * i:2 * i + 2, 40:48] = t * part
+        x[2 * i + 1, 256:] = torch.randn(D - 256)
+    x = x.cuda().to(torch.bfloat16 if typ == BF16 else torch.float32)
+    g = torch.tensor([1.0, 2.0], device="cuda").repeat(D)[:D].contiguous()
+    codes = torch.full((T, D), 0x5A, dtype=torch.uint8, device="cuda")
+    scale = torch.full((T, 3), float("nan"), device="cuda")
+    dsa.dsa_add_rmsnorm_e4m3(x, D, None, 0, g, 1e-6, T, D, typ, None, None, codes, D, scale, pow2)
+    _, y64 = ref.add_rmsnorm(f64(x), None, f64(g), float(np.float32(1e-6)), typ == BF16)
+    ref.check_quantised(y64, codes.cpu().numpy(), scale.cpu().numpy(), pow2)
+
+
+def test_add_rmsnorm_tiny_group_by_hand():
+    # 1 / rms is 1000, max|y| = 1.2e-33: the largest value is 448 times its scale, half of it 224, zeros stay zero
+    x = torch.zeros(1, 128, device="cuda")
+    x[0, 0], x[0, 1] = 1.2e-36, 6e-37
+    codes, scale = torch.zeros(1, 128, dtype=torch.uint8, device="cuda"), torch.zeros(1, 1, device="cuda")
+    dsa.dsa_add_rmsnorm_e4m3(x, 128, None, 0, torch.ones(128, device="cuda"), 1e-6, 1, 128, F32, None, None, codes, 128, scale)
+    assert codes[0, :3].tolist() == [0x7E, 0x76, 0] and not codes[0, 2:].any()
+
+
 # ------------------------------------------------------------------ gemm
 def gemm_inputs(M, N, K, seed=0, lda=None, ldw=None, signed=False, codes=None):
     rng = np.random.default_rng(seed + M + 7 * N + 13 * K)
