@@ -251,19 +251,18 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>)
             p[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q(r[j][i]), q(r[j][i + 1])), __NV_SATFINITE, __NV_E4M3)
                          << (8 * (i & 3));
         };
-        if (amax >= 1e-30f && amax <= 1e30f && !(s < kMin) && !a.pow2) {
+        if (amax >= 1e-30f && amax <= 1e30f && s >= kMin && !a.pow2) {
           const float r0 = rcp_approx(amax);           // and one Newton step on the quotient: half an ulp
           f = __fmul_rn(448.f, r0);
           f = fmaf(fmaf(-amax, f, 448.f), r0, f);
-          f = fmaf(0.f, rstd, f);                      // NaN with rstd
           put([&](float z) { return __fmul_rn(z, f); });
         } else {
-          if (amax > 0.f) {
+          if (amax > 0.f && amax < INFINITY && rstd > 0.f) {
             if (s < kMin) s = kMin;
             if (a.pow2) s = next_pow2_f32(s);
-            f = amax < INFINITY ? __fdiv_rn(1.f, s) : 0.f;   // an infinity times 0 is a NaN code
-          } else {
-            s = 1.f;
+            f = __fdiv_rn(1.f, s);
+          } else {                                     // zeros, or a row with an infinity (rstd 0) or a NaN, whose codes
+            s = 1.f;                                   // are NaN: infinity times 0, NaN times anything
             f = 0.f;
           }
           put([&](float z) { return __fmul_rn(__fmul_rn(z, rstd), f); });

@@ -342,8 +342,8 @@ dsa_status dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens,
  * common factor (from y itself where pow2_scale is set, y_scale is 2^-126, or max|r gamma| is
  * outside [1e-30, 1e30]), so a code can differ from the exact quotient's only where that lies
  * within a few fp32 ulps of a rounding boundary.
- * r * gamma must be finite.  A row holding a NaN gives NaN codes; an infinity gives NaN at its
- * place and zeros elsewhere in the row.
+ * r * gamma must be finite.  A row holding a NaN gives NaN codes; an infinity gives a NaN code at
+ * its place and zeros elsewhere in the row.  Every scale of such a row is 1.
  */
 dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
                                 float eps, int64_t T, int D, dsa_real type, void* residual_out, void* y,

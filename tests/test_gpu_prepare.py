@@ -355,6 +355,26 @@ def test_add_rmsnorm_tiny_group_by_hand():
     assert codes[0, :3].tolist() == [0x7E, 0x76, 0] and not codes[0, 2:].any()
 
 
+@pytest.mark.parametrize("pow2", [False, True])
+@pytest.mark.parametrize("typ", [BF16, F32])
+@pytest.mark.parametrize("D", [384, 381])
+def test_add_rmsnorm_scales_of_non_finite_rows(D, typ, pow2):
+    # the codes tell: NaN everywhere in a row that holds a NaN; NaN at an infinity's place and zeros elsewhere.  Every
+    # scale of such a row is 1, so that what is finite stays finite when the codes are multiplied by it
+    x = torch.randn(4, D, device="cuda")
+    x[0, 200], x[1, 5], x[2, 300] = float("inf"), float("nan"), float("-inf")
+    x = x.to(torch.bfloat16 if typ == BF16 else torch.float32)
+    codes, scale = torch.zeros(4, D, dtype=torch.uint8, device="cuda"), torch.zeros(4, 3, device="cuda")
+    dsa.dsa_add_rmsnorm_e4m3(x, D, None, 0, torch.ones(D, device="cuda"), 1e-6, 4, D, typ, None, None, codes, D, scale, pow2)
+    c = codes.cpu().numpy() & 0x7F
+    assert bool((scale[:3] == 1.0).all()) and bool(torch.isfinite(scale[3]).all())
+    assert (c[1] == 0x7F).all()
+    for row, at in ((0, 200), (2, 300)):
+        assert c[row, at] == 0x7F and (np.delete(c[row], at) == 0).all()
+    _, y64 = ref.add_rmsnorm(f64(x[3:]), None, np.ones(D), float(np.float32(1e-6)), typ == BF16)
+    ref.check_quantised(y64, codes[3:].cpu().numpy(), scale[3:].cpu().numpy(), pow2)
+
+
 # ------------------------------------------------------------------ gemm
 def gemm_inputs(M, N, K, seed=0, lda=None, ldw=None, signed=False, codes=None):
     rng = np.random.default_rng(seed + M + 7 * N + 13 * K)
