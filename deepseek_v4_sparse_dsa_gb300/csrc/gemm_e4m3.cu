@@ -36,6 +36,8 @@ constexpr size_t kSmemOne = 232448;          // dynamic shared memory of the one
 constexpr size_t kSmemTwo = 115712;          // of each of two (228 KB per SM, 1 KB reserved per CTA)
 
 struct GemmArgs {
+  // The scales are read by plain loads, behind the grid's wait: the kernel may be resident while the one that writes
+  // them still runs, so they are not constant over its life, which the read-only path requires.
   const float* a_scale;                      // [M, G]
   const float* w_scale;                      // [ceil(N / 128), G]
   int64_t M;
@@ -375,13 +377,13 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
     if constexpr (Sh::kTok) {
       // the token's factor of block i, and of the two blocks after it in flight
       const float* as = g.a_scale + (m0 + min(row, mv - 1)) * g.G + kb0;
-      float a0 = __ldg(as), w0 = __ldg(ws), a1 = __ldg(as + min(1, nkb - 1)), w1 = __ldg(ws + min(1, nkb - 1));
+      float a0 = as[0], w0 = ws[0], a1 = as[min(1, nkb - 1)], w1 = ws[min(1, nkb - 1)];
       for (int i = 0; i < nkb; ++i) {
         const float f = a0 * w0;
         const int kn = min(i + 2, nkb - 1);
         a0 = a1, w0 = w1;
-        a1 = __ldg(as + kn);
-        w1 = __ldg(ws + kn);
+        a1 = as[kn];
+        w1 = ws[kn];
         uint32_t d[kCols];
         take(d);
         if (!ok) break;
@@ -397,11 +399,11 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
       const float* as = g.a_scale + m0 * g.G + kb0;
       float pa[kPer], pw;
       auto fetch = [&](int i0) {
-        pw = i0 + sk < nkb ? __ldg(ws + i0 + sk) : 0.f;
+        pw = i0 + sk < nkb ? ws[i0 + sk] : 0.f;
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
           const int m = sm0 + u * kStep;
-          pa[u] = (m < mv && i0 + sk < nkb) ? __ldg(as + (int64_t)m * g.G + i0 + sk) : 0.f;
+          pa[u] = (m < mv && i0 + sk < nkb) ? as[(int64_t)m * g.G + i0 + sk] : 0.f;
         }
       };
       fetch(0);
@@ -754,13 +756,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
 #pragma unroll
       for (int i = 0; i < 128; ++i) acc[i] = 0.f;
       // scales of block kb, and of the two after it in flight
-      float a0 = __ldg(as), w0 = __ldg(ws), a1 = __ldg(as + min(1, G - 1)), w1 = __ldg(ws + min(1, G - 1));
+      float a0 = as[0], w0 = ws[0], a1 = as[min(1, G - 1)], w1 = ws[min(1, G - 1)];
       for (int kb = 0; kb < G; ++kb) {
         const float f = a0 * w0;
         const int kn = min(kb + 2, G - 1);
         a0 = a1, w0 = w1;
-        a1 = __ldg(as + kn);
-        w1 = __ldg(ws + kn);
+        a1 = as[kn];
+        w1 = ws[kn];
         ok = mbar_wait(afull(b), ph, limit, abort_flag);
         if (!(ok = __all_sync(0xFFFFFFFFu, ok))) break;
         tc_fence_after();

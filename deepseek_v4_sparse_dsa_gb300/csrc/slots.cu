@@ -77,13 +77,15 @@ __global__ void __launch_bounds__(kSlotThreads) assign_slots_kernel(const SlotAr
   bool bad = false;
   int64_t tok = 0, pg = 0;                               // running sums before this step's requests
   const int steps = (a.B + kSlotTile - 1) / kSlotTile;
-  int32_t n_next[kSlotPer], old_next[kSlotPer];          // the next step's lengths, in flight
+  // The next step's lengths, in flight.  Plain loads: the kernel may be resident before they are written, so the
+  // read-only path is not for them.
+  int32_t n_next[kSlotPer], old_next[kSlotPer];
   auto fetch = [&](int c) {
 #pragma unroll
     for (int i = 0; i < kSlotPer; ++i) {
       const int b = c * kSlotTile + tid * kSlotPer + i;
-      n_next[i] = b < a.B ? __ldg(a.fresh + b) : 0;
-      old_next[i] = b < a.B ? __ldg(a.cached + b) : 0;
+      n_next[i] = b < a.B ? a.fresh[b] : 0;
+      old_next[i] = b < a.B ? a.cached[b] : 0;
     }
   };
   fetch(0);

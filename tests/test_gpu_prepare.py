@@ -550,6 +550,46 @@ def test_calls_behind_copies_and_other_kernels_in_a_graph(M, N):
     assert dsa.dsa_device_error() == 0
 
 
+@pytest.mark.parametrize("M", [5, 24, 100, 2100])
+def test_a_chain_whose_scales_change_from_link_to_link(M):
+    # product -> norm -> product over the same code and scale buffers, nothing between them: a product is resident
+    # before the norm in front of it has written its scales, while the product before that still reads the old ones
+    D, links = 2304, 6
+    a, asc, w, wsc = gemm_inputs(M, D, D)
+    dw, dws = dev(w), dev(wsc)
+    gammas = [torch.rand(D, device="cuda") * 2.0 ** (3 * i % 8) + 0.1 for i in range(links)]
+    start = torch.randn(M, D, device="cuda")
+    e = lambda *s, t=torch.float32: torch.empty(s, dtype=t, device="cuda")  # noqa: E731
+    codes, scale, out = e(M, D, t=torch.uint8), e(M, D // 128), e(M, D)
+    seen = [(torch.empty_like(codes), torch.empty_like(scale), torch.empty_like(out)) for _ in range(links)]
+
+    def chain(apart):
+        src = start
+        for i, g in enumerate(gammas):
+            dsa.dsa_add_rmsnorm_e4m3(src, D, None, 0, g, 1e-6, M, D, F32, None, None, codes, D, scale)
+            if apart:
+                torch.cuda.synchronize()
+            dsa.dsa_gemm_e4m3(codes, D, scale, dw, D, dws, M, D, D, out, D, F32)
+            if apart:
+                torch.cuda.synchronize()
+                for t, s in zip((codes, scale, out), seen[i]):
+                    s.copy_(t)
+            src = out
+
+    chain(True)
+    assert all(not torch.equal(seen[i][1], seen[i + 1][1]) for i in range(links - 1))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            chain(False)
+    for _ in range(10):
+        for t in (codes, scale, out):
+            t.zero_()
+        graph.replay()
+        assert all(torch.equal(p, q) for p, q in zip((codes, scale, out), seen[-1]))
+    assert dsa.dsa_device_error() == 0
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 256, 4096), (200, 300, 2048), (2000, 2000, 1024)])
 def test_gemm_expired_waits_flag_timeout(M, N, K):
     a, asc, w, wsc = gemm_inputs(M, N, K)
