@@ -272,7 +272,9 @@ __global__ void __launch_bounds__(32 + kGroup, 2) sparse_attn_kernel(const AttnA
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = (uint32_t)flags[2];
-  grid_dependency_wait();               // q, the selection and the sinks may come from the kernel before
+  // q, the selection and the sinks may come from the kernel before, while this one is resident: plain loads, not the
+  // read-only path, for which they would have to be constant over this kernel's life
+  grid_dependency_wait();
 
   if (warp == 0) {
     // ================================ MMA issue ================================
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(32 + kGroup, 2) sparse_attn_kernel(const AttnA
       } else {
         for (int h = 0; h < kHeads; ++h) opart[h * kDim + j] = 0.f;
         if (gt < kHeads) {
-          const float s2 = __ldg(a.sink + gt) * kLog2e;
+          const float s2 = a.sink[gt] * kLog2e;
           sink2[gt] = s2;
           mrun[gt] = s2;
           lpart[gt] = 0.f;
@@ -348,11 +350,11 @@ __global__ void __launch_bounds__(32 + kGroup, 2) sparse_attn_kernel(const AttnA
       for (int r = 0; r < 8; ++r) {
         const int idx = gt + kGroup * r;          // 16-byte piece of the 64 x 256-byte tile
         const int h = idx >> 4, p16 = idx & 15;
-        const uint4 v = __ldg(qrow + idx);
+        const uint4 v = qrow[idx];
         *reinterpret_cast<uint4*>(q_s + (p16 >> 3) * 8192 + h * 128 + (((p16 & 7) ^ (h & 7)) << 4)) = v;
       }
       if (gt < kHeads) {
-        const float s2 = __ldg(a.sink + gt) * kLog2e;
+        const float s2 = a.sink[gt] * kLog2e;
         sink2[gt] = s2;
         mrun[gt] = s2;                            // the running max starts at the sink logit
       }
@@ -367,7 +369,7 @@ __global__ void __launch_bounds__(32 + kGroup, 2) sparse_attn_kernel(const AttnA
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int slot = (tile0 + m0 + u) * kTile + j;
-          pos[u] = (m0 + u < ntiles && slot < a.k) ? __ldg(a.sel + t * a.k + slot) : -1;
+          pos[u] = (m0 + u < ntiles && slot < a.k) ? a.sel[t * a.k + slot] : -1;
         }
 #pragma unroll
         for (int u = 0; u < 8; ++u)

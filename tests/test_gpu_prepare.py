@@ -590,6 +590,43 @@ def test_a_chain_whose_scales_change_from_link_to_link(M):
     assert dsa.dsa_device_error() == 0
 
 
+@pytest.mark.parametrize("T", [3, 70])
+def test_a_product_feeds_the_sparse_attention(T):
+    # product -> attention over one query buffer, whose rows change from link to link: the attention is resident while
+    # the product writes its queries
+    from deepseek_v4_sparse_dsa_gb300 import synth
+    ab = synth.make_attn(5, [200] * T, 1, 64)
+    K, N, links = 512, 64 * 128, 4
+    w, wsc = gemm_inputs(8, N, K)[2:]
+    d = lambda v: torch.from_numpy(np.ascontiguousarray(v)).cuda()  # noqa: E731
+    dw, dws, sel, fp4, sc, tab, sink = map(d, (w, wsc, ab.sel, ab.kv_fp4, ab.kv_scale, ab.table, ab.sink))
+    acts = [tuple(map(d, gemm_inputs(T, 8, K, seed=i)[:2])) for i in range(links)]
+    q, out = torch.empty(T, N, dtype=torch.bfloat16, device="cuda"), torch.empty(links, T, 64, 128, device="cuda")
+
+    def chain(apart):
+        for i, (a, asc) in enumerate(acts):
+            dsa.dsa_gemm_e4m3(a, K, asc, dw, K, dws, T, N, K, q, N, BF16)
+            if apart:
+                torch.cuda.synchronize()
+            dsa.dsa_sparse_attn_mxfp4(q, T, 64, 128, sel, ab.topk, fp4, sc, fp4.shape[0], ab.block_size, tab, tab.shape[1],
+                                      1, sink, 1e-3, out[i])
+            if apart:
+                torch.cuda.synchronize()
+
+    chain(True)
+    want = out.clone()
+    assert all(not torch.equal(want[i], want[i + 1]) for i in range(links - 1)) and bool(torch.isfinite(want).all())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            chain(False)
+    for _ in range(10):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, want)
+    assert dsa.dsa_device_error() == 0
+
+
 @pytest.mark.parametrize("M,N,K", [(4, 256, 4096), (200, 300, 2048), (2000, 2000, 1024)])
 def test_gemm_expired_waits_flag_timeout(M, N, K):
     a, asc, w, wsc = gemm_inputs(M, N, K)
