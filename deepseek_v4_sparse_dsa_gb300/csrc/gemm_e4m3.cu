@@ -1053,8 +1053,9 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
   if (M <= 0 || N <= 0) return cudaSuccess;
   GemmArgs g{a_scale, w_scale, M, N, (K + kBlk - 1) / kBlk, out, ldo, out_f32 ? 1 : 0, 0, 2, 0, 0};
   const int64_t es = out_f32 ? 4 : 2;
-  g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo * es % 16 == 0 ? 1 : 0;
-  g.out_tma = g.out_vec && N * es % 16 == 0 && ldo * es < (int64_t)1 << 40 ? 1 : 0;
+  // A single row's stride is any number: no products of it that could overflow.
+  g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo % (16 / es) == 0 ? 1 : 0;
+  g.out_tma = g.out_vec && N * es % 16 == 0 && ldo < ((int64_t)1 << 40) / es ? 1 : 0;
   // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 20 us
   // against 36 us, while at 256 x 8192 x 4096 (one wave) the clusters win (14.7 and 19.0 us).
   // Tiles of 32 tokens pay where those of 128, split over K, leave half the SMs idle (128 x 512 x 8192 6.8 us

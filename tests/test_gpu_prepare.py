@@ -467,6 +467,20 @@ def test_gemm_offsets_past_32_bits():
     assert torch.equal(out[:, :N], want) and not out[:, N:].any()
 
 
+def test_gemm_one_row_of_any_stride():
+    # one row's stride is never used: out rows may be any distance apart, also where it exceeds 2^40 bytes
+    a, asc, w, wsc = gemm_inputs(1, 19600, 256)
+    want, tol = ref.gemm(a, asc, w, wsc)
+    d = [dev(v) for v in (a, asc, w, wsc)]
+    for typ, tt in ((F32, torch.float32), (BF16, torch.bfloat16)):
+        for ldo in (1 << 40, 1 << 61, 1 << 62):
+            out = torch.full((1, 19600), 7.0, dtype=tt, device="cuda")
+            dsa.dsa_gemm_e4m3(d[0], 256, d[1], d[2], 256, d[3], 1, 19600, 256, out, ldo, typ)
+            assert dsa.dsa_device_error() == 0
+            half = 2.0 ** -8 if typ == BF16 else 0.0
+            assert (np.abs(f64(out) - want) <= tol + half * (np.abs(want) + tol)).all()
+
+
 def test_gemm_on_two_streams_at_once():
     # products of different shapes in flight together, each repeated: every result as when run alone
     cases = [(gemm_inputs(m, n, k), k) for m, n, k in ((3, 700, 2048), (300, 900, 1024), (2300, 2100, 512))]
