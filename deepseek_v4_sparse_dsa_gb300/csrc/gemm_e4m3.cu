@@ -598,6 +598,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
   auto empty = [&](int s) { return bars + 8u * (uint32_t)(16 + s); };
   auto afull = [&](int b) { return bars + 8u * (uint32_t)(24 + b); };
   auto aempty = [&](int b) { return bars + 8u * (uint32_t)(26 + b); };
+  const uint32_t drain = bars + 8u * 28u;                    // both issuers' products and signals are done
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1u;                     // = the CTA's rank in its cluster
@@ -616,8 +617,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
     n0 = r / h * 256;
   };
 
-  if (warp == 0) {                                           // a barrier per lane (full, ready, empty: 8 each; 2 + 2)
-    if (lane < 28) mbar_init(bars + 8u * (uint32_t)lane, lane >= 26 ? 16u : (lane >= 8 && lane < 16 ? 2u : 1u));
+  if (warp == 0) {                                           // a barrier per lane (full, ready, empty: 8 each; 2 + 2; 1)
+    if (lane < 29)
+      mbar_init(bars + 8u * (uint32_t)lane, lane == 28 || (lane >= 8 && lane < 16) ? 2u : (lane >= 26 ? 16u : 1u));
     if (lane == 0) {
       flags[0] = 0;
       tma_prefetch_desc(&tma);
@@ -678,6 +680,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
         mbar_wait(full(st), par, kCleanupWaitNs, nullptr);
         if (ok) ok = mbar_wait(empty(st), par, limit, abort_flag);
       }
+      // An abandoned call's CTA does not know how many products the pair has issued: their signals reach both CTAs, so
+      // neither leaves before the issuers' last one, which follows all others.
+      mbar_wait(drain, 0u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();
   } else if (warp < 4) {
@@ -729,6 +734,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) gemm_e4m3_pair_kernel(const _
         *abort_flag = 1;
       }
       // the last product has completed before either CTA frees TMEM or leaves
+      mma_commit_pair(drain);
       if (k > b) mbar_wait(afull(b), (uint32_t)((k - 2) >> 1) & 1u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();

@@ -661,6 +661,32 @@ def test_gemm_expired_waits_flag_timeout(M, N, K):
     assert (np.abs(f64(out)[:8] - want) <= tol).all()
 
 
+@pytest.mark.parametrize("out_typ", [BF16, F32])
+def test_gemm_pairs_abandoned_again_and_again(out_typ):
+    # a pair's CTAs give up at different points: what one still signals to the other arrives before it has left, the
+    # context stays usable and the next call is right.  One tile of a pair, and more tiles than pairs.
+    for M, N, K in ((300, 9800, 512), (2600, 2600, 640)):
+        a, asc, w, wsc = gemm_inputs(M, N, K)
+        d = [dev(v) for v in (a, asc, w, wsc)]
+        out = torch.empty(M, N, dtype=torch.bfloat16 if out_typ == BF16 else torch.float32, device="cuda")
+        call = lambda: dsa.dsa_gemm_e4m3(d[0], K, d[1], d[2], K, d[3], M, N, K, out, N, out_typ)  # noqa: E731
+        call()
+        want = out.clone()
+        assert dsa.dsa_device_error() == 0
+        for limit in (1, 500, 2000, 4000, 1):
+            dsa.dsa_set_wait_limit_ns(limit)
+            try:
+                for _ in range(10):
+                    call()
+                err = dsa.dsa_device_error()
+            finally:
+                dsa.dsa_set_wait_limit_ns(0)
+            assert err >= 0 and err & ~dsa.DSA_DEVERR_TIMEOUT == 0
+            out.zero_()
+            call()
+            assert dsa.dsa_device_error() == 0 and torch.equal(out, want)
+
+
 # ------------------------------------------------------------------ the run of them
 HID, NH, DH, RD = 1024, 64, 128, 64
 
