@@ -108,8 +108,10 @@ def _ptr(x):
         return None
     try:
         return x.data_ptr()
-    except AttributeError:                # an integer address
-        return int(x)
+    except AttributeError:
+        if isinstance(x, int):            # an address
+            return x
+        raise
 
 
 _raw_stream = None

@@ -83,6 +83,18 @@ def test_empty_problems_are_no_ops(lib):  # noqa: F811
     assert dsa.dsa_launch_count() == before
 
 
+@pytest.mark.parametrize("bad", [3.9, 4096.0, "128", b"128", np.int64(4096), np.array(4096), np.array([4096]), [4096]])
+def test_only_integers_and_tensors_are_addresses(lib, bad):  # noqa: F811
+    # whatever int() would make an address of is refused before the call, for every argument that is one
+    before = dsa.dsa_launch_count()
+    for call in (lambda: slots(cached=bad), lambda: norm(gamma=bad), lambda: gemm(w=bad),
+                 lambda: _status(dsa.dsa_indexer_k_hadamard_mxfp4, bad, _p(1), 0, 128, _p(2), _p(3), 64, 0)):
+        with pytest.raises((AttributeError, TypeError)):
+            call()
+    assert dsa.dsa_launch_count() == before
+    assert dsa._ptr(4096) == 4096 and dsa._ptr(None) is None
+
+
 # ------------------------------------------------------------------ the references
 def test_reference_slots_by_hand():
     # block size 4; request 0 holds 3 tokens (1 page) and brings 3: one slot left in page 7, then a new page;
