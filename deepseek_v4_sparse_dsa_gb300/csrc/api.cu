@@ -263,6 +263,11 @@ dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual
   if (y != nullptr && (y == residual || y == residual_out)) return DSA_ERR_INVALID_ARG;
   if (y_fp8 != nullptr && (y_fp8 == x || y_fp8 == residual || y_fp8 == residual_out || y_fp8 == y))
     return DSA_ERR_INVALID_ARG;
+  // every row reads gamma, and the scales are nobody else's
+  if (gamma == residual_out || gamma == y || gamma == static_cast<const void*>(y_fp8)) return DSA_ERR_INVALID_ARG;
+  if (y_scale != nullptr && (y_scale == x || y_scale == residual || y_scale == gamma || y_scale == residual_out ||
+                             y_scale == y || y_scale == static_cast<const void*>(y_fp8)))
+    return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_add_rmsnorm_e4m3(x, ldx, residual, ldr, gamma, eps, T, D, type == DSA_REAL_F32,
                                              residual_out, y, y_fp8, ldy, y_scale, pow2_scale != 0, device_sm_count(),
                                              static_cast<cudaStream_t>(stream)));

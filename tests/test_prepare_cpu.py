@@ -55,6 +55,15 @@ def test_add_rmsnorm_refusals(lib, bad, status):  # noqa: F811
     assert dsa.dsa_launch_count() == before
 
 
+@pytest.mark.parametrize("bad", [dict(scale=_p(1)), dict(scale=_p(2)), dict(scale=_p(3)), dict(scale=_p(4)), dict(scale=_p(5)),
+                                 dict(scale=_p(6)), dict(gamma=_p(4)), dict(gamma=_p(5)), dict(gamma=_p(6))])
+def test_add_rmsnorm_refuses_outputs_at_gamma_and_anything_at_the_scales(lib, bad):  # noqa: F811
+    # every row reads gamma and no other row's scales: an output there would change later rows
+    before = dsa.dsa_launch_count()
+    assert norm(**bad) == INVALID
+    assert dsa.dsa_launch_count() == before
+
+
 def gemm(a=_p(1), lda=256, asc=_p(2), w=_p(3), ldw=256, wsc=_p(4), M=4, N=128, K=256, out=_p(5), ldo=128,
          typ=dsa.DSA_REAL_BF16):
     return _status(dsa.dsa_gemm_e4m3, a, lda, asc, w, ldw, wsc, M, N, K, out, ldo, typ, 0)
