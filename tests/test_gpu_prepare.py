@@ -375,6 +375,73 @@ def test_add_rmsnorm_scales_of_non_finite_rows(D, typ, pow2):
     ref.check_quantised(y64, codes[3:].cpu().numpy(), scale[3:].cpu().numpy(), pow2)
 
 
+def test_add_rmsnorm_rows_of_batches_on_both_sides_of_the_thread_split():
+    # up to two rows per SM a row takes twice the threads: within one launch shape a row's bits do not depend on its
+    # neighbours; across the limit its sum of squares has another order, and both results hold against 64 bits
+    n = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    x = torch.randn(n + 1, 1536, device="cuda").to(torch.bfloat16)
+    g = torch.rand(1536, device="cuda") + 0.5
+    _, y64 = ref.add_rmsnorm(f64(x), None, f64(g), float(np.float32(1e-6)), True)
+
+    def call(v):
+        c = torch.empty(v.shape, dtype=torch.uint8, device="cuda")
+        s = torch.empty(v.shape[0], 12, device="cuda")
+        dsa.dsa_add_rmsnorm_e4m3(v, 1536, None, 0, g, 1e-6, v.shape[0], 1536, BF16, None, None, c, 1536, s)
+        return c, s
+    few, many, more = call(x[:n]), call(x), call(torch.cat((x, x)))
+    for c, s in (few, many, more):
+        m = min(len(c), n + 1)
+        ref.check_quantised(y64[:m], c[:m].cpu().numpy(), s[:m].cpu().numpy(), False)
+    assert all(torch.equal(p, q[:n + 1]) and torch.equal(p, q[n + 1:]) for p, q in zip(many, more))
+    for rows in (slice(17, 18), slice(0, 40), slice(n - 1, n)):
+        assert all(torch.equal(p[rows], q) for p, q in zip(few, call(x[rows])))
+
+
+@pytest.mark.parametrize("typ", [BF16, F32])
+def test_add_rmsnorm_power_of_two_scales_of_a_prompt(typ):
+    # The scale before it is rounded up: |r gamma| and the two products round at 2^-24 each, 1 / 448 is off by at most that;
+    # 1 / rms by the root's 2 ulps (2^-22) and half the sum of squares' error, a thread's 16 squares, 5 + 8 sums of warps
+    # and the mean: 31 roundings of 2^-24.  Together 23.5 * 2^-24 < 2^-19: farther than that from a power of two the
+    # exponent is the 64-bit one, nearer it is that or its neighbour.
+    T, D = 16384, 4096
+    tt = torch.bfloat16 if typ == BF16 else torch.float32
+    x = torch.randn(T, D, device="cuda").to(tt)
+    g = torch.rand(D, device="cuda") + 0.5
+    codes, scale = torch.empty(T, D, dtype=torch.uint8, device="cuda"), torch.empty(T, D // 128, device="cuda")
+    dsa.dsa_add_rmsnorm_e4m3(x, D, None, 0, g, 1e-6, T, D, typ, None, None, codes, D, scale, True)
+    near = 0
+    for t in range(0, T, 2048):
+        r = x[t:t + 2048].double()
+        y = r / (r.square().mean(-1, keepdim=True) + float(np.float32(1e-6))).sqrt() * g.double()
+        want = torch.log2(y.view(2048, D // 128, 128).abs().amax(-1) / 448.0)
+        m, e = torch.frexp(scale[t:t + 2048])
+        assert bool((m == 0.5).all())
+        got = (e - 1).double()
+        edge = (want - want.round()).abs() < 1.5 * 2.0 ** -19       # log2(1 + d) < 1.5 d
+        near += int(edge.sum())
+        assert bool((got == want.ceil())[~edge].all())
+        assert bool(((got - want.round()) * (got - want.round() - 1) == 0)[edge].all())
+        q = codes[t:t + 2048].view(torch.float8_e4m3fn).double() * scale[t:t + 2048].double().repeat_interleave(128, 1)
+        # half a code's step, 2^-4 relative, and y's own error (at most 2^-18)
+        assert bool(((q - y).abs() <= (2.0 ** -4 + 2.0 ** -17) * y.abs() + scale[t:t + 2048].double().repeat_interleave(128, 1) * 2.0 ** -10).all())
+    assert near < 20                                      # of 524288 groups some 4 x 2^-19 of them are expected there
+
+
+def test_add_rmsnorm_power_of_two_scales_at_the_border():
+    # mean(r^2) + eps = 4: y = r gamma / 2, and a largest value of 448 2^k gives a scale of 2^k.  2^-18 above it the next
+    # power, 2^-18 below it the same; on the border itself the root's last bit decides between the two
+    x = torch.ones(6, 256, device="cuda").to(torch.bfloat16)
+    for k in (-3, 0, 5):
+        for d, want in ((0.0, (1, 2)), (2.0 ** -18, (2,)), (-2.0 ** -18, (1,))):
+            g = torch.full((256,), 0.25, device="cuda")
+            g[7], g[200] = 896.0 * 2.0 ** k * (1 + d), -896.0 * 2.0 ** k * (1 + d)
+            codes, scale = torch.empty(6, 256, dtype=torch.uint8, device="cuda"), torch.empty(6, 2, device="cuda")
+            dsa.dsa_add_rmsnorm_e4m3(x, 256, None, 0, g, 3.0, 6, 256, BF16, None, None, codes, 256, scale, True)
+            assert set((scale / 2.0 ** k).flatten().tolist()) <= {float(w) for w in want}
+            top = codes.view(torch.float8_e4m3fn).float() * scale.repeat_interleave(128, 1)
+            assert bool(((top[:, 7] - 448.0 * 2.0 ** k).abs() <= 448.0 * 2.0 ** k * 2.0 ** -17).all())
+
+
 # ------------------------------------------------------------------ gemm
 def gemm_inputs(M, N, K, seed=0, lda=None, ldw=None, signed=False, codes=None):
     rng = np.random.default_rng(seed + M + 7 * N + 13 * K)
@@ -451,6 +518,14 @@ def test_gemm_large_product():
 def test_gemm_many_tiles(M, N, K, ldo, typ):
     # whole and ragged tiles in both directions, K past its last whole block, stores of 16 bytes and less
     gemm_check(M, N, K, typ, ldo=ldo, signed=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 19456, 160), (1, 19457, 160), (16, 24576, 144), (17, 24577, 144), (64, 32768, 128),
+                                   (128, 19456, 128), (130, 9800, 272), (200, 9856, 256), (256, 9984, 256), (257, 6500, 400)])
+@pytest.mark.parametrize("typ", [BF16, F32])
+def test_gemm_few_tokens_with_many_columns(M, N, K, typ):
+    # on both sides of the number of tiles that sends a product to the CTA pairs, down to one token
+    gemm_check(M, N, K, typ, signed=True)
 
 
 def test_gemm_offsets_past_32_bits():
@@ -685,6 +760,58 @@ def test_gemm_pairs_abandoned_again_and_again(out_typ):
             out.zero_()
             call()
             assert dsa.dsa_device_error() == 0 and torch.equal(out, want)
+
+
+SECOND_CONTEXT = r"""
+import ctypes, sys
+sys.path.insert(0, sys.argv[1])
+import torch
+from deepseek_v4_sparse_dsa_gb300 import dsa
+cu, lib = ctypes.CDLL("libcuda.so.1"), dsa.load()
+torch.zeros(1, device="cuda")
+
+def ck(r):
+    assert r == 0, r
+
+def products():
+    # all ones, all scales one: every output is K
+    for M, N, K in ((2000, 2000, 256), (200, 300, 2048), (20, 128, 4096), (3, 128, 4096)):
+        g = K // 128
+        sizes, p = (M * K, M * g * 4, N * K, -(-N // 128) * g * 4, M * N * 4), []
+        for n in sizes:
+            p.append(ctypes.c_uint64())
+            ck(cu.cuMemAlloc_v2(ctypes.byref(p[-1]), ctypes.c_size_t(n)))
+        for i in (0, 2):
+            ck(cu.cuMemsetD8_v2(p[i], 0x38, ctypes.c_size_t(sizes[i])))
+        for i in (1, 3):
+            ck(cu.cuMemsetD32_v2(p[i], 0x3F800000, ctypes.c_size_t(sizes[i] // 4)))
+        a, sa, w, sw, o = (v.value for v in p)
+        assert lib.dsa_gemm_e4m3(a, K, sa, w, K, sw, M, N, K, o, N, dsa.DSA_REAL_F32, None) == dsa.DSA_OK
+        assert lib.dsa_device_error(None) == 0
+        host = (ctypes.c_float * (M * N))()
+        ck(cu.cuMemcpyDtoH_v2(host, p[4], ctypes.c_size_t(sizes[4])))
+        assert min(host) == max(host) == K
+        for v in p:
+            ck(cu.cuMemFree_v2(v))
+
+products()
+for _ in range(2):
+    ctx = ctypes.c_void_p()
+    ck(cu.cuCtxCreate_v2(ctypes.byref(ctx), 0, 0))
+    products()
+    ck(cu.cuCtxDestroy_v2(ctx))
+products()
+"""
+
+
+def test_gemm_in_further_contexts_of_the_device():
+    # the shared-memory limit that a kernel asks for once per device holds in every context of the process
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SECOND_CONTEXT, root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
 
 
 # ------------------------------------------------------------------ the run of them
