@@ -7,15 +7,16 @@
 // multiply it by its two scales and add it to fp32 registers while the next block's product runs (the
 // scales are any fp32 values, so they cannot ride along in the block-scaled MMA).
 //
-// Few tokens are bound by the weights' stream from memory, many by the tensor cores and, at full rate, by
-// the board's power; what lies between, by the fixed costs of a launch.  Two kernels:
+// Few tokens are bound by the weights' stream from memory, many by the way of a block's sums out of TMEM and,
+// behind that, by the board's power; what lies between, by the fixed costs of a launch.  Two kernels:
 //  * gemm_e4m3_kernel: tiles of 128 weight rows x 16, 32 or 128 tokens.  A cluster of up to 8 CTAs shares a
 //    tile, each with its part of K, so that a product with few tiles still streams its weights on every
 //    SM; the parts are added in the order of K through distributed shared memory, so the result does
 //    not depend on timing and there is no workspace.
 //  * gemm_e4m3_pair_kernel: tiles of 256 x 256 on persistent CTA pairs (cta_group::2).
-// Measured: 1 x 8192 x 2048 5.2 us (weights in L2; 5.9 from memory), 64 x 8192 x 4096 9.4 us, 8192 x 64 x
-// 4096 10.3 us, 8192 x 8192 x 4096 212 us = 2.6 PFLOP/s.
+// Measured on quantised normals, operands in L2 and from memory: 1 x 8192 x 2048 5.1 and 5.9 us, 64 x 8192 x 4096
+// 9.3 and 10.4 us, 8192 x 64 x 4096 10.2 and 11.6 us.  8192 x 8192 x 4096: 24 calls 214 us each = 2.6 PFLOP/s, run on
+// and on 227 to 233 us = 2.4 PFLOP/s, the board at its power limit.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -551,8 +552,9 @@ __global__ void __launch_bounds__(FewShape<BT>::kThreads, BT == 128 ? 1 : 2)
 // registers while block kb + 1 runs.  Warps: producer, two MMA issuers (the even CTA's), one that
 // tells the even CTA that this CTA's copies have landed, eight epilogue warps (128 columns each).
 // The pairs walk the tiles in groups of 8 token tiles, so that the tiles in flight share rows.
-// Bound by power: at 2.7 PFLOP/s (16384 x 8192 x 8192) the board draws 1.38 of its 1.4 kW.  Without the sums
-// the products alone reach 3.1 PFLOP/s.
+// Bound by the accumulators' way back to the issuers: 837 cycles per block at 1.8 to 1.9 GHz, where the products alone
+// need 512.  Power comes next: 16384 x 8192 x 8192 runs at 2.85 PFLOP/s in a burst, and on and on at 2.6 with 1.39 of
+// 1.4 kW and 1.8 GHz; without the sums the products alone reach 3.1 PFLOP/s.
 constexpr int kPairThreads = 384;             // warps 0..3: producer, two MMA issuers, forwarder; 4..11: epilogue
 constexpr int kPairStages = 5;
 constexpr uint32_t kPairStage = 32768u;      // 128 tokens and 128 weight rows of 128 bytes
@@ -1062,11 +1064,14 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
   // A single row's stride is any number: no products of it that could overflow.
   g.out_vec = reinterpret_cast<uintptr_t>(out) % 16 == 0 && ldo % (16 / es) == 0 ? 1 : 0;
   g.out_tma = g.out_vec && N * es % 16 == 0 && ldo < ((int64_t)1 << 40) / es ? 1 : 0;
-  // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs: 512 x 8192 x 4096 20 us
-  // against 36 us, while at 256 x 8192 x 4096 (one wave) the clusters win (14.7 and 19.0 us).
-  // Tiles of 32 tokens pay where those of 128, split over K, leave half the SMs idle (128 x 512 x 8192 6.8 us
-  // against 8.0 with 128 tokens, 500 x 128 x 4096 5.3 and 6.4); elsewhere they read the weights too often
-  // (333 x 1000 x 1808 7.3 and 6.8 us, 95 x 2816 x 6704 13.6 and 9.9).  Up to 16 tokens 16 columns suffice.
+  // Tiles of 128 x 128 that fill the SMs more than once go to the CTA pairs (operands from memory): 512 x 8192 x 4096
+  // 19.6 us against 28.8, 130 x 9800 x 4096 19.3 and 23.9, 256 x 9984 x 4096 19.3 and 28.0, 257 x 6500 x 4096 20.8 and
+  // 23.7, while at 256 x 8192 x 4096 (one wave) the clusters win (15.0 and 19.0).  The rule does not look at the tokens:
+  // up to 128 of them with more than 152 x 128 columns the pairs lose (128 x 19584 x 4096 34.1 us against 30.8, 64 x
+  // 24576 x 4096 34.1 and 28.6, 1 x 24576 x 4096 36.6 and 22.0 with 16 tokens).
+  // Tiles of 32 tokens pay where those of 128, split over K, leave half the SMs idle (128 x 512 x 8192 7.2 us
+  // against 8.5 with 128 tokens, 500 x 128 x 4096 5.6 and 7.1); elsewhere they read the weights too often
+  // (333 x 1000 x 1808 7.9 and 7.2 us, 95 x 2816 x 6704 13.8 and 10.5).  Up to 16 tokens 16 columns suffice.
   const int64_t nt = (N + 127) / 128;
   cudaError_t e;
   if ((M + 127) / 128 * nt > num_sms) e = launch_pair(a, lda, w, ldw, K, g, num_sms, stream);

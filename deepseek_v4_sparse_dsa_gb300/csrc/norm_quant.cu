@@ -9,9 +9,9 @@
 // the code), so one pass over the row: its threads keep r in registers between the sum of
 // squares and the codes.  A group of 128 belongs to 16 neighbouring lanes, 8 elements each,
 // so its maximum takes four shuffles and no shared memory.  Measured: 16384 x 4096 bf16 with a
-// residual 79 us = 5.9 TB/s (the copy rate is 6.8), 4096 x 4096 fp32 34 us = 6.3 TB/s.  Rows that read
-// only 2 bytes per element are bound by the instructions (16384 x 1536 without a residual: 25 us,
-// 3 TB/s), one row by the launch (1.9 us).
+// residual 79 us = 5.9 TB/s (the copy rate is 6.8), 4096 x 4096 fp32 35 us = 6.3 TB/s, 517 x 4999 fp32 without a
+// residual 7.5 us in L2 and 9.1 from memory.  16384 x 1536 bf16 without a residual, 3 bytes per element, takes 24 us =
+// 3.1 TB/s, one row 1.9 us (the launch).
 #include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -147,7 +147,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
 // Element-wise accesses need the registers for more warps (4096 x 4097 bf16: 79 us with the next row in
 // flight, 38 us without); gamma and the residual are loaded with x where they fit (bf16; fp32 517 x 4999
 // 6.2 us without, 7.9 us with).  bf16 rows are held to 64 registers (8192 x 7168: 88 -> 76 us), fp32 rows lose by that
-// (4096 x 4096: 35 -> 43 us; one piece a thread, held to 64, 128 x 4096: 2.2 -> 3.1 us).  The next launch is
+// (4096 x 4096: 35 -> 43 us; one piece a thread, held to 64, 128 x 4096: 2.2 -> 3.1 us).  At 64 registers the two-piece
+// bf16 kernel spills 36 bytes, the four-piece fp32 kernels 8 and, element by element, 92.  The next launch is
 // let in at the start: after the first loads a chain of norm and three products takes 16.5 us for one token, not 15.3.
 template <typename T, int VPT, bool VEC>
 constexpr int kNormThreads = VEC && sizeof(T) == 4 && VPT < 4 ? (VPT == 2 ? 512 : 768) : 1024;   // at most
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>)
       ss = 0.f;
       for (int w = 0; w < nw; ++w) ss += s_sum[it][w0 + w];
     }
+    // A sum past fp32 gives rstd 0, as an infinity does: a second, scaled sum for such rows costs the others 2 to 18 %.
     const float rstd = rsqrtf(fmaf(ss, a.inv_d, a.eps));
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kNormThreads<T, VPT, VEC>)
         // one rounding less than by way of y.  Where the scale is a power of two or clamped, or 448 / amax may pass fp32,
         // y comes first and then y / scale: 1 / scale is at most 2^126, while rstd / scale overflows for tiny groups.
         // Each way packs its own codes where a thread has several pieces: r changed in place by one of them costs
-        // registers there (16384 x 4096 79 -> 83 us; with one piece 16384 x 128 5.6 us, 5.9 packed apart).
+        // registers there (16384 x 4096 79 -> 83 us; with one piece 16384 x 128 5.7 us, 5.9 packed apart).
         constexpr bool kApart = VPT > 1;
         constexpr float kMin = 1.17549435e-38f;
         float s = __fmul_rn(__fmul_rn(amax, rstd), 1.f / 448.f), f;
@@ -335,8 +337,10 @@ cudaError_t launch_norm_v(NormArgs a, int num_sms, cudaStream_t stream) {
   const int64_t few = wide ? num_sms : 2 * (int64_t)num_sms;       // rows
   int vpt = pieces <= 32 || (a.T <= few && !(wide && VEC && sizeof(T) == 4)) ? 1 : 2;
   // Rows of more than 1024 pieces: two a thread for a row per SM at most (64 x 8454 bf16: 4.1 us, with four 7.0), and
-  // for 16-byte rows with a residual that exceed the L2, where the next row's loads count (4000 x 12288: 68 and
-  // 89 us; 1200 x 10240, 86 MB: 18.2 and 17.3; 4000 x 12288 without a residual: 56 and 51).
+  // for 16-byte rows with a residual of more than 96 MiB, which the 129 MB L2 cannot keep from the call before, where
+  // the next row's loads count: 1300 x 12288 24.9 and 33.2 us, 1800 x 10240 28.8 and 31.0, 4000 x 12288 68 and 89
+  // (without a residual 56 and 51).  Below it what lies in L2 goes either way: 600 x 16384 13.3 and 11.5 us, 1200 x
+  // 10240 18.0 and 16.8, but 1000 x 12288 18.0 and 20.8; from memory two would win there too (1200 x 10240 20.2 and 23.6).
   if (pieces > 1024) {
     const int64_t bytes = a.T * a.D * (int64_t)(sizeof(T) * (2 + (a.res_out != nullptr) + (a.y != nullptr)) + 1);
     const bool streams = VEC && a.res != nullptr && bytes > (int64_t)96 << 20;

@@ -323,7 +323,8 @@ dsa_status dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens,
  *   y = r * gamma / sqrt(mean(r^2) + eps), in fp32;
  *   per group g of 128 elements (the last may be shorter): y_scale[t, g] = max|y| / 448 (at
  *   least 2^-126; 1 for an all-zero group), with pow2_scale != 0 rounded up to a power of
- *   two; y_fp8 = E4M3(y / y_scale), nearest even, saturating at +-448.
+ *   two; y_fp8 = E4M3(y / y_scale), nearest even, saturating at +-448.  The division by 448
+ *   is a product with the rounded 1 / 448.
  *  x        [T, D] of `type`, rows ldx elements apart; residual, residual_out [T, D] of
  *           `type`, rows ldr apart, both nullable (residual_out receives r; it may be
  *           residual itself, or x where ldr == ldx).
@@ -336,14 +337,19 @@ dsa_status dsa_assign_slots(const int32_t* cached_lens, const int32_t* new_lens,
  * or with one another.  1 <= D <= 32768.  Any element-aligned
  * pointers and strides >= D work; with D and the strides multiples of 8 and 16-byte aligned
  * pointers the rows move in 16-byte accesses.
- * Arithmetic in fp32: the sum of squares in an order that D, T, the type, the alignment and the
- * device's SM count fix, 1 / rms by the hardware's reciprocal root (2 ulps), each product
+ * Arithmetic in fp32: the sum of squares in an order that D, T, the type, the alignment, the
+ * device's SM count and which of residual, residual_out and y are given fix (so a row's last bits
+ * may differ in another batch), 1 / rms by the hardware's reciprocal root (2 ulps), each product
  * rounded on its own; y / y_scale is formed as (r gamma) (448 / max|r gamma|), without the row's
  * common factor (from y itself where pow2_scale is set, y_scale is 2^-126, or max|r gamma| is
  * outside [1e-30, 1e30]), so a code can differ from the exact quotient's only where that lies
- * within a few fp32 ulps of a rounding boundary.
- * r * gamma must be finite.  A row holding a NaN gives NaN codes; an infinity gives a NaN code at
- * its place and zeros elsewhere in the row.  Every scale of such a row is 1.
+ * within a few fp32 ulps of a rounding boundary.  For the same reason a power-of-two scale can
+ * be the neighbouring power where max|y| / 448 lies within 2^-18 of one.
+ * r * gamma and the row's fp32 sum of squares must be finite (|r| up to 1.8e19 / sqrt(D) always
+ * is enough; past it y and the codes are 0, not the formula's), and squares below 2^-126 lose
+ * precision, which shows only where eps is as small.  A row holding a NaN gives NaN codes; an
+ * infinity gives a NaN code at its place and zeros elsewhere in the row.  Every scale of such a
+ * row is 1.
  */
 dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
                                 float eps, int64_t T, int D, dsa_real type, void* residual_out, void* y,
@@ -361,7 +367,8 @@ dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual
  * past K in a row is not part of the product), M and N any; any element-aligned out and ldo
  * >= N (16-byte aligned rows are stored in 16-byte accesses).  out may not overlap an input.
  * Arithmetic: exact products summed in fp32 by the tensor cores within a block of 128, the
- * block's sum times its two scales (their product rounded to fp32) added in fp32 in the order
+ * block's sum times its two scales (their product rounded to fp32: it overflows, or loses
+ * precision below 2^-126, as any fp32 product) added in fp32 in the order
  * of K; with few tiles K is cut into 2, 4 or 8 parts whose sums are added in order.  One
  * rounding to bf16 at the end.  The result depends on the sizes and the device's SM count (a
  * row's sums may be cut differently in another batch) but not on timing.  No workspace.  A
