@@ -46,8 +46,11 @@ __device__ __forceinline__ int64_t gather_source(const GatherArgs& g, int64_t r,
   return -1;
 }
 
-__global__ void __launch_bounds__(256) mxfp4_gather_kernel(const GatherArgs g) {
-  grid_dependency_wait();              // positions may come from the kernel just before
+// Four CTAs per SM, as the grid is sized: at 70 registers three fit, and 64 x 16 rows x top-1024 take 87 us, not 69.
+__global__ void __launch_bounds__(256, 4) mxfp4_gather_kernel(const GatherArgs g) {
+  // The positions may come from the kernel just before, written while this one is resident: plain loads, not the
+  // read-only path, for which they would have to be constant over this kernel's life.
+  grid_dependency_wait();
   const uint32_t lane = threadIdx.x & 31u;
   const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
   const int64_t step = ((int64_t)gridDim.x * blockDim.x) >> 5;
@@ -57,12 +60,12 @@ __global__ void __launch_bounds__(256) mxfp4_gather_kernel(const GatherArgs g) {
   int64_t src_next = -1;
   if (r0 < g.rows) {
     const int64_t r = r0 + lane;
-    src_next = gather_source(g, r, r < g.rows ? __ldg(g.sel + r) : -1);
+    src_next = gather_source(g, r, r < g.rows ? g.sel[r] : -1);
   }
   for (; r0 < g.rows; r0 += step * 32) {
     const int64_t src = src_next;
     const int64_t r1 = r0 + step * 32 + lane;
-    const int32_t pos_next = r1 < g.rows ? __ldg(g.sel + r1) : -1;   // in flight meanwhile
+    const int32_t pos_next = r1 < g.rows ? g.sel[r1] : -1;   // in flight meanwhile
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t w[8], sb[8];

@@ -111,3 +111,33 @@ def test_gather_flash_decode_full_size():
     assert err == 0
     want = orc.mxfp4_paged_gather(wl.kv_fp4, wl.kv_scale, wl.gather_block_table, sel, wl.B, wl.next_n, 64)
     assert np.array_equal(got, want)
+
+
+def test_gather_of_selections_that_change_from_call_to_call():
+    # top-k and gather of two batches over one selection buffer, in a row: a gather is resident while the selection is
+    # written, and the one before it has read the old one
+    from deepseek_v4_sparse_dsa_gb300.device import DeviceBatch
+    wls = [parity.make_case(s, [20000, 700, 9000, 64], next_n=2, topk=256, gather=True) for s in (31, 32)]
+    dbs = [DeviceBatch.from_workload(w) for w in wls]
+    idx = torch.empty(dbs[0].T, 256, dtype=torch.int32, device="cuda")
+    wss = [db.workspace(dsa.DSA_OP_LOGITS_TOPK) for db in dbs]
+    outs = [torch.empty(db.T, 256, 128, dtype=torch.int16, device="cuda") for db in dbs]
+    want = []
+    for db, ws in zip(dbs, wss):
+        db.logits_topk(ws=ws, out_idx=idx, with_values=False)
+        torch.cuda.synchronize()
+        want.append(db.gather(idx).clone())
+        torch.cuda.synchronize()
+    assert not torch.equal(want[0], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(4):
+            for db, ws, out in zip(dbs, wss, outs):
+                db.logits_topk(ws=ws, out_idx=idx, with_values=False)
+                db.gather(idx, out)
+    for _ in range(10):
+        for out in outs:
+            out.zero_()
+        graph.replay()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert dsa.dsa_device_error() == 0
