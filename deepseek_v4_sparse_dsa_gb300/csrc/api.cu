@@ -68,6 +68,28 @@ dsa_status check_indexer_common(const void* q, const float* q_scale, dsa_dtype d
   return check_keys(keys, dtype, qs.B);
 }
 
+// A cache that calls write or read; its addresses are formed in 64-bit elements.
+dsa_status check_cache(const dsa_kv_cache& kv, int Hkv, int D) {
+  if (kv.num_blocks < 0 || kv.block_size < 1) return DSA_ERR_INVALID_ARG;
+  if (kv.row_stride < D || kv.block_stride < D || (Hkv > 1 && kv.head_stride < D)) return DSA_ERR_INVALID_ARG;
+  if (kv.num_blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 40;
+  if (kv.block_stride >= most || kv.row_stride >= most || kv.head_stride >= most) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
+// The rotation's arguments (rope_dim > 0).
+dsa_status check_rotation(const int32_t* positions, const float* cos_sin, int64_t max_pos, int rope_dim, int rope_off,
+                          dsa_rope_layout layout, int D) {
+  if (layout != DSA_ROPE_INTERLEAVED && layout != DSA_ROPE_HALF) return DSA_ERR_INVALID_ARG;
+  if (rope_dim < 0 || rope_dim % 2 != 0 || rope_off < 0 || rope_dim > D || rope_off > D - rope_dim || max_pos < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (rope_dim > 0 && (positions == nullptr || !aligned(positions, 4) || !aligned(cos_sin, 4) ||
+                       (cos_sin == nullptr && max_pos > 0)))
+    return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
 dsa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
 
 }  // namespace
@@ -291,6 +313,96 @@ dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, co
     return DSA_ERR_INVALID_ARG;
   return cuda_status(launch_gemm_e4m3(a, lda, a_scale, w, ldw, w_scale, M, N, K, out, ldo, out_type == DSA_REAL_F32,
                                       device_sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_rope_table(dsa_rope_params p, int rope_dim, int64_t pos0, int64_t n, float* cos_sin, void* stream) {
+  if (rope_dim < 2 || rope_dim % 2 != 0 || n < 0 || pos0 < 0) return DSA_ERR_INVALID_ARG;
+  if (!(p.base > 1.0) || !std::isfinite(p.base) || !std::isfinite(p.amplitude)) return DSA_ERR_INVALID_ARG;
+  if (p.scaling != DSA_ROPE_PLAIN && p.scaling != DSA_ROPE_LINEAR && p.scaling != DSA_ROPE_YARN) return DSA_ERR_INVALID_ARG;
+  if (p.scaling != DSA_ROPE_PLAIN && (!(p.factor >= 1.0) || !std::isfinite(p.factor))) return DSA_ERR_INVALID_ARG;
+  if (p.scaling == DSA_ROPE_YARN &&
+      (!(p.original_max_pos > 0.0) || !std::isfinite(p.original_max_pos) || !(p.beta_slow > 0.0) ||
+       !(p.beta_fast >= p.beta_slow) || !std::isfinite(p.beta_fast)))
+    return DSA_ERR_INVALID_ARG;
+  if (rope_dim > 256 || pos0 > (int64_t)1 << 31 || n > ((int64_t)1 << 31) - pos0) return DSA_ERR_UNSUPPORTED;
+  if (n == 0) return DSA_OK;
+  if (cos_sin == nullptr || !aligned(cos_sin, 4)) return DSA_ERR_INVALID_ARG;
+  return cuda_status(launch_rope_table(p, rope_dim, pos0, n, cos_sin, device_sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_rope(const void* x, int64_t ldx, int64_t hx, const int32_t* positions, const float* cos_sin,
+                    int64_t max_pos, int rope_dim, int rope_off, dsa_rope_layout layout, int inverse, int64_t T, int H,
+                    int D, dsa_real type, void* y, int64_t ldy, int64_t hy, void* stream) {
+  if (type != DSA_REAL_BF16 && type != DSA_REAL_F32) return DSA_ERR_INVALID_ARG;
+  if (T < 0 || H < 0 || D < 1 || rope_dim < 2) return DSA_ERR_INVALID_ARG;
+  if (D > 256) return DSA_ERR_UNSUPPORTED;
+  if (rope_dim > D || rope_off < 0 || rope_off > D - rope_dim) return DSA_ERR_INVALID_ARG;
+  if (T > INT32_MAX || T * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (T * H == 0) return DSA_OK;
+  const dsa_status s = check_rotation(positions, cos_sin, max_pos, rope_dim, rope_off, layout, D);
+  if (s != DSA_OK) return s;
+  const uintptr_t el = type == DSA_REAL_F32 ? 4 : 2;
+  if (x == nullptr || y == nullptr || !aligned(x, el) || !aligned(y, el)) return DSA_ERR_INVALID_ARG;
+  if ((H > 1 && (hx < D || hy < D)) || (T > 1 && (ldx < D || ldy < D))) return DSA_ERR_INVALID_ARG;
+  if (x == y && ((T > 1 && ldx != ldy) || (H > 1 && hx != hy))) return DSA_ERR_INVALID_ARG;
+  if (y == positions || y == cos_sin) return DSA_ERR_INVALID_ARG;
+  return cuda_status(launch_rope(x, ldx, hx, positions, cos_sin, max_pos, rope_dim, rope_off, layout == DSA_ROPE_HALF,
+                                 inverse != 0, T, H, D, type == DSA_REAL_F32, y, ldy, hy, device_sm_count(),
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, int64_t ldk, int Hkv, const void* v,
+                            int64_t ldv, int64_t T, int D, dsa_real type, const float* gamma_q, const float* gamma_k,
+                            float eps, const int32_t* positions, const float* cos_sin, int64_t max_pos, int rope_dim,
+                            int rope_off, dsa_rope_layout layout, void* q_out, int64_t ldqo, void* k_out, int64_t ldko,
+                            dsa_kv_cache kv, const int64_t* slot_mapping, void* stream) {
+  if (type != DSA_REAL_BF16 && type != DSA_REAL_F32) return DSA_ERR_INVALID_ARG;
+  if (T < 0 || H < 0 || Hkv < 0 || D < 1) return DSA_ERR_INVALID_ARG;
+  if (D > 256) return DSA_ERR_UNSUPPORTED;
+  if (T > INT32_MAX || T * ((int64_t)H + 2 * (int64_t)Hkv) > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  if (T == 0 || H + Hkv == 0) return DSA_OK;
+  dsa_status s = check_rotation(positions, cos_sin, max_pos, rope_dim, rope_off, layout, D);
+  if (s != DSA_OK) return s;
+  const bool norm = gamma_q != nullptr || gamma_k != nullptr;
+  if (norm && ((H > 0 && gamma_q == nullptr) || (Hkv > 0 && gamma_k == nullptr) || !(eps > 0.f) || !std::isfinite(eps)))
+    return DSA_ERR_INVALID_ARG;
+  if (H > 0 && (q == nullptr || q_out == nullptr || ldq < (int64_t)H * D || ldqo < (int64_t)H * D)) return DSA_ERR_INVALID_ARG;
+  if (Hkv > 0 && (k == nullptr || ldk < (int64_t)Hkv * D)) return DSA_ERR_INVALID_ARG;
+  if (Hkv > 0 && k_out == nullptr && kv.k == nullptr) return DSA_ERR_INVALID_ARG;
+  if (Hkv > 0 && k_out != nullptr && ldko < (int64_t)Hkv * D) return DSA_ERR_INVALID_ARG;
+  if (Hkv == 0) {
+    k = v = nullptr;
+    k_out = kv.k = kv.v = nullptr;
+  }
+  if (H == 0) {
+    q = nullptr;
+    q_out = nullptr;
+  }
+  if (kv.k == nullptr) v = nullptr;
+  if (v != nullptr && (ldv < (int64_t)Hkv * D || kv.v == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (kv.k != nullptr) {
+    if (slot_mapping == nullptr || !aligned(slot_mapping, 8) || !aligned(kv.k, 2) || !aligned(kv.v, 2)) return DSA_ERR_INVALID_ARG;
+    if ((s = check_cache(kv, Hkv, D)) != DSA_OK) return s;
+  }
+  const uintptr_t el = type == DSA_REAL_F32 ? 4 : 2;
+  if (!aligned(q, el) || !aligned(k, el) || !aligned(v, el) || !aligned(q_out, el) || !aligned(k_out, el) ||
+      !aligned(gamma_q, 4) || !aligned(gamma_k, 4))
+    return DSA_ERR_INVALID_ARG;
+  // in place only where a lane writes the elements it has read; nothing else is written where it is read
+  if ((q_out != nullptr && q_out == q && ldqo != ldq) || (k_out != nullptr && k_out == k && ldko != ldk)) return DSA_ERR_INVALID_ARG;
+  const void* out[] = {q_out, k_out, kv.k, v != nullptr ? kv.v : nullptr};
+  const void* in[] = {q, k, v, gamma_q, gamma_k, positions, rope_dim > 0 ? cos_sin : nullptr, kv.k != nullptr ? slot_mapping : nullptr};
+  for (int i = 0; i < 4; ++i) {
+    if (out[i] == nullptr) continue;
+    for (int j = 0; j < 8; ++j)
+      if (out[i] == in[j] && !(i == 0 && j == 0) && !(i == 1 && j == 1)) return DSA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[i] == out[j]) return DSA_ERR_INVALID_ARG;
+  }
+  return cuda_status(launch_qk_norm_rope(q, ldq, H, k, ldk, Hkv, v, ldv, T, D, type == DSA_REAL_F32, gamma_q, gamma_k, eps,
+                                         positions, cos_sin, max_pos, rope_dim, rope_off, layout == DSA_ROPE_HALF, q_out,
+                                         ldqo, k_out, ldko, kv, slot_mapping, device_sm_count(),
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 size_t dsa_workspace_bytes(dsa_op op, dsa_dtype dtype, dsa_queries qs, int topk) {

@@ -117,6 +117,18 @@ cudaError_t launch_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale
                              const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, bool out_f32,
                              int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------------------------ rotary positions (rope.cu)
+cudaError_t launch_rope_table(const dsa_rope_params& p, int R, int64_t pos0, int64_t n, float* out, int num_sms,
+                              cudaStream_t stream);
+cudaError_t launch_rope(const void* x, int64_t ldx, int64_t hx, const int32_t* positions, const float* cos_sin,
+                        int64_t max_pos, int R, int off, bool halves, bool inverse, int64_t T, int H, int D, bool f32,
+                        void* y, int64_t ldy, int64_t hy, int num_sms, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, int64_t ldk, int Hkv, const void* v,
+                                int64_t ldv, int64_t T, int D, bool f32, const float* gamma_q, const float* gamma_k,
+                                float eps, const int32_t* positions, const float* cos_sin, int64_t max_pos, int R, int off,
+                                bool halves, void* q_out, int64_t ldqo, void* k_out, int64_t ldko, const dsa_kv_cache& kv,
+                                const int64_t* slot, int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------------------------ sparse attention (sparse_attn.cu)
 // q [T, 64, 128] bf16 (16-byte aligned), sel [T, k], the paged mxfp4 cache, sink [64],
 // out [T, 64, 128] fp32.  One CTA per query row.
@@ -154,6 +166,7 @@ DSA_DECLARE_TU_ERROR_ACCESSORS(producer)
 DSA_DECLARE_TU_ERROR_ACCESSORS(attn)
 DSA_DECLARE_TU_ERROR_ACCESSORS(slots)
 DSA_DECLARE_TU_ERROR_ACCESSORS(gemm)
+DSA_DECLARE_TU_ERROR_ACCESSORS(rope)
 
 // Every translation unit's accessors, for dsa_device_error / dsa_set_wait_limit_ns.
 struct TuWords {
@@ -165,7 +178,7 @@ inline const TuWords* all_tu_words(int* n) {
   static const TuWords w[] = {DSA_TU_WORDS(gather), DSA_TU_WORDS(indexer), DSA_TU_WORDS(indexer_bf16_topk),
                               DSA_TU_WORDS(indexer_bf16_logits), DSA_TU_WORDS(indexer_fp8_topk),
                               DSA_TU_WORDS(indexer_fp8_logits), DSA_TU_WORDS(topk), DSA_TU_WORDS(producer),
-                              DSA_TU_WORDS(attn), DSA_TU_WORDS(slots), DSA_TU_WORDS(gemm)};
+                              DSA_TU_WORDS(attn), DSA_TU_WORDS(slots), DSA_TU_WORDS(gemm), DSA_TU_WORDS(rope)};
   *n = (int)(sizeof(w) / sizeof(w[0]));
   return w;
 }

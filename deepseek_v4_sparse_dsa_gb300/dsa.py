@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
+from ctypes import c_double, c_float, c_int, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdsa_gb300.so")
@@ -19,6 +19,8 @@ LIB_PATH = os.path.join(_HERE, "libdsa_gb300.so")
 DSA_OK, DSA_ERR_INVALID_ARG, DSA_ERR_UNSUPPORTED, DSA_ERR_CUDA, DSA_ERR_WORKSPACE = 0, 1, 2, 3, 4
 DSA_BF16, DSA_E4M3, DSA_E4M3_MXFP4K = 0, 1, 2
 DSA_REAL_BF16, DSA_REAL_F32 = 0, 1
+DSA_ROPE_INTERLEAVED, DSA_ROPE_HALF = 0, 1
+DSA_ROPE_PLAIN, DSA_ROPE_LINEAR, DSA_ROPE_YARN = 0, 1, 2
 DSA_OP_TOPK, DSA_OP_LOGITS_TOPK = 1, 2
 DSA_DEVERR_INDEX, DSA_DEVERR_TIMEOUT = 1, 2
 
@@ -48,6 +50,30 @@ class dsa_queries(ctypes.Structure):
         ("context_lens", c_void_p),
         ("max_context_len", c_int32),
         ("causal", c_int32),
+    ]
+
+
+class dsa_rope_params(ctypes.Structure):
+    _fields_ = [
+        ("base", c_double),
+        ("scaling", c_int),
+        ("factor", c_double),
+        ("original_max_pos", c_double),
+        ("beta_fast", c_double),
+        ("beta_slow", c_double),
+        ("amplitude", c_double),
+    ]
+
+
+class dsa_kv_cache(ctypes.Structure):
+    _fields_ = [
+        ("k", c_void_p),
+        ("v", c_void_p),
+        ("num_blocks", c_int64),
+        ("block_size", c_int32),
+        ("block_stride", c_int64),
+        ("row_stride", c_int64),
+        ("head_stride", c_int64),
     ]
 
 
@@ -89,6 +115,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                          c_int, c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int, c_void_p]),
         "dsa_gemm_e4m3": (c_int, [c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_int, c_int,
                                   c_void_p, c_int64, c_int, c_void_p]),
+        "dsa_rope_table": (c_int, [dsa_rope_params, c_int, c_int64, c_int64, c_void_p, c_void_p]),
+        "dsa_rope": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_int, c_int, c_int, c_int, c_int64,
+                             c_int, c_int, c_int, c_void_p, c_int64, c_int64, c_void_p]),
+        "dsa_qk_norm_rope": (c_int, [c_void_p, c_int64, c_int, c_void_p, c_int64, c_int, c_void_p, c_int64, c_int64, c_int,
+                                     c_int, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_int64, c_int, c_int, c_int,
+                                     c_void_p, c_int64, c_void_p, c_int64, dsa_kv_cache, c_void_p, c_void_p]),
         "dsa_workspace_bytes": (c_size_t, [c_int, c_int, dsa_queries, c_int]),
         "dsa_status_string": (ctypes.c_char_p, [c_int]),
         "dsa_device_error": (c_int, [c_void_p]),
@@ -160,6 +192,23 @@ def make_keys(data, scale=None, block_table=None, block_size: int = 64, num_rows
 
 def make_queries(B: int, next_n: int, context_lens, max_context_len: int, causal: bool) -> dsa_queries:
     return dsa_queries(int(B), int(next_n), _ptr(context_lens), int(max_context_len), 1 if causal else 0)
+
+
+def make_rope_params(base=10000.0, scaling=DSA_ROPE_PLAIN, factor=1.0, original_max_pos=4096.0, beta_fast=32.0,
+                     beta_slow=1.0, amplitude=1.0) -> dsa_rope_params:
+    return dsa_rope_params(float(base), int(scaling), float(factor), float(original_max_pos), float(beta_fast),
+                           float(beta_slow), float(amplitude))
+
+
+def make_kv_cache(k, v=None) -> dsa_kv_cache:
+    """dsa_kv_cache from bf16 tensors [num_blocks, block_size, heads, D] (any strides of the first three, D contiguous;
+    transpose(1, 2) of [num_blocks, heads, block_size, D] is one); k None: no cache."""
+    if k is None:
+        return dsa_kv_cache()
+    st = k.stride()
+    if st[3] != 1 and k.shape[3] > 1 or v is not None and (v.stride() != st or v.shape != k.shape):
+        raise ValueError("keys and values need the same shape and strides, and contiguous heads")
+    return dsa_kv_cache(k.data_ptr(), None if v is None else v.data_ptr(), k.shape[0], k.shape[1], st[0], st[1], st[2])
 
 
 def dsa_indexer_logits(q, q_scale, dtype, weights, H, D, keys, qs, logits, ld_logits, stream=None):
@@ -235,6 +284,27 @@ def dsa_add_rmsnorm_e4m3(x, ldx, residual, ldr, gamma, eps, T, D, type, residual
 def dsa_gemm_e4m3(a, lda, a_scale, w, ldw, w_scale, M, N, K, out, ldo, out_type, stream=None):
     _check(load().dsa_gemm_e4m3(_ptr(a), int(lda), _ptr(a_scale), _ptr(w), int(ldw), _ptr(w_scale), int(M), int(N),
                                 int(K), _ptr(out), int(ldo), int(out_type), _stream(stream)), "dsa_gemm_e4m3")
+
+
+def dsa_rope_table(params, rope_dim, pos0, n, cos_sin, stream=None):
+    _check(load().dsa_rope_table(params, int(rope_dim), int(pos0), int(n), _ptr(cos_sin), _stream(stream)),
+           "dsa_rope_table")
+
+
+def dsa_rope(x, ldx, hx, positions, cos_sin, max_pos, rope_dim, rope_off, layout, inverse, T, H, D, type, y, ldy, hy,
+             stream=None):
+    _check(load().dsa_rope(_ptr(x), int(ldx), int(hx), _ptr(positions), _ptr(cos_sin), int(max_pos), int(rope_dim),
+                           int(rope_off), int(layout), 1 if inverse else 0, int(T), int(H), int(D), int(type), _ptr(y),
+                           int(ldy), int(hy), _stream(stream)), "dsa_rope")
+
+
+def dsa_qk_norm_rope(q, ldq, H, k, ldk, Hkv, v, ldv, T, D, type, gamma_q, gamma_k, eps, positions, cos_sin, max_pos,
+                     rope_dim, rope_off, layout, q_out, ldqo, k_out, ldko, kv, slot_mapping, stream=None):
+    _check(load().dsa_qk_norm_rope(_ptr(q), int(ldq), int(H), _ptr(k), int(ldk), int(Hkv), _ptr(v), int(ldv), int(T),
+                                   int(D), int(type), _ptr(gamma_q), _ptr(gamma_k), float(eps), _ptr(positions),
+                                   _ptr(cos_sin), int(max_pos), int(rope_dim), int(rope_off), int(layout), _ptr(q_out),
+                                   int(ldqo), _ptr(k_out), int(ldko), kv, _ptr(slot_mapping), _stream(stream)),
+           "dsa_qk_norm_rope")
 
 
 def dsa_workspace_bytes(op, dtype, qs, topk) -> int:

@@ -68,6 +68,38 @@ typedef enum { DSA_BF16 = 0, DSA_E4M3 = 1, DSA_E4M3_MXFP4K = 2 } dsa_dtype;
 /* Storage of hidden rows and of a projection's result. */
 typedef enum { DSA_REAL_BF16 = 0, DSA_REAL_F32 = 1 } dsa_real;
 
+/* Which dims of a head turn together: (2i, 2i + 1), or (i, i + rope_dim / 2). */
+typedef enum { DSA_ROPE_INTERLEAVED = 0, DSA_ROPE_HALF = 1 } dsa_rope_layout;
+
+/* Frequencies of rotary positions; see dsa_rope_table. */
+typedef enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_YARN = 2 } dsa_rope_scaling;
+typedef struct {
+  double base;               /* > 1, e.g. 10000                                          */
+  dsa_rope_scaling scaling;
+  double factor;             /* LINEAR, YARN: >= 1, how much longer the context gets     */
+  double original_max_pos;   /* YARN: the context the frequencies were trained for       */
+  double beta_fast;          /* YARN: turns within it above which a pair is kept         */
+  double beta_slow;          /* YARN: turns below which it is slowed by the factor       */
+  double amplitude;          /* multiplies cos and sin (1 for none)                      */
+} dsa_rope_params;
+
+/*
+ * Paged bf16 cache of keys and values (DEVICE memory): head h of position j of sequence b is
+ * the D elements at k (or v) + block * block_stride + (j % block_size) * row_stride +
+ * h * head_stride with block = block_table[b * bt_stride + j / block_size], strides in
+ * elements.  [num_blocks, block_size, heads, D] and [num_blocks, heads, block_size, D] are
+ * both cases of it.  v may be k (keys that are their own values).
+ */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t num_blocks;
+  int32_t block_size;
+  int64_t block_stride;
+  int64_t row_stride;
+  int64_t head_stride;
+} dsa_kv_cache;
+
 typedef enum { DSA_OP_TOPK = 1, DSA_OP_LOGITS_TOPK = 2 } dsa_op;
 
 /* Bits of the per-device error word (see dsa_device_error). */
@@ -377,6 +409,76 @@ dsa_status dsa_add_rmsnorm_e4m3(const void* x, int64_t ldx, const void* residual
 dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, const uint8_t* w, int64_t ldw,
                          const float* w_scale, int64_t M, int N, int K, void* out, int64_t ldo, dsa_real out_type,
                          void* stream);
+
+/*
+ * The calls of a layer that attends to every cached key (a draft layer, a layer without the
+ * selection, a prompt no longer than it).  (The pages have no counterpart.)  The table is made
+ * once; dsa_qk_norm_rope turns the projected heads and writes keys and values to the slots of
+ * dsa_assign_slots; dsa_paged_attn reads them through its block table, query_start and
+ * context_lens; dsa_rope with inverse set takes the rotation of an output back.
+ *
+ * dsa_rope_table -- cos / sin table of the positions pos0 .. pos0 + n - 1, in the layout that
+ * dsa_rope, dsa_qk_norm_rope and dsa_indexer_q_rope_quant read: for i < rope_dim / 2
+ *   cos_sin[r, i] = amplitude cos((pos0 + r) f_i), cos_sin[r, rope_dim / 2 + i] the sine,
+ *   PLAIN:  f_i = base^(-2i / rope_dim);  LINEAR: that / factor;
+ *   YARN (Peng et al. 2023): f_i (1 - w_i) + f_i / factor w_i, w_i = clamp((i - lo) / (hi -
+ *   lo), 0, 1), lo = max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)), rope_dim - 1),
+ *   c(b) = rope_dim ln(original_max_pos / (2 pi b)) / (2 ln base); hi - lo is at least 0.001.
+ *  cos_sin  [n, rope_dim] fp32.  rope_dim even, 2 .. 256; pos0 >= 0, pos0 + n <= 2^31.
+ * Each value is within 2^-22 amplitude of the exact one at any position: the angle is reduced
+ * by whole turns in 64-bit integers.  params is read on the host.
+ */
+dsa_status dsa_rope_table(dsa_rope_params params, int rope_dim, int64_t pos0, int64_t n, float* cos_sin, void* stream);
+
+/*
+ * dsa_rope -- rotation of heads.  For every token t and head h, with c and s the cosine and
+ * sine of pair i at positions[t] (s negated where inverse is set: the rotation is taken back,
+ * which is also its gradient where the table's amplitude is 1), the elements (x0, x1) =
+ * (rope_off + 2i, rope_off + 2i + 1) (INTERLEAVED) or (rope_off + i, rope_off + rope_dim / 2
+ * + i) (HALF), i < rope_dim / 2, become (x0 c - x1 s, x0 s + x1 c); the other dims are copied.
+ *  x, y     heads of D elements of `type`: token t, head h at t * ldx + h * hx (t * ldy +
+ *           h * hy), in elements.  y may be x where the strides are the same; no other overlap
+ *           of y with an input, and heads of y do not overlap one another.
+ *  positions [T] int32; one outside [0, max_pos) gives zeros in the rotated dims and sets
+ *           DSA_DEVERR_INDEX.  cos_sin [max_pos, rope_dim] fp32 as dsa_rope_table writes it.
+ * D <= 256 (DSA_ERR_UNSUPPORTED above); rope_dim even, >= 2, rope_off + rope_dim <= D; |hx|,
+ * |hy| >= D where H > 1, token strides any.  Any
+ * element-aligned pointers and strides work; heads move in units of four elements where D is a
+ * multiple of 8, rope_off of 4, rope_dim of 4 (HALF: 8), the strides of 4, and pointers are
+ * aligned to four elements (the table to 16 bytes).
+ * fp32 arithmetic, one rounding to `type` at the end.
+ */
+dsa_status dsa_rope(const void* x, int64_t ldx, int64_t hx, const int32_t* positions, const float* cos_sin,
+                    int64_t max_pos, int rope_dim, int rope_off, dsa_rope_layout layout, int inverse, int64_t T, int H,
+                    int D, dsa_real type, void* y, int64_t ldy, int64_t hy, void* stream);
+
+/*
+ * dsa_qk_norm_rope -- per-head RMS norm and rotation of queries and keys, and the write of
+ * keys and values into the paged cache, in one pass.  For every token t and query head h:
+ *   y = q[t, h] * gamma_q / sqrt(mean(q[t, h]^2) + eps) (q itself without a gamma), then the
+ *   rotation of dsa_rope, in fp32 with one rounding to `type` (the cache: to bf16) at the end;
+ * the same for the key heads with gamma_k; value heads are copied.
+ *  q        [T, H, D] of `type`, tokens ldq elements apart, heads D apart; q_out the same with
+ *           ldqo, and may be q where ldqo == ldq.  Both may be NULL where H == 0.
+ *  k, v     [T, Hkv, D], tokens ldk and ldv apart (one projection's output holds q, k and v
+ *           side by side).  v may be NULL: no values are written.  k may be NULL where Hkv == 0.
+ *  k_out    [T, Hkv, D] of `type`, nullable; may be k where ldko == ldk.
+ *  gamma_q, gamma_k [D] fp32: both, or both NULL (no norm); one that has no heads may be NULL.
+ *  positions, cos_sin, max_pos, rope_dim, rope_off, layout as for dsa_rope; rope_dim may be 0
+ *           (no rotation; positions and cos_sin may then be NULL).
+ *  kv       the cache; kv.k NULL: none (then v is not read).  slot_mapping [T] int64: token t's
+ *           keys and values go to row slot % block_size of block slot / block_size; negative:
+ *           none; past the pool: none, and DSA_DEVERR_INDEX.  Slots are distinct.
+ * No other overlap of outputs with inputs or with one another.  D <= 256, T * (H + 2 Hkv) <
+ * 2^31.  Any element-aligned pointers and strides work, faster under the conditions of
+ * dsa_rope.  A head's squares must sum to a finite fp32 (past it y is 0), |y| is the formula's
+ * within a few fp32 ulps before the last rounding.
+ */
+dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, int64_t ldk, int Hkv, const void* v,
+                            int64_t ldv, int64_t T, int D, dsa_real type, const float* gamma_q, const float* gamma_k,
+                            float eps, const int32_t* positions, const float* cos_sin, int64_t max_pos, int rope_dim,
+                            int rope_off, dsa_rope_layout layout, void* q_out, int64_t ldqo, void* k_out, int64_t ldko,
+                            dsa_kv_cache kv, const int64_t* slot_mapping, void* stream);
 
 /*
  * dsa_indexer_logits_topk_noalloc -- dsa_indexer_logits_topk for callers that cannot
