@@ -78,6 +78,12 @@ dsa_status check_cache(const dsa_kv_cache& kv, int Hkv, int D) {
   return DSA_OK;
 }
 
+dsa_status check_attn_sizes(int64_t T, int B, int H, int Hkv, int D) {
+  if (T < 0 || B < 0 || H < 1 || Hkv < 1 || H % Hkv != 0) return DSA_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128) || B > 65536 || T > INT32_MAX || T * H > INT32_MAX) return DSA_ERR_UNSUPPORTED;
+  return DSA_OK;
+}
+
 // The rotation's arguments (rope_dim > 0).
 dsa_status check_rotation(const int32_t* positions, const float* cos_sin, int64_t max_pos, int rope_dim, int rope_off,
                           dsa_rope_layout layout, int D) {
@@ -403,6 +409,45 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
                                          positions, cos_sin, max_pos, rope_dim, rope_off, layout == DSA_ROPE_HALF, q_out,
                                          ldqo, k_out, ldko, kv, slot_mapping, device_sm_count(),
                                          static_cast<cudaStream_t>(stream)));
+}
+
+size_t dsa_paged_attn_workspace_bytes(int64_t T, int B, int H, int Hkv, int D) {
+  if (check_attn_sizes(T, B, H, Hkv, D) != DSA_OK || T == 0 || B == 0) return 0;
+  return paged_attn_ws_bytes(T, B, H, Hkv, D, device_sm_count());
+}
+
+dsa_status dsa_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* query_start,
+                          const int32_t* context_lens, int B, const int32_t* block_table, int64_t bt_stride,
+                          dsa_kv_cache kv, float softmax_scale, int causal, int window, const float* sink, uint16_t* out,
+                          int64_t ldo, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  dsa_status s = check_attn_sizes(T, B, H, Hkv, D);
+  if (s != DSA_OK) return s;
+  if (T == 0 || B == 0) return DSA_OK;
+  if (window < 0 || bt_stride < 1 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return DSA_ERR_INVALID_ARG;
+  if (q == nullptr || query_start == nullptr || context_lens == nullptr || block_table == nullptr || kv.k == nullptr ||
+      kv.v == nullptr || out == nullptr)
+    return DSA_ERR_INVALID_ARG;
+  if ((s = check_cache(kv, Hkv, D)) != DSA_OK) return s;
+  if (ldq < (int64_t)H * D || ldo < (int64_t)H * D || ldq % 8 != 0 || ldo % 8 != 0 || kv.block_stride % 8 != 0 ||
+      kv.row_stride % 8 != 0 || (Hkv > 1 && kv.head_stride % 8 != 0))
+    return DSA_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv.k, 16) || !aligned(kv.v, 16) || !aligned(out, 16) || !aligned(query_start, 4) ||
+      !aligned(context_lens, 4) || !aligned(block_table, 4) || !aligned(sink, 4) || !aligned(lse, 4))
+    return DSA_ERR_INVALID_ARG;
+  const void* outs[] = {out, lse, ws};
+  const void* in[] = {q, kv.k, kv.v, query_start, context_lens, block_table, sink};
+  for (int i = 0; i < 3; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (int j = 0; j < 7; ++j)
+      if (outs[i] == in[j]) return DSA_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (outs[i] == outs[j]) return DSA_ERR_INVALID_ARG;
+  }
+  const int sms = device_sm_count();
+  if (ws == nullptr || ws_bytes < paged_attn_ws_bytes(T, B, H, Hkv, D, sms) || !aligned(ws, 16)) return DSA_ERR_WORKSPACE;
+  return cuda_status(launch_paged_attn(q, ldq, T, H, Hkv, D, query_start, context_lens, B, block_table, bt_stride, kv,
+                                       softmax_scale, causal != 0, window, sink, out, ldo, lse, ws, sms,
+                                       static_cast<cudaStream_t>(stream)));
 }
 
 size_t dsa_workspace_bytes(dsa_op op, dsa_dtype dtype, dsa_queries qs, int topk) {

@@ -129,6 +129,13 @@ cudaError_t launch_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k
                                 bool halves, void* q_out, int64_t ldqo, void* k_out, int64_t ldko, const dsa_kv_cache& kv,
                                 const int64_t* slot, int num_sms, cudaStream_t stream);
 
+// ------------------------------------------------------------------ attention over a paged cache (paged_attn.cu)
+size_t paged_attn_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms);
+cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* start,
+                              const int32_t* lens, int B, const int32_t* table, int64_t bt_stride, const dsa_kv_cache& kv,
+                              float scale, bool causal, int window, const float* sink, uint16_t* out, int64_t ldo, float* lse,
+                              void* ws, int num_sms, cudaStream_t stream);
+
 // ------------------------------------------------------------------ sparse attention (sparse_attn.cu)
 // q [T, 64, 128] bf16 (16-byte aligned), sel [T, k], the paged mxfp4 cache, sink [64],
 // out [T, 64, 128] fp32.  One CTA per query row.
@@ -167,6 +174,7 @@ DSA_DECLARE_TU_ERROR_ACCESSORS(attn)
 DSA_DECLARE_TU_ERROR_ACCESSORS(slots)
 DSA_DECLARE_TU_ERROR_ACCESSORS(gemm)
 DSA_DECLARE_TU_ERROR_ACCESSORS(rope)
+DSA_DECLARE_TU_ERROR_ACCESSORS(paged_attn)
 
 // Every translation unit's accessors, for dsa_device_error / dsa_set_wait_limit_ns.
 struct TuWords {
@@ -178,7 +186,8 @@ inline const TuWords* all_tu_words(int* n) {
   static const TuWords w[] = {DSA_TU_WORDS(gather), DSA_TU_WORDS(indexer), DSA_TU_WORDS(indexer_bf16_topk),
                               DSA_TU_WORDS(indexer_bf16_logits), DSA_TU_WORDS(indexer_fp8_topk),
                               DSA_TU_WORDS(indexer_fp8_logits), DSA_TU_WORDS(topk), DSA_TU_WORDS(producer),
-                              DSA_TU_WORDS(attn), DSA_TU_WORDS(slots), DSA_TU_WORDS(gemm), DSA_TU_WORDS(rope)};
+                              DSA_TU_WORDS(attn), DSA_TU_WORDS(slots), DSA_TU_WORDS(gemm), DSA_TU_WORDS(rope),
+                              DSA_TU_WORDS(paged_attn)};
   *n = (int)(sizeof(w) / sizeof(w[0]));
   return w;
 }

@@ -1,0 +1,1050 @@
+// Attention of new tokens over a paged bf16 cache (sm_103a).
+//
+// Sequence b has n_b new tokens, rows query_start[b] .. query_start[b + 1] - 1 of q, and L_b keys; its token i sits at
+// position p = L_b - n_b + i.  For query head h of key head h / G (G = H / Hkv), over the visible keys j (j < L_b, with
+// `causal` j <= p, with a window j > p - window):
+//   s_j = scale q . k_j,  out = sum_j e^(s_j - m) v_j / (sum_j e^(s_j - m) + e^(sink - m)),  lse = ln of the denominator.
+//
+// Rows and tiles.  The G query heads of a key head share its keys, so row r of a (sequence, key head) is head r % G of
+// token r / G, and an item is a block of its rows: 256 (two row tiles of 128) or, where sequences bring few rows, 128.
+// Keys come in tiles of 128.  Items lie end to end on a line, each as long as the key tiles that its rows see; the line
+// is cut into equal slices, one per CTA (one CTA per SM).  So a decode batch of any lengths, one long row or a causal
+// prompt load every SM alike.  An item cut by a slice's end leaves its parts (unnormalised sums, maximum, denominator)
+// in the workspace, and combine_kernel adds them in order: results do not depend on timing.
+//
+// In a CTA, two streams alternate on the tensor cores: while one's softmax runs, the other's products do.  With two row
+// tiles each is a stream, and both use every key tile; with one, the streams take the even and the odd key tiles with
+// sums of their own, joined at the item's end.
+//   S_t = Q_t K^T        128 x 128, both operands from shared memory
+//   P_t = 2^(S c - m)    by the stream's four softmax warps, a row per thread: fp32 statistics, P rounded to bf16 and
+//                        written over S in tensor memory; the maximum moves only when a tile exceeds it by more than 8
+//                        in base 2 (P <= 2^8 loses nothing in bf16), and only then are the sums O_t rescaled
+//   O_t += P_t V         A from tensor memory, V as stored (dims contiguous)
+// The denominator sums the unrounded weights: P's rounding (2^-9 of each weight on average, as often up as down) then
+// touches the output as the output's own rounding does, and the lse not at all.
+//
+// Warps: 0-3 and 4-7 softmax, 8-11 loaders (16-byte asynchronous copies, whatever the page size and strides; rows that
+// no query of the item sees are filled with zeros, never read), 12 issues the products.  Tensor memory: S_t 2 x 128
+// columns, O_t 2 x 128.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kKeys = 128;                   // keys per tile
+constexpr int kThreads = 512;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.0f;                // base-2 headroom before the running maximum moves
+constexpr int kPlanMax = 1024;               // items (and sequences) that a CTA plans by itself
+constexpr int kLag = 4;                      // copies a loader has in flight before it waits for the oldest
+
+struct AttnArgs {
+  const uint16_t* q;
+  int64_t ldq;
+  const int32_t* start;        // [B + 1]
+  const int32_t* lens;         // [B]
+  const int32_t* table;        // [B, bt_stride]
+  int64_t bt_stride;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t num_blocks, block_stride, row_stride, head_stride;
+  int64_t cap;                 // keys a block-table row can hold
+  int block_size;
+  int64_t T;
+  int B, H, Hkv, G;
+  int causal, window;          // window 0: none
+  float scale_log2;            // softmax scale in base 2
+  const float* sink;           // nullable
+  uint16_t* out;
+  int64_t ldo;
+  float* lse;                  // nullable
+  // workspace
+  int32_t* meta;               // [CTAs][8]
+  float* ml;                   // [2 * CTAs][rows][2]
+  float* part;                 // [2 * CTAs][rows][D]
+  int64_t* prefix;             // the plan, where it is not made in shared memory
+  int32_t* first;
+  int32_t* seq;
+  int planned;
+  int limit;                   // row blocks there can be: sequences that overlap would bring more
+};
+
+// ------------------------------------------------------------------ items
+struct Seq {
+  int s, n, L;                 // first row of q, new tokens, keys
+};
+
+// What the arguments say of sequence b, or an empty one (`bad`) where that is no range of the T rows.
+__device__ __forceinline__ Seq sequence(const AttnArgs& a, int b, bool& bad) {
+  Seq q;
+  q.s = a.start[b];
+  const int64_t e = a.start[b + 1];
+  q.L = a.lens[b];
+  q.n = (int)(e - q.s);
+  if (q.s < 0 || e < q.s || e > a.T) {
+    bad = true;
+    q.n = 0;
+  }
+  if (q.L < 0) {
+    bad = true;
+    q.L = 0;
+  }
+  return q;
+}
+
+struct Item {
+  int b, s, n, L;
+  int row0, rows;              // rows row0 .. row0 + rows - 1 of the (sequence, key head)
+  int lo, hi;                  // keys that some row sees
+  int tile0, tiles;            // key tiles of [lo, hi)
+};
+
+// Visible keys of the token at position p, as [lo, hi).
+__device__ __forceinline__ int low_key(const AttnArgs& a, int p) {
+  return a.window > 0 ? (int)max((int64_t)p - a.window + 1, (int64_t)0) : 0;
+}
+__device__ __forceinline__ int high_key(const AttnArgs& a, int L, int p) {
+  const int hi = a.causal ? max(0, min(L, p + 1)) : L;
+  return (int)min((int64_t)hi, a.cap);
+}
+
+template <int kRows>
+__device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& q, int b, int block) {
+  Item it;
+  it.b = b, it.s = q.s, it.n = q.n, it.L = q.L;
+  it.row0 = block * kRows;
+  it.rows = min(kRows, q.n * a.G - it.row0);
+  const int i0 = it.row0 / a.G, i1 = (it.row0 + it.rows - 1) / a.G;
+  it.lo = low_key(a, q.L - q.n + i0);
+  it.hi = high_key(a, q.L, q.L - q.n + i1);
+  it.tile0 = it.lo / kKeys;
+  it.tiles = it.hi > it.lo ? (it.hi - 1) / kKeys - it.tile0 + 1 : 0;
+  return it;
+}
+
+// Exclusive prefix sum over the NT threads of the block; returns the sum of the threads before, `total` of all.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_s, int64_t& total) {
+  const int lane = (int)threadIdx.x & 31, w = (int)threadIdx.x >> 5;
+  int64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) warp_s[w] = incl;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 32; ++i) {
+    const int64_t c = warp_s[i];
+    if (i < w) before += c;
+    all += c;
+  }
+  __syncthreads();
+  total = all;
+  return before + incl - v;
+}
+
+// The plan: first[b] = row blocks of the sequences before b; for row block e of sequence seq[e], prefix[e] = key tiles
+// of the row blocks before it (at least one each, so that a block that sees nothing still has its turn).  A row block
+// has an item per key head; these lie side by side on the line, whose length is prefix[count] * Hkv.
+template <int kRows, int NT>
+__device__ int make_plan(const AttnArgs& a, int64_t* prefix, int32_t* first, int32_t* seq, int64_t* warp_s, bool tell) {
+  int64_t carry = 0, total;
+  bool bad = false;
+  for (int b0 = 0; b0 < a.B; b0 += NT) {
+    const int b = b0 + (int)threadIdx.x;
+    int64_t c = 0;
+    if (b < a.B) c = ((int64_t)sequence(a, b, bad).n * a.G + kRows - 1) / kRows;
+    const int64_t before = block_scan<NT>(c, warp_s, total);
+    if (b < a.B) first[b] = (int32_t)min(carry + before, (int64_t)INT32_MAX);
+    carry += total;
+  }
+  __syncthreads();
+  const int count = (int)min(carry, (int64_t)a.limit);
+  if (carry > a.limit) bad = true;
+  carry = 0;
+  for (int e0 = 0; e0 < count; e0 += NT) {
+    const int e = e0 + (int)threadIdx.x;
+    int64_t c = 0;
+    if (e < count) {
+      int lo = 0, hi = a.B;                        // the last sequence with first[b] <= e
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (first[mid] <= e) lo = mid;
+        else hi = mid;
+      }
+      seq[e] = lo;
+      const Seq q = sequence(a, lo, bad);
+      const Item it = make_item<kRows>(a, q, lo, e - first[lo]);
+      c = max(it.tiles, 1);
+      if (it.L > a.cap) bad = true;                // keys past the block table's row
+    }
+    const int64_t before = block_scan<NT>(c, warp_s, total);
+    if (e < count) prefix[e] = carry + before;
+    carry += total;
+  }
+  if (threadIdx.x == 0) prefix[count] = carry;
+  if (tell && bad) raise_error(DSA_DEVERR_INDEX);
+  __syncthreads();
+  return count;
+}
+
+template <int kRows>
+__global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
+  __shared__ int64_t warp_s[32];
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int count = make_plan<kRows, 1024>(a, a.prefix, a.first, a.seq, warp_s, true);
+  if (threadIdx.x == 0) a.meta[7] = count;
+}
+
+// One CTA's pieces of the line, in order.
+struct Pieces {
+  const int64_t* prefix;
+  const int32_t* first;
+  const int32_t* seq;
+  int Hkv, e;
+  int64_t x, end;
+
+  __device__ __forceinline__ void begin(int count, int64_t from, int64_t to) {
+    x = from, end = to;
+    int lo = 0, hi = count;
+    while (hi - lo > 1) {                          // the row block that holds x
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] * Hkv <= x) lo = mid;
+      else hi = mid;
+    }
+    e = lo;
+  }
+};
+
+struct Piece {
+  Item it;
+  int hk;                      // key head
+  int t0, len, cost;           // key tiles t0 .. t0 + len - 1 of the item's `cost`
+};
+
+template <int kRows>
+__device__ __forceinline__ bool next_piece(const AttnArgs& a, Pieces& ps, Piece& p) {
+  if (ps.x >= ps.end) return false;
+  const int64_t base = ps.prefix[ps.e];
+  p.cost = (int)(ps.prefix[ps.e + 1] - base);
+  const uint32_t rem = (uint32_t)(ps.x - base * ps.Hkv);
+  p.hk = (int)(rem / (uint32_t)p.cost);
+  p.t0 = (int)(rem % (uint32_t)p.cost);
+  p.len = (int)min((int64_t)(p.cost - p.t0), ps.end - ps.x);
+  const int b = ps.seq[ps.e];
+  bool bad = false;
+  p.it = make_item<kRows>(a, sequence(a, b, bad), b, ps.e - ps.first[b]);
+  ps.x += p.len;
+  if (p.hk == ps.Hkv - 1 && p.t0 + p.len == p.cost) ++ps.e;
+  return true;
+}
+
+// Whether some row of the item does not see some key of [lo, hi) in key tile `tile`: only there can a value that one row
+// must not see be a factor of the others' zero weights.
+__device__ __forceinline__ bool tile_masked(const AttnArgs& a, const Item& it, int tile) {
+  const int i0 = it.row0 / a.G, i1 = (it.row0 + it.rows - 1) / a.G;
+  const int least_hi = high_key(a, it.L, it.L - it.n + i0), most_lo = low_key(a, it.L - it.n + i1);
+  const int64_t k0 = (int64_t)tile * kKeys;
+  return min(k0 + kKeys, (int64_t)it.hi) > least_hi || k0 < most_lo;
+}
+
+// ------------------------------------------------------------------ tensor memory and barriers
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = 0;
+  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
+  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
+  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// D += A B with A [128 rows][16 elements] in tensor memory: row r in lane r, elements 2c and 2c + 1 in column c.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "{\n tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      " tcgen05.wait::ld.sync.aligned;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Named barrier over n threads that also tells whether all of them are well.
+__device__ __forceinline__ bool all_well(int bar, int n, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.and.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(r)
+      : "r"(bar), "r"(n), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
+// 16 bytes, or zeros where there is nothing to copy (then src is not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
+               "r"(on ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Bits [lo, hi) of a word, for any lo and hi.
+__device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
+  const int l = min(max(lo, 0), 32), h = min(max(hi, 0), 32);
+  const uint32_t below_h = h >= 32 ? ~0u : (1u << h) - 1u, below_l = l >= 32 ? ~0u : (1u << l) - 1u;
+  return below_h & ~below_l;
+}
+
+template <int D, int kTiles>
+struct Shape {
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr uint32_t kTile = 128u * D * 2u;                  // a tile of Q, K or V
+  static constexpr int kStages = (D == 128 ? 4 : 8) + (kTiles == 1 ? 1 : 0) - (D == 64 ? 1 : 0);
+  static constexpr uint32_t kStageOff = kTiles * kTile;
+  static constexpr uint32_t kPlanOff = kStageOff + kStages * kTile;          // prefix, first, seq
+  static constexpr uint32_t kRowOff = kPlanOff + 8 * (kPlanMax + 8) + 4 * kPlanMax * 2;   // key rows [4][128] int64
+  static constexpr uint32_t kMaskOff = kRowOff + 4 * 128 * 8;       // keys that exist [8][4] words
+  static constexpr uint32_t kBadOff = kMaskOff + 8 * 16;            // values that are no numbers, per piece [16]
+  static constexpr uint32_t kStatOff = kBadOff + 64;                // (m, l) of both streams [2][128]
+  static constexpr uint32_t kBarOff = kStatOff + 2048;
+  static constexpr int kBars = 2 * kStages + 2 * 5 + 1;
+  static constexpr uint32_t kCtlOff = kBarOff + 8 * 32;             // abort, TMEM base
+  static constexpr uint32_t kScanOff = kCtlOff + 16;
+  static constexpr size_t kSmem = 1024 + kScanOff + 16 * 8;
+  static_assert(kBars <= 32 && kStages <= 8 && kSmem <= 232448, "shared memory");
+};
+
+template <int D, int kTiles>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ AttnArgs a) {
+  using Sh = Shape<D, kTiles>;
+  constexpr int kStages = Sh::kStages, kRows = Sh::kRows;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sm32 = smem_u32(sm);
+  int64_t* prefix_s = reinterpret_cast<int64_t*>(sm + Sh::kPlanOff);
+  int32_t* first_s = reinterpret_cast<int32_t*>(prefix_s + kPlanMax + 8);
+  int32_t* seq_s = first_s + kPlanMax;
+  int64_t* rows_s = reinterpret_cast<int64_t*>(sm + Sh::kRowOff);
+  uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Sh::kMaskOff);
+  volatile int* bad_s = reinterpret_cast<volatile int*>(sm + Sh::kBadOff);
+  float2* stat_s = reinterpret_cast<float2*>(sm + Sh::kStatOff);
+  int* ctl = reinterpret_cast<int*>(sm + Sh::kCtlOff);
+  volatile int* abort_flag = ctl;
+  const uint32_t bars = sm32 + Sh::kBarOff;
+  // barrier numbers: stages full, stages empty, then per stream
+  constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2, kSFull = kQFree + 2,
+                kPFull = kSFull + 2, kODone = kPFull + 2, kDrain = kODone + 2;
+  auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
+
+  const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
+  const unsigned long long limit = wait_limit_ns();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(kFull + i), 128);
+      mbar_init(bar(kEmpty + i), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(kQFull + t), 128);
+      mbar_init(bar(kQFree + t), 1);
+      mbar_init(bar(kSFull + t), 1);
+      mbar_init(bar(kPFull + t), 4);
+      mbar_init(bar(kODone + t), 1);
+    }
+    mbar_init(bar(kDrain), 1);
+    ctl[0] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 12) tmem_alloc(smem_u32(ctl + 1), 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)ctl[1];
+  grid_launch_dependents();
+  grid_dependency_wait();
+
+  // the plan, and this CTA's slice of the line
+  Pieces ps;
+  ps.Hkv = a.Hkv;
+  int count;
+  if (a.planned) {
+    ps.prefix = a.prefix, ps.first = a.first, ps.seq = a.seq;
+    count = *reinterpret_cast<volatile int32_t*>(a.meta + 7);
+  } else {
+    count = make_plan<kRows, kThreads>(a, prefix_s, first_s, seq_s, reinterpret_cast<int64_t*>(sm + Sh::kScanOff), blockIdx.x == 0);
+    ps.prefix = prefix_s, ps.first = first_s, ps.seq = seq_s;
+  }
+  const int64_t C = gridDim.x, c = blockIdx.x;
+  const int64_t line = count > 0 ? ps.prefix[count] * a.Hkv : 0;
+  ps.begin(count, line * c / C, line * (c + 1) / C);
+
+  if (warp < 8) {
+    // ================================ softmax ================================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    const int t = warp >> 2;                       // stream
+    const int r = 32 * (warp & 3) + lane;          // row in its tile = TMEM lane
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t tS = tl + 128u * (uint32_t)t, tO = tl + 256u + 128u * (uint32_t)t;
+    uint32_t jobs = 0;                             // of this stream so far
+    uint32_t tiles_before = 0;                     // key tiles of the pieces before
+    bool ok = true;
+    int32_t* my_meta = a.meta + 8 * (c + 1);
+    if (threadIdx.x == 0) {
+      my_meta[0] = 0;
+      my_meta[6] = ps.end > ps.x;                  // whether it has any of the line
+    }
+    Piece p;
+    uint32_t np = 0;                               // pieces so far that see any key
+    while (ok && next_piece<kRows>(a, ps, p)) {
+      const Item& it = p.it;
+      const int row = (kTiles == 2 ? 128 * t : 0) + r;             // row of the item
+      const bool live = row < it.rows;
+      const int gr = it.row0 + (live ? row : 0);
+      const int token = gr / a.G, head = p.hk * a.G + gr % a.G;
+      const int pos = it.L - it.n + token;
+      const int lo = low_key(a, pos), hi = high_key(a, it.L, pos);
+      const bool warp_live = (kTiles == 2 ? 128 * t : 0) + 32 * (warp & 3) < it.rows;
+      const bool empty = it.tiles == 0;
+      const int step = kTiles == 2 ? 1 : 2, j0 = kTiles == 2 ? 0 : t;
+      const int mine = empty ? 0 : kTiles == 2 ? (128 * t < it.rows ? p.len : 0) : (p.len + 1 - t) / 2;   // jobs
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; ok && i < mine; ++i, ++jobs) {
+        const int j = j0 + step * i;
+        ok = mbar_wait(bar(kSFull + t), jobs & 1u, limit, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (warp_live) {
+          tc_fence_after();
+          uint32_t s0[64], s1[64];
+          tmem_ld64_issue(tS, s0);
+          tmem_ld64_issue(tS + 64u, s1);
+          tmem_ld64_wait(s0);
+          tmem_ld64_wait(s1);
+          const int k0 = (it.tile0 + p.t0 + j) * kKeys;
+          const uint4 have = *reinterpret_cast<const uint4*>(mask_s + 4 * ((tiles_before + (uint32_t)j) & 7u));
+          const uint32_t w0 = have.x & bits_between(lo - k0, hi - k0), w1 = have.y & bits_between(lo - k0 - 32, hi - k0 - 32),
+                         w2 = have.z & bits_between(lo - k0 - 64, hi - k0 - 64), w3 = have.w & bits_between(lo - k0 - 96, hi - k0 - 96);
+          if (__any_sync(0xFFFFFFFFu, (w0 & w1 & w2 & w3) != ~0u)) {
+            const uint32_t none = __float_as_uint(-INFINITY);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              s0[e] = (w0 >> e) & 1u ? s0[e] : none;
+              s0[32 + e] = (w1 >> e) & 1u ? s0[32 + e] : none;
+              s1[e] = (w2 >> e) & 1u ? s1[e] : none;
+              s1[32 + e] = (w3 >> e) & 1u ? s1[32 + e] : none;
+            }
+          }
+          float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 64; e += 4) {
+            x0 = fmaxf(fmaxf(x0, __uint_as_float(s0[e])), __uint_as_float(s1[e]));
+            x1 = fmaxf(fmaxf(x1, __uint_as_float(s0[e + 1])), __uint_as_float(s1[e + 1]));
+            x2 = fmaxf(fmaxf(x2, __uint_as_float(s0[e + 2])), __uint_as_float(s1[e + 2]));
+            x3 = fmaxf(fmaxf(x3, __uint_as_float(s0[e + 3])), __uint_as_float(s1[e + 3]));
+          }
+          const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2;
+          const bool moves = mt > m + kLazy;
+          const float f = moves ? ex2(m - mt) : 1.f;
+          if (moves) {
+            m = mt;
+            l *= f;
+          }
+          if (i > 0 && __any_sync(0xFFFFFFFFu, moves)) {
+            // the products of the job before have added to O
+            ok = mbar_wait(bar(kODone + t), (jobs - 1) & 1u, limit, abort_flag);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int cc = 0; cc < D; cc += 32) {
+              uint32_t o[32];
+              tmem_ld32(tO + (uint32_t)cc, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st32(tO + (uint32_t)cc, o);
+            }
+          }
+          const float mm = m == -INFINITY ? 0.f : m;
+          float l0 = 0.f, l1 = 0.f;
+          uint32_t pw[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float pa = ex2(fmaf(__uint_as_float(s0[2 * e]), a.scale_log2, -mm));
+            const float pb = ex2(fmaf(__uint_as_float(s0[2 * e + 1]), a.scale_log2, -mm));
+            l0 += pa;
+            l1 += pb;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(pa, pb);
+            pw[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st32(tS, pw);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float pa = ex2(fmaf(__uint_as_float(s1[2 * e]), a.scale_log2, -mm));
+            const float pb = ex2(fmaf(__uint_as_float(s1[2 * e + 1]), a.scale_log2, -mm));
+            l0 += pa;
+            l1 += pb;
+            const __nv_bfloat162 h = __floats2bfloat162_rn(pa, pb);
+            pw[e] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st32(tS + 32u, pw);
+          l += l0 + l1;
+          tmem_st_wait();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPFull + t));
+      }
+      // ---- the item's rows (or its part of them)
+      const bool whole = p.t0 == 0 && p.len == p.cost;
+      const int slot = p.t0 == 0 ? 2 * (int)c + 1 : 2 * (int)c;
+      if (!whole && p.t0 == 0 && threadIdx.x == 0) {               // the item's first part: it owns the sum
+        const int64_t last = ps.x - p.len + p.cost - 1;            // the line's last position of the item
+        my_meta[1] = it.b, my_meta[2] = it.row0, my_meta[3] = it.rows, my_meta[4] = p.hk;
+        my_meta[5] = (int)(((last + 1) * C - 1) / line);           // the CTA that holds it
+        my_meta[0] = 1;
+      }
+      if (ok && mine > 0) {
+        ok = mbar_wait(bar(kODone + t), (jobs - 1) & 1u, limit, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+      }
+      float m2 = -INFINITY, l2 = 0.f;                              // the other stream's
+      bool other = false;
+      if constexpr (kTiles == 1) {
+        stat_s[128 * t + r] = make_float2(m, l);
+        ok = all_well(2, 256, ok);
+        if (!ok) break;
+        const float2 o = stat_s[128 * (t ^ 1) + r];
+        m2 = o.x, l2 = o.y;
+        other = !empty && p.len > 1;                               // both streams had tiles
+      }
+      if (!ok) break;
+      tc_fence_after();
+      if (warp_live) {
+        // weights of the two streams' sums, and the joint statistics
+        const float M = fmaxf(m, m2);
+        float f = 1.f, f2 = 0.f;
+        if (kTiles == 1) {
+          f = M == -INFINITY ? 1.f : ex2(m - M);
+          f2 = M == -INFINITY ? 1.f : ex2(m2 - M);
+          l = l * f + l2 * f2;
+          m = M;
+        }
+        const float sn = a.sink != nullptr ? a.sink[head] : -INFINITY, sk = sn * kLog2e;
+        float inv = 1.f;
+        if (whole) {
+          const float top = fmaxf(m, sk);
+          if (top == -INFINITY && !(l != l)) {
+            inv = 0.f;
+            l = -INFINITY;                                         // lse
+          } else {
+            const float g = ex2(m - top), den = l * g + ex2(sk - top);
+            inv = g / den;
+            l = (sk >= m ? sn : m * kLn2) + logf(den);
+          }
+          if (a.lse != nullptr && live && (kTiles == 2 || t == 0)) a.lse[(int64_t)(it.s + token) * a.H + head] = l;
+        } else if (live && (kTiles == 2 || t == 0)) {
+          reinterpret_cast<float2*>(a.ml)[(int64_t)slot * kRows + row] = make_float2(m, l);
+        }
+        f *= inv, f2 *= inv;
+        const bool bad = !empty && bad_s[np & 15u] != 0;
+        constexpr int kCols = kTiles == 2 ? D : D / 2;             // of this warp; one row tile: half each
+        const int c0 = kTiles == 2 ? 0 : t * kCols;
+        // which sums exist: with one tile the second stream has none
+        const bool has0 = !empty, has1 = other;
+#pragma unroll
+        for (int cc = 0; cc < kCols; cc += 32) {
+          float o[32];
+          {
+            uint32_t w[32];
+            if (has0) {
+              tmem_ld32(kTiles == 2 ? tO + (uint32_t)cc : tl + 256u + (uint32_t)(c0 + cc), w);
+              const float g = kTiles == 2 || t == 0 ? f : f2;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(w[e]) * g;
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            }
+            if (kTiles == 1 && has1) {
+              tmem_ld32(tl + 384u + (uint32_t)(c0 + cc), w);
+              const float g = t == 0 ? f2 : f;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(w[e]), g, o[e]);
+            }
+          }
+          if (bad && live) {
+            // values that are no numbers were taken out of the tiles that some row sees in part: the rows that see them
+            // get them back, as sums with them give
+            for (int j = 0; j < p.len; ++j) {
+              const int tile = it.tile0 + p.t0 + j;
+              if (!tile_masked(a, it, tile)) continue;
+              for (int64_t key = max((int64_t)tile * kKeys, (int64_t)lo); key < min((int64_t)(tile + 1) * kKeys, (int64_t)hi); ++key) {
+                const int blk = a.table[it.b * a.bt_stride + key / a.block_size];
+                if (blk < 0 || blk >= a.num_blocks) continue;
+                const uint16_t* v = a.v + blk * a.block_stride + key % a.block_size * a.row_stride + p.hk * a.head_stride + c0 + cc;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if ((v[e] & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float((uint32_t)v[e] << 16);
+              }
+            }
+          }
+          if (live) {
+            if (whole) {
+              uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)(it.s + token) * a.ldo + (int64_t)head * D + c0 + cc);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __nv_bfloat162 h = __floats2bfloat162_rn(o[e + 2 * i], o[e + 2 * i + 1]);
+                  w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(a.part + ((int64_t)slot * kRows + row) * D + c0 + cc);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+      }
+      if constexpr (kTiles == 1) ok = all_well(2, 256, ok);       // both streams' sums have been read
+      if (!empty) {
+        tiles_before += (uint32_t)p.len;
+        ++np;
+      }
+    }
+    if (!ok && lane == 0) {
+      raise_error(DSA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  } else if (warp < 12) {
+    // ================================ loaders ================================
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    const int lt = (int)threadIdx.x - 256;
+    constexpr int kPer = D / 8;                    // 16-byte pieces of a row
+    constexpr int kStep = 128 / kPer;              // rows of a pass
+    const int pc = lt % kPer, r0 = lt / kPer;      // the thread's piece, and its first row
+    const uint32_t dst0 = (uint32_t)(pc >> 3) * 16384u + (uint32_t)r0 * 128u + (uint32_t)(((pc & 7) ^ (r0 & 7)) << 4);
+    uint32_t loads = 0, qloads[2] = {0, 0}, tiles = 0;
+    bool ok = true;
+    // copies in flight, oldest in the low bits: barrier number, and for values 0x80 + 0x100 * stage where they are looked
+    // through when they have landed
+    uint64_t fifo = 0;
+    int flying = 0;
+    uint32_t np = 0;
+    auto landed = [&]() {                          // the oldest copy of this thread is complete
+      const uint32_t op = (uint32_t)fifo & 0xFFFFu;
+      fifo >>= 16;
+      --flying;
+      if (op & 0x80u) {
+        uint8_t* at = sm + Sh::kStageOff + (op >> 8 & 7u) * Sh::kTile + dst0;
+        bool found = false;
+#pragma unroll 4
+        for (int i = 0; i < 128 / kStep; ++i) {
+          uint4 w = *reinterpret_cast<uint4*>(at + i * kStep * 128);
+          uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+          bool here = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if ((ww[e] & 0x7F80u) == 0x7F80u) ww[e] &= 0xFFFF0000u, here = true;
+            if ((ww[e] & 0x7F800000u) == 0x7F800000u) ww[e] &= 0x0000FFFFu, here = true;
+          }
+          if (here) *reinterpret_cast<uint4*>(at + i * kStep * 128) = w;
+          found |= here;
+        }
+        if (found) bad_s[op >> 11 & 15u] = 1;
+      }
+      proxy_fence();
+      mbar_arrive(bar((int)(op & 0x3Fu)));
+    };
+    auto land_all = [&]() {
+      copies_wait<0>();
+      while (flying > 0) landed();
+    };
+    // room for one more copy in `where`: before a wait that may be long, everything in flight is passed on
+    auto free_wait = [&](int which, uint32_t parity) {
+      if (!ok || mbar_try_wait(bar(which), parity)) return;
+      land_all();
+      ok = mbar_wait(bar(which), parity, limit, abort_flag);
+    };
+    auto sent = [&](uint32_t op) {
+      copies_commit();
+      fifo |= (uint64_t)op << (16 * flying);
+      ++flying;
+    };
+    auto make_room = [&]() {
+      if (flying == kLag) {
+        copies_wait<kLag - 1>();
+        landed();
+      }
+    };
+    Piece p;
+    while (next_piece<kRows>(a, ps, p)) {
+      const Item& it = p.it;
+      if (it.tiles == 0) continue;
+      const int nq = kTiles == 2 && it.rows > 128 ? 2 : 1;
+      for (int t = 0; t < nq; ++t) {
+        free_wait(kQFree + t, (qloads[t] & 1u) ^ 1u);
+        make_room();
+        if (ok) {
+          const uint32_t dst = sm32 + (uint32_t)t * Sh::kTile + dst0;
+#pragma unroll 4
+          for (int i = 0; i < 128 / kStep; ++i) {
+            const int row = 128 * t + r0 + i * kStep;
+            const bool on = row < it.rows;
+            const uint32_t gr = (uint32_t)(it.row0 + (on ? row : 0));
+            const uint32_t token = gr / (uint32_t)a.G, g = gr % (uint32_t)a.G;
+            copy16(dst + (uint32_t)i * kStep * 128u,
+                   a.q + (int64_t)(it.s + (int)token) * a.ldq + (int64_t)(p.hk * a.G + (int)g) * D + pc * 8, on);
+          }
+          sent((uint32_t)(kQFull + t));
+        }
+        ++qloads[t];
+      }
+      const int first = it.tile0 + p.t0;
+      const int32_t* table = a.table + (int64_t)it.b * a.bt_stride;
+      // the block of this thread's key of a tile; keys that no row sees have none
+      auto block_of = [&](int j) {
+        const int64_t key = (int64_t)(first + j) * kKeys + lt;
+        return j < p.len && key >= it.lo && key < it.hi ? table[(uint32_t)key / (uint32_t)a.block_size] : -1;
+      };
+      int blk = block_of(0);
+      bool left = false;
+      // the rows of key tile j, resolved by a thread each
+      auto rows_of = [&](int j) {
+        const int64_t key = (int64_t)(first + j) * kKeys + lt;
+        const bool seen = key >= it.lo && key < it.hi;
+        const bool have = seen && blk >= 0 && blk < a.num_blocks;
+        if (seen && !have) raise_error(DSA_DEVERR_INDEX);
+        const uint32_t at = (tiles + (uint32_t)j);
+        rows_s[(at & 3u) * 128u + (uint32_t)lt] =
+            have ? blk * a.block_stride + (int64_t)((uint32_t)key % (uint32_t)a.block_size) * a.row_stride + p.hk * a.head_stride : -1;
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, have);
+        if (lane == 0) mask_s[4 * (at & 7u) + (uint32_t)(warp & 3)] = word;
+        if (j == 0 && lt == 0) bad_s[np & 15u] = 0;
+        blk = block_of(j + 1);
+        ok = all_well(1, 128, ok);
+      };
+      auto copy_tile = [&](const uint16_t* base, int j, uint32_t op) {
+        const int s = (int)(loads % kStages);
+        free_wait(kEmpty + s, (loads / kStages & 1u) ^ 1u);
+        make_room();
+        if (ok) {
+          const int64_t* rows = rows_s + ((tiles + (uint32_t)j) & 3u) * 128u + r0;
+          const uint32_t dst = sm32 + Sh::kStageOff + (uint32_t)s * Sh::kTile + dst0;
+#pragma unroll 8
+          for (int i = 0; i < 128 / kStep; ++i) {
+            const int64_t o = rows[i * kStep];
+            copy16(dst + (uint32_t)i * kStep * 128u, base + (o < 0 ? 0 : o) + pc * 8, o >= 0);
+          }
+          sent((uint32_t)(kFull + s) | (op ? 0x80u | (uint32_t)s << 8 | (np & 15u) << 11 : 0u));
+        }
+        ++loads;
+      };
+      auto values = [&](int j) { copy_tile(a.v, j, tile_masked(a, it, first + j) ? 1u : 0u); };
+      if constexpr (kTiles == 2) {
+        for (int j = 0; j < p.len; ++j) {
+          rows_of(j);
+          if (!ok) {
+            left = true;
+            break;
+          }
+          copy_tile(a.k, j, 0u);
+          values(j);
+        }
+      } else {                                     // keys two tiles ahead of the values
+        for (int j = 0; j < p.len + 2; ++j) {
+          if (j < p.len) {
+            if (j >= 2) values(j - 2);
+            rows_of(j);
+            if (!ok) {
+              left = true;
+              break;
+            }
+            copy_tile(a.k, j, 0u);
+          } else if (j >= 2) {
+            values(j - 2);
+          }
+        }
+      }
+      if (left) break;
+      tiles += (uint32_t)p.len;
+      ++np;
+    }
+    land_all();
+    if (!ok && lane == 0) {
+      raise_error(DSA_DEVERR_TIMEOUT);
+      *abort_flag = 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    if (warp == 12 && lane == 0) {
+      // ================================ products ================================
+      constexpr uint32_t kIdescS = idesc_bf16(128, 128), kIdescO = idesc_bf16(128, D) | (1u << 16);   // V: dims contiguous
+      uint32_t base = 0, qs[2] = {0, 0}, jobs[2] = {0, 0};
+      bool ok = true;
+      Piece p;
+      while (ok && next_piece<kRows>(a, ps, p)) {
+        if (p.it.tiles == 0) continue;
+        const int act = kTiles == 2 && p.it.rows <= 128 ? 1 : 2;   // streams in turn
+        const int turns = kTiles == 2 ? p.len * act : p.len;
+        // turn u: which stream and key tile; loads come in the order K0 V0 K1 V1 .. or K0 K1 V0 K2 V1 ..
+        auto stream = [&](int u) { return act == 2 ? u & 1 : 0; };
+        auto tile = [&](int u) { return kTiles == 2 ? (act == 2 ? u >> 1 : u) : u; };
+        auto k_load = [&](int j) { return base + (uint32_t)(kTiles == 2 ? 2 * j : j < 2 ? j : 2 * j - 1); };
+        auto v_load = [&](int j) { return base + (uint32_t)(kTiles == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * p.len - 1)); };
+        auto scores = [&](int u) {
+          const int t = stream(u), j = tile(u), tq = kTiles == 2 ? t : 0;
+          const uint32_t ld = k_load(j), s = ld % kStages;
+          if (u < 2) {                             // the item's queries
+            if (!mbar_wait(bar(kQFull + tq), qs[tq] & 1u, limit, abort_flag)) return false;
+          }
+          if (!mbar_wait(bar(kFull + (int)s), ld / kStages & 1u, limit, abort_flag)) return false;
+          tc_fence_after();
+          const uint32_t qa = sm32 + (uint32_t)tq * Sh::kTile, ka = sm32 + Sh::kStageOff + s * Sh::kTile;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
+            mma_bf16(tmem + 128u * (uint32_t)t, desc_sw128(qa + off, 16u, 1024u), desc_sw128(ka + off, 16u, 1024u), kIdescS,
+                     kk > 0 ? 1u : 0u);
+          }
+          mma_commit(bar(kSFull + t));
+          if (kTiles == 1 || t == act - 1) mma_commit(bar(kEmpty + (int)s));
+          if (kTiles == 2 ? j == p.len - 1 : u == turns - 1) mma_commit(bar(kQFree + tq));
+          return true;
+        };
+        for (int u = 0; ok && u < act && u < turns; ++u) ok = scores(u);
+        for (int u = 0; ok && u < turns; ++u) {
+          const int t = stream(u), j = tile(u);
+          const uint32_t ld = v_load(j), s = ld % kStages;
+          ok = mbar_wait(bar(kPFull + t), jobs[t] & 1u, limit, abort_flag) &&
+               mbar_wait(bar(kFull + (int)s), ld / kStages & 1u, limit, abort_flag);
+          if (!ok) break;
+          ++jobs[t];
+          tc_fence_after();
+          const uint32_t va = sm32 + Sh::kStageOff + s * Sh::kTile;
+          const bool fresh = u < act;              // the stream's first tile of the item
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_bf16_ta(tmem + 256u + 128u * (uint32_t)t, tmem + 128u * (uint32_t)t + 8u * (uint32_t)kk,
+                        desc_sw128(va + (uint32_t)kk * 2048u, 16384u, 1024u), kIdescO, fresh && kk == 0 ? 0u : 1u);
+          mma_commit(bar(kODone + t));
+          if (kTiles == 1 || t == act - 1) mma_commit(bar(kEmpty + (int)s));
+          if (u + act < turns) ok = scores(u + act);
+        }
+        base += 2u * (uint32_t)p.len;
+        ++qs[0];
+        if (kTiles == 2 && act == 2) ++qs[1];
+      }
+      if (!ok) {
+        raise_error(DSA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      mma_commit(bar(kDrain));                     // everything issued has completed
+      mbar_wait(bar(kDrain), 0u, kCleanupWaitNs, nullptr);
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// Adds the parts of the items that slice ends have cut, in the order of their keys:
+//   M = max(m_p, sink), out = sum_p 2^(m_p - M) O_p / (sum_p 2^(m_p - M) l_p + 2^(sink - M)).
+// Block c: the item whose first part is CTA c's (at most one); a warp per row.
+template <int D, int kRows>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a, int C) {
+  grid_launch_dependents();
+  grid_dependency_wait();
+  const int c = (int)blockIdx.x;
+  const int32_t* meta = a.meta + 8 * (c + 1);
+  if (meta[0] == 0) return;
+  const int b = meta[1], row0 = meta[2], rows = meta[3], hk = meta[4], last = meta[5];
+  const int lane = (int)threadIdx.x & 31;
+  for (int row = (int)(blockIdx.y * 8 + (threadIdx.x >> 5)); row < rows; row += (int)gridDim.y * 8) {
+    const int token = (row0 + row) / a.G, head = hk * a.G + (row0 + row) % a.G;
+    const float sn = a.sink != nullptr ? a.sink[head] : -INFINITY, sk = sn * kLog2e;
+    const float2* ml = reinterpret_cast<const float2*>(a.ml);
+    // a CTA without a piece (more CTAs than tiles) has left nothing: its slot is marked
+    auto slot_of = [&](int p) { return p == c ? 2 * c + 1 : 2 * p; };
+    float M = sk;
+    for (int p = c; p <= last; ++p) {
+      if (p > c && a.meta[8 * (p + 1) + 6] == 0) continue;
+      M = fmaxf(M, ml[(int64_t)slot_of(p) * kRows + row].x);
+    }
+    float acc[D / 32], den = M == -INFINITY ? 0.f : ex2(sk - M);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+    for (int p = c; p <= last; ++p) {
+      if (p > c && a.meta[8 * (p + 1) + 6] == 0) continue;
+      const float2 s = ml[(int64_t)slot_of(p) * kRows + row];
+      const float f = M == -INFINITY ? 1.f : ex2(s.x - M);
+      den = fmaf(s.y, f, den);
+      const float* o = a.part + ((int64_t)slot_of(p) * kRows + row) * D + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(o[e], f, acc[e]);
+    }
+    const int s0 = a.start[b];
+    const bool none = M == -INFINITY && !(den != den);
+    const float inv = none ? 0.f : 1.f / den;
+    uint16_t* dst = a.out + (int64_t)(s0 + token) * a.ldo + (int64_t)head * D + lane * (D / 32);
+#pragma unroll
+    for (int e = 0; e < D / 32; e += 2)
+      *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+    if (a.lse != nullptr && lane == 0) a.lse[(int64_t)(s0 + token) * a.H + head] = none ? -INFINITY : (sk >= M ? sn : M * kLn2) + logf(den);
+  }
+}
+
+struct Layout {
+  int tiles, rows, ctas;
+  bool planned;
+  int64_t blocks;
+  size_t meta, ml, part, prefix, first, seq, total;
+};
+
+// Two row tiles where a sequence brings more than one on average: each key tile then feeds twice the products.
+Layout layout(int64_t T, int B, int H, int Hkv, int D, int num_sms) {
+  Layout y{};
+  const int64_t G = H / Hkv;
+  y.tiles = T * G > 128 * (int64_t)B ? 2 : 1;
+  y.rows = 128 * y.tiles;
+  y.ctas = num_sms;
+  const int64_t blocks = T * G / y.rows + (B < T ? B : T);        // at most so many row blocks
+  y.blocks = blocks;
+  y.planned = blocks > kPlanMax || B > kPlanMax;
+  const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
+  y.meta = 0;
+  y.ml = up(32 * (size_t)(y.ctas + 1));
+  y.part = y.ml + up((size_t)2 * y.ctas * y.rows * 8);
+  y.prefix = y.part + up((size_t)2 * y.ctas * y.rows * D * 4);
+  y.first = y.prefix + (y.planned ? up(8 * (size_t)(blocks + 1)) : 0);
+  y.seq = y.first + (y.planned ? up(4 * (size_t)B) : 0);
+  y.total = y.seq + (y.planned ? up(4 * (size_t)blocks) : 0);
+  return y;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+template <int D, int kTiles>
+cudaError_t launch_shape(const AttnArgs& a, int ctas, cudaStream_t stream) {
+  using Sh = Shape<D, kTiles>;
+  auto kernel = paged_attn_kernel<D, kTiles>;
+  static std::atomic<unsigned long long> ready{0};               // devices on which the kernel is set up
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1u)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, kernel);
+    if (e != cudaSuccess) return e;
+    // the warps' shares, 2 x 192 + 80 + 48 registers a thread, are those of the launch
+    if (fa.numRegs * kThreads < 128 * (2 * 192 + 80 + 48)) return cudaErrorInvalidConfiguration;
+    if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+  }
+  if (a.planned) {
+    e = launch_pdl(plan_kernel<Sh::kRows>, dim3(1), 1024u, 0, stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  e = launch_pdl(kernel, dim3((unsigned)ctas), (unsigned)kThreads, Sh::kSmem, stream, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(combine_kernel<D, Sh::kRows>, dim3((unsigned)ctas, kTiles == 2 ? 8 : 2), 256u, 0, stream, a, ctas);
+}
+
+}  // namespace
+
+size_t paged_attn_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms) { return layout(T, B, H, Hkv, D, num_sms).total; }
+
+cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* start,
+                              const int32_t* lens, int B, const int32_t* table, int64_t bt_stride, const dsa_kv_cache& kv,
+                              float scale, bool causal, int window, const float* sink, uint16_t* out, int64_t ldo, float* lse,
+                              void* ws, int num_sms, cudaStream_t stream) {
+  const Layout y = layout(T, B, H, Hkv, D, num_sms);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  AttnArgs a{};
+  a.q = q, a.ldq = ldq, a.start = start, a.lens = lens, a.table = table, a.bt_stride = bt_stride;
+  a.k = static_cast<const uint16_t*>(kv.k), a.v = static_cast<const uint16_t*>(kv.v);
+  a.num_blocks = kv.num_blocks, a.block_stride = kv.block_stride, a.row_stride = kv.row_stride, a.head_stride = kv.head_stride;
+  a.block_size = kv.block_size;
+  a.cap = bt_stride > INT32_MAX / kv.block_size ? INT32_MAX : bt_stride * kv.block_size;
+  a.T = T, a.B = B, a.H = H, a.Hkv = Hkv, a.G = H / Hkv;
+  a.causal = causal, a.window = window;
+  a.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  a.sink = sink, a.out = out, a.ldo = ldo, a.lse = lse;
+  a.meta = reinterpret_cast<int32_t*>(w + y.meta);
+  a.ml = reinterpret_cast<float*>(w + y.ml);
+  a.part = reinterpret_cast<float*>(w + y.part);
+  a.prefix = reinterpret_cast<int64_t*>(w + y.prefix);
+  a.first = reinterpret_cast<int32_t*>(w + y.first);
+  a.seq = reinterpret_cast<int32_t*>(w + y.seq);
+  a.planned = y.planned;
+  a.limit = (int)y.blocks;
+  if (D == 128) return y.tiles == 2 ? launch_shape<128, 2>(a, y.ctas, stream) : launch_shape<128, 1>(a, y.ctas, stream);
+  return y.tiles == 2 ? launch_shape<64, 2>(a, y.ctas, stream) : launch_shape<64, 1>(a, y.ctas, stream);
+}
+
+DSA_DEFINE_TU_ERROR_ACCESSORS(paged_attn)
+
+}  // namespace dsa

@@ -121,6 +121,10 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "dsa_qk_norm_rope": (c_int, [c_void_p, c_int64, c_int, c_void_p, c_int64, c_int, c_void_p, c_int64, c_int64, c_int,
                                      c_int, c_void_p, c_void_p, c_float, c_void_p, c_void_p, c_int64, c_int, c_int, c_int,
                                      c_void_p, c_int64, c_void_p, c_int64, dsa_kv_cache, c_void_p, c_void_p]),
+        "dsa_paged_attn_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int]),
+        "dsa_paged_attn": (c_int, [c_void_p, c_int64, c_int64, c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_void_p,
+                                   c_int64, dsa_kv_cache, c_float, c_int, c_int, c_void_p, c_void_p, c_int64, c_void_p,
+                                   c_void_p, c_size_t, c_void_p]),
         "dsa_workspace_bytes": (c_size_t, [c_int, c_int, dsa_queries, c_int]),
         "dsa_status_string": (ctypes.c_char_p, [c_int]),
         "dsa_device_error": (c_int, [c_void_p]),
@@ -305,6 +309,18 @@ def dsa_qk_norm_rope(q, ldq, H, k, ldk, Hkv, v, ldv, T, D, type, gamma_q, gamma_
                                    _ptr(cos_sin), int(max_pos), int(rope_dim), int(rope_off), int(layout), _ptr(q_out),
                                    int(ldqo), _ptr(k_out), int(ldko), kv, _ptr(slot_mapping), _stream(stream)),
            "dsa_qk_norm_rope")
+
+
+def dsa_paged_attn_workspace_bytes(T, B, H, Hkv, D) -> int:
+    return int(load().dsa_paged_attn_workspace_bytes(int(T), int(B), int(H), int(Hkv), int(D)))
+
+
+def dsa_paged_attn(q, ldq, T, H, Hkv, D, query_start, context_lens, B, block_table, bt_stride, kv, softmax_scale, causal,
+                   window, sink, out, ldo, lse, ws, ws_bytes, stream=None):
+    _check(load().dsa_paged_attn(_ptr(q), int(ldq), int(T), int(H), int(Hkv), int(D), _ptr(query_start),
+                                 _ptr(context_lens), int(B), _ptr(block_table), int(bt_stride), kv, float(softmax_scale),
+                                 1 if causal else 0, int(window), _ptr(sink), _ptr(out), int(ldo), _ptr(lse), _ptr(ws),
+                                 int(ws_bytes), _stream(stream)), "dsa_paged_attn")
 
 
 def dsa_workspace_bytes(op, dtype, qs, topk) -> int:

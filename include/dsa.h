@@ -481,6 +481,48 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
                             dsa_kv_cache kv, const int64_t* slot_mapping, void* stream);
 
 /*
+ * dsa_paged_attn -- attention of new tokens over a paged cache.  Sequence b brings the rows
+ * t = query_start[b] .. query_start[b + 1] - 1 of q (n_b of them: one for a decode step, any
+ * number for a chunk of a prompt) and has L_b = context_lens[b] keys in the cache, the new
+ * tokens' own among them: token i of the n_b sits at position p = L_b - n_b + i.  It sees the
+ * keys j < L_b with j <= p (causal != 0) and j > p - window (window > 0).  For query head h,
+ * with key head h / (H / Hkv):
+ *   s_j = softmax_scale * q[t,h,:] . k_j,
+ *   out[t,h,:] = sum_j e^(s_j - m) v_j / (sum_j e^(s_j - m) + e^(sink[h] - m)),
+ *   lse[t,h] = ln(sum_j e^(s_j) + e^(sink[h])),
+ * m any shift.  A row that sees nothing gives zeros, and lse the sink (-inf without one).
+ *  q        [T, H, D] bf16 bit patterns, tokens ldq elements apart, heads D apart; out the same
+ *           with ldo.  Rows of q that belong to no sequence (past query_start[B], or in a gap)
+ *           are not read, and their rows of out and lse are left as they are.
+ *  query_start [B + 1] int32, ascending, as dsa_assign_slots writes it; context_lens [B] int32.
+ *  block_table [B, bt_stride] int32; kv the cache (see dsa_kv_cache); block_size any >= 1.
+ *           Entries of pages that hold no visible key are not read (with a window the old
+ *           pages of a sequence may be gone).
+ *  sink     [H] fp32 logits that join the denominators, nullable.  lse [T, H] fp32, nullable.
+ *  ws       dsa_paged_attn_workspace_bytes(T, B, H, Hkv, D) bytes, 16-byte aligned; its
+ *           contents on entry do not matter.  Calls that may run at the same time need one each.
+ * Pointers of q, out and kv are 16-byte aligned, ldq, ldo and kv's strides multiples of 8.
+ * D is 64 or 128 (DSA_ERR_UNSUPPORTED otherwise), Hkv divides H, B <= 65536, T * H < 2^31,
+ * softmax_scale > 0.  No output overlaps an input or another output.
+ * Arithmetic: bf16 products summed in fp32 by the tensor cores, softmax in base 2 with fp32
+ * statistics; each weight is rounded once to bf16 for its product with v, the denominator sums
+ * the unrounded ones: |out - exact| <= (2^-8 + 2 max_j |ds_j|) sum_j p_j |v_j| + 2^-8 |exact| to
+ * first order, p_j the exact weights and ds_j the fp32 error of score j; lse is fp32 throughout.
+ * Long rows are cut where the work of all sequences divides evenly among the SMs, and the parts
+ * added in order: results depend on the batch and the device's SM count, but not on timing.
+ * Keys and values that a row does not see never touch it, whatever they hold.  An infinity or a
+ * NaN that it sees gives what the formula gives (at a value: an infinity or NaN in its dim).
+ * Flagged with DSA_DEVERR_INDEX, never accessed out of range: a block id outside [0,
+ * num_blocks) or a page at or past bt_stride (its keys are seen by no row); a negative length
+ * (0); rows of a sequence outside [0, T) (left out); overlapping sequences (rows are lost).
+ */
+size_t dsa_paged_attn_workspace_bytes(int64_t T, int B, int H, int Hkv, int D);
+dsa_status dsa_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* query_start,
+                          const int32_t* context_lens, int B, const int32_t* block_table, int64_t bt_stride,
+                          dsa_kv_cache kv, float softmax_scale, int causal, int window, const float* sink, uint16_t* out,
+                          int64_t ldo, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
  * dsa_indexer_logits_topk_noalloc -- dsa_indexer_logits_topk for callers that cannot
  * allocate device memory: a process whose device memory is all reserved at start-up
  * and handed out by its own pool, or a latency-critical loop that cannot afford

@@ -67,3 +67,55 @@ def close(got, want, part, dtype, rel):
     tol = HALF[dtype] * (want.abs() + rel * part) + rel * part
     err = (got.double() - want).abs()
     assert bool((err <= tol).all()), float((err / tol.clamp(min=1e-300)).max())
+
+
+def attention(q, k_rows, v_rows, new, lens, scale, causal, window, sink):
+    """out [T, H, D], lse [T, H] and their bounds, from the definition, sequence by sequence.  q [T, H, D] holds the
+    sequences' rows one after the other; k_rows[b], v_rows[b] [L, Hkv, D] the keys of sequence b (None: a masked key in
+    its place is a row of NaN in `k_rows`, see `dead`).
+
+    Bounds.  Score j is a sum of D products in fp32 by the tensor core: off by at most D 2^-23 of the sum of their
+    magnitudes, and by 2^-22 of its size through the factor and the subtraction of the maximum: ds_j.  A weight
+    e^(s_j - m) is off by ds_j + 2^-21 (the hardware's 2^x), its bf16 form by another 2^-8.  The denominator sums at most
+    64 weights in a chain, then a tile at a time: 2^-24 for each step.  out is rounded once to bf16, 2^-8 of its value."""
+    T, H, D = q.shape
+    dev = q.device
+    out, lse = torch.zeros(T, H, D, dtype=torch.float64, device=dev), torch.empty(T, H, dtype=torch.float64, device=dev)
+    out_tol, lse_tol = torch.zeros_like(out), torch.zeros_like(lse)
+    at = 0
+    for b, n in enumerate(new):
+        n, L = int(n), int(lens[b])
+        if n == 0:
+            continue
+        k, v, live = k_rows[b].double(), v_rows[b].double(), ~k_rows[b].isnan().all(-1).all(-1)
+        k, v = torch.where(live[:, None, None], k, 0.0), torch.where(live[:, None, None], v, 0.0)
+        Hkv = k.shape[1]
+        qs = q[at:at + n].double().view(n, Hkv, H // Hkv, D)
+        s = torch.einsum("nkgd,lkd->nkgl", qs, k) * scale
+        size = torch.einsum("nkgd,lkd->nkgl", qs.abs(), k.abs()) * scale
+        p = L - n + torch.arange(n, device=dev)
+        j = torch.arange(L, device=dev)
+        see = live[None, :].expand(n, L)
+        if causal:
+            see = see & (j[None, :] <= p[:, None])
+        if window:
+            see = see & (j[None, :] > p[:, None] - window)
+        see = see[:, None, None, :]
+        s = s.masked_fill(~see, -math.inf)
+        sk = torch.full((H,), -math.inf, device=dev, dtype=torch.float64) if sink is None else sink.double()
+        sk = sk.view(1, Hkv, H // Hkv, 1)
+        m = torch.maximum(s.amax(-1, keepdim=True) if L else sk, sk).clamp(min=-1e300)
+        w = (s - m).exp()
+        den = w.sum(-1, keepdim=True) + (sk - m).exp()
+        pr = torch.where(den > 0, w / den, 0.0)
+        ds = ((D * 2.0 ** -23 + 2.0 ** -22) * size).masked_fill(~see, 0.0).amax(-1, keepdim=True) if L else 0 * den
+        steps = (2 * 64 + L // 128 + 8) * 2.0 ** -24
+        o = torch.einsum("nkgl,lkd->nkgd", pr, v)
+        mean = torch.einsum("nkgl,lkd->nkgd", pr, v.abs())
+        out[at:at + n] = o.reshape(n, H, D)
+        out_tol[at:at + n] = ((2.0 ** -8 + 2 * ds + 2.0 ** -20 + steps) * 1.01 * mean + 2.0 ** -8 * o.abs()).reshape(n, H, D)
+        le = torch.where(den > 0, m + den.log(), -math.inf)
+        lse[at:at + n] = le.reshape(n, H)
+        lse_tol[at:at + n] = (ds + steps + 2.0 ** -20 + 2.0 ** -22 * torch.where(den > 0, le.abs() + m.abs(), 0.0)).reshape(n, H)
+        at += n
+    return out, lse, out_tol, lse_tol
