@@ -73,7 +73,7 @@ dsa_status check_cache(const dsa_kv_cache& kv, int Hkv, int D) {
   if (kv.num_blocks < 0 || kv.block_size < 1) return DSA_ERR_INVALID_ARG;
   if (kv.row_stride < D || kv.block_stride < D || (Hkv > 1 && kv.head_stride < D)) return DSA_ERR_INVALID_ARG;
   if (kv.num_blocks > INT32_MAX) return DSA_ERR_UNSUPPORTED;
-  const int64_t most = (int64_t)1 << 40;
+  const int64_t most = (int64_t)1 << 39;                                                     // tensor-map strides
   if (kv.block_stride >= most || kv.row_stride >= most || kv.head_stride >= most) return DSA_ERR_UNSUPPORTED;
   return DSA_OK;
 }
@@ -443,6 +443,9 @@ dsa_status dsa_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int 
     for (int j = 0; j < i; ++j)
       if (outs[i] == outs[j]) return DSA_ERR_INVALID_ARG;
   }
+  if (kv.num_blocks == 0) return DSA_ERR_INVALID_ARG;
+  if (ldq >= (int64_t)1 << 39) return DSA_ERR_UNSUPPORTED;                                   // tensor-map strides
+  if (!paged_attn_cache_fits(kv, Hkv)) return DSA_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
   if (ws == nullptr || ws_bytes < paged_attn_ws_bytes(T, B, H, Hkv, D, sms) || !aligned(ws, 16)) return DSA_ERR_WORKSPACE;
   return cuda_status(launch_paged_attn(q, ldq, T, H, Hkv, D, query_start, context_lens, B, block_table, bt_stride, kv,

@@ -130,6 +130,7 @@ cudaError_t launch_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k
                                 const int64_t* slot, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------ attention over a paged cache (paged_attn.cu)
+bool paged_attn_cache_fits(const dsa_kv_cache& kv, int Hkv);   // strides whose ratios its copies can address
 size_t paged_attn_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms);
 cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* start,
                               const int32_t* lens, int B, const int32_t* table, int64_t bt_stride, const dsa_kv_cache& kv,

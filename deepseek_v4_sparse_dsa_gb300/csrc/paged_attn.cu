@@ -23,12 +23,16 @@
 // The denominator sums the unrounded weights: P's rounding (2^-9 of each weight on average, as often up as down) then
 // touches the output as the output's own rounding does, and the lse not at all.
 //
-// Warps: 0-3 and 4-7 softmax, 8-11 loaders (16-byte asynchronous copies, whatever the page size and strides; rows that
-// no query of the item sees are filled with zeros, never read), 12 issues the products.  Tensor memory: S_t 2 x 128
-// columns, O_t 2 x 128.
+// Warps: 0-3 and 4-7 softmax, 8-11 bring keys and values (32 rows of each tile per warp) by tensor copies, 12 issues the
+// products, 13 brings the queries, 14 and 15 look through the values of tiles that some row sees in part.  Where the page
+// size is a multiple of 8, a copy's box is as many rows as divide both a page and a tile; other pages are gathered row by
+// row, four to a copy.  What no row of the item sees is asked for past the tensor's end, which reads as zeros.  Tensor
+// memory: S_t 2 x 128 columns, O_t 2 x 128.
 #include <cuda_bf16.h>
+#include <cudaTypedefs.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "common.cuh"
 #include "launch.h"
@@ -42,7 +46,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;                // base-2 headroom before the running maximum moves
 constexpr int kPlanMax = 1024;               // items (and sequences) that a CTA plans by itself
-constexpr int kLag = 4;                      // copies a loader has in flight before it waits for the oldest
+constexpr int kItemCost = 2;                 // an item's fixed cost, in key tiles
 
 struct AttnArgs {
   const uint16_t* q;
@@ -54,6 +58,11 @@ struct AttnArgs {
   const uint16_t* k;
   const uint16_t* v;
   int64_t num_blocks, block_stride, row_stride, head_stride;
+  int block_rows, head_rows;   // block_stride and head_stride in rows of the copies' tensor
+  int head_cols;               // and what of head_stride lies within a row, in elements
+  int no_row;                  // the tensor's rows: one past its end
+  int box;                     // rows of a copy: 8 .. 128 dividing page and tile, or 1 (gathered)
+  int q_boxes;                 // G divides 128: a row tile of queries is one box of tokens and heads
   int64_t cap;                 // keys a block-table row can hold
   int block_size;
   int64_t T;
@@ -152,9 +161,10 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_s, int64_
   return before + incl - v;
 }
 
-// The plan: first[b] = row blocks of the sequences before b; for row block e of sequence seq[e], prefix[e] = key tiles
-// of the row blocks before it (at least one each, so that a block that sees nothing still has its turn).  A row block
-// has an item per key head; these lie side by side on the line, whose length is prefix[count] * Hkv.
+// The plan: first[b] = row blocks of the sequences before b; for row block e of sequence seq[e], prefix[e] = the length
+// of the row blocks before it, each kItemCost and its key tiles (at least one, so that a block that sees nothing still
+// has its turn).  A row block has an item per key head; these lie side by side on the line, whose length is
+// prefix[count] * Hkv.
 template <int kRows, int NT>
 __device__ int make_plan(const AttnArgs& a, int64_t* prefix, int32_t* first, int32_t* seq, int64_t* warp_s, bool tell) {
   int64_t carry = 0, total;
@@ -184,7 +194,7 @@ __device__ int make_plan(const AttnArgs& a, int64_t* prefix, int32_t* first, int
       seq[e] = lo;
       const Seq q = sequence(a, lo, bad);
       const Item it = make_item<kRows>(a, q, lo, e - first[lo]);
-      c = max(it.tiles, 1);
+      c = kItemCost + max(it.tiles, 1);
       if (it.L > a.cap) bad = true;                // keys past the block table's row
     }
     const int64_t before = block_scan<NT>(c, warp_s, total);
@@ -230,32 +240,43 @@ struct Piece {
   Item it;
   int hk;                      // key head
   int t0, len, cost;           // key tiles t0 .. t0 + len - 1 of the item's `cost`
+  int64_t end;                 // where the item ends on the line
 };
 
 template <int kRows>
 __device__ __forceinline__ bool next_piece(const AttnArgs& a, Pieces& ps, Piece& p) {
-  if (ps.x >= ps.end) return false;
-  const int64_t base = ps.prefix[ps.e];
-  p.cost = (int)(ps.prefix[ps.e + 1] - base);
-  const uint32_t rem = (uint32_t)(ps.x - base * ps.Hkv);
-  p.hk = (int)(rem / (uint32_t)p.cost);
-  p.t0 = (int)(rem % (uint32_t)p.cost);
-  p.len = (int)min((int64_t)(p.cost - p.t0), ps.end - ps.x);
-  const int b = ps.seq[ps.e];
-  bool bad = false;
-  p.it = make_item<kRows>(a, sequence(a, b, bad), b, ps.e - ps.first[b]);
-  ps.x += p.len;
-  if (p.hk == ps.Hkv - 1 && p.t0 + p.len == p.cost) ++ps.e;
-  return true;
+  while (ps.x < ps.end) {
+    const int64_t base = ps.prefix[ps.e];
+    const int length = (int)(ps.prefix[ps.e + 1] - base);
+    const uint32_t rem = (uint32_t)(ps.x - base * ps.Hkv);
+    p.hk = (int)(rem / (uint32_t)length);
+    const int from = (int)(rem % (uint32_t)length), to = (int)min((int64_t)length, from + (ps.end - ps.x));
+    p.cost = length - kItemCost;
+    p.t0 = max(from - kItemCost, 0);
+    p.len = max(to - kItemCost, 0) - p.t0;
+    const int e = ps.e;
+    ps.x += to - from;
+    p.end = ps.x + (length - to);
+    if (p.hk == ps.Hkv - 1 && to == length) ++ps.e;
+    if (p.len == 0) continue;                      // the slice ends within the item's fixed cost
+    const int b = ps.seq[e];
+    bool bad = false;
+    p.it = make_item<kRows>(a, sequence(a, b, bad), b, e - ps.first[b]);
+    return true;
+  }
+  return false;
 }
 
-// Whether some row of the item does not see some key of [lo, hi) in key tile `tile`: only there can a value that one row
-// must not see be a factor of the others' zero weights.
-__device__ __forceinline__ bool tile_masked(const AttnArgs& a, const Item& it, int tile) {
+// The key tiles that every row of the item sees whole are those of [from, to).  In the others, a value that some row
+// must not see would be a factor of its zero weight.
+struct Whole {
+  int from, to;
+  __device__ __forceinline__ bool has(int tile) const { return tile >= from && tile < to; }
+};
+__device__ __forceinline__ Whole whole_tiles(const AttnArgs& a, const Item& it) {
   const int i0 = it.row0 / a.G, i1 = (it.row0 + it.rows - 1) / a.G;
   const int least_hi = high_key(a, it.L, it.L - it.n + i0), most_lo = low_key(a, it.L - it.n + i1);
-  const int64_t k0 = (int64_t)tile * kKeys;
-  return min(k0 + kKeys, (int64_t)it.hi) > least_hi || k0 < most_lo;
+  return {(int)(((int64_t)most_lo + kKeys - 1) / kKeys), least_hi / kKeys};
 }
 
 // ------------------------------------------------------------------ tensor memory and barriers
@@ -318,17 +339,34 @@ __device__ __forceinline__ bool all_well(int bar, int n, bool v) {
   return r != 0;
 }
 
+// Four rows of 64 elements, 128 bytes each, at (x, y0 .. y3) into neighbouring rows of shared memory.
+__device__ __forceinline__ void gather4(uint32_t dst, const void* tmap, uint32_t bar, int x, const int (&y)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], "
+      "[%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3])
+      : "memory");
+}
+
+// Box at (x, y, z) of a tensor of three dimensions.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("{\n .reg .b64 st;\n mbarrier.arrive.shared::cta.b64 st, [%0], %1;\n}" ::"r"(bar), "r"(n) : "memory");
+}
+
 // 16 bytes, or zeros where there is nothing to copy (then src is not read).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)),
                "r"(on ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Bits [lo, hi) of a word, for any lo and hi.
@@ -345,20 +383,21 @@ struct Shape {
   static constexpr int kStages = (D == 128 ? 4 : 8) + (kTiles == 1 ? 1 : 0) - (D == 64 ? 1 : 0);
   static constexpr uint32_t kStageOff = kTiles * kTile;
   static constexpr uint32_t kPlanOff = kStageOff + kStages * kTile;          // prefix, first, seq
-  static constexpr uint32_t kRowOff = kPlanOff + 8 * (kPlanMax + 8) + 4 * kPlanMax * 2;   // key rows [4][128] int64
-  static constexpr uint32_t kMaskOff = kRowOff + 4 * 128 * 8;       // keys that exist [8][4] words
+  static constexpr uint32_t kMaskOff = kPlanOff + 8 * (kPlanMax + 8) + 4 * kPlanMax * 2;  // keys that exist [8][4] words
   static constexpr uint32_t kBadOff = kMaskOff + 8 * 16;            // values that are no numbers, per piece [16]
   static constexpr uint32_t kStatOff = kBadOff + 64;                // (m, l) of both streams [2][128]
   static constexpr uint32_t kBarOff = kStatOff + 2048;
-  static constexpr int kBars = 2 * kStages + 2 * 5 + 1;
-  static constexpr uint32_t kCtlOff = kBarOff + 8 * 32;             // abort, TMEM base
+  static constexpr int kBars = 2 * kStages + 2 * 5 + 8 + 1;
+  static constexpr uint32_t kCtlOff = kBarOff + 8 * 48;             // abort, TMEM base
   static constexpr uint32_t kScanOff = kCtlOff + 16;
   static constexpr size_t kSmem = 1024 + kScanOff + 16 * 8;
-  static_assert(kBars <= 32 && kStages <= 8 && kSmem <= 232448, "shared memory");
+  static_assert(kBars <= 48 && kStages <= 8 && kSmem <= 232448, "shared memory");
 };
 
 template <int D, int kTiles>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                                                              const __grid_constant__ CUtensorMap tmv,
+                                                              const __grid_constant__ AttnArgs a) {
   using Sh = Shape<D, kTiles>;
   constexpr int kStages = Sh::kStages, kRows = Sh::kRows;
   extern __shared__ uint8_t smem_raw[];
@@ -367,34 +406,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   int64_t* prefix_s = reinterpret_cast<int64_t*>(sm + Sh::kPlanOff);
   int32_t* first_s = reinterpret_cast<int32_t*>(prefix_s + kPlanMax + 8);
   int32_t* seq_s = first_s + kPlanMax;
-  int64_t* rows_s = reinterpret_cast<int64_t*>(sm + Sh::kRowOff);
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Sh::kMaskOff);
   volatile int* bad_s = reinterpret_cast<volatile int*>(sm + Sh::kBadOff);
   float2* stat_s = reinterpret_cast<float2*>(sm + Sh::kStatOff);
   int* ctl = reinterpret_cast<int*>(sm + Sh::kCtlOff);
   volatile int* abort_flag = ctl;
   const uint32_t bars = sm32 + Sh::kBarOff;
-  // barrier numbers: stages full, stages empty, then per stream
+  // barrier numbers: stages full, stages empty, then per stream, then a ring of the tiles that are looked through
   constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2, kSFull = kQFree + 2,
-                kPFull = kSFull + 2, kODone = kPFull + 2, kDrain = kODone + 2;
+                kPFull = kSFull + 2, kODone = kPFull + 2, kLook = kODone + 2, kDrain = kLook + 8;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
 
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
   const unsigned long long limit = wait_limit_ns();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(kFull + i), 128);
+      mbar_init(bar(kFull + i), 4);
       mbar_init(bar(kEmpty + i), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(kQFull + t), 128);
+      mbar_init(bar(kQFull + t), a.q_boxes ? 1 : 64);
       mbar_init(bar(kQFree + t), 1);
       mbar_init(bar(kSFull + t), 1);
       mbar_init(bar(kPFull + t), 4);
       mbar_init(bar(kODone + t), 1);
     }
+    for (int i = 0; i < 8; ++i) mbar_init(bar(kLook + i), 4);
     mbar_init(bar(kDrain), 1);
     ctl[0] = 0;
+    if (a.q_boxes) tma_prefetch_desc(&tmq);
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12) tmem_alloc(smem_u32(ctl + 1), 512);
@@ -540,9 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       const bool whole = p.t0 == 0 && p.len == p.cost;
       const int slot = p.t0 == 0 ? 2 * (int)c + 1 : 2 * (int)c;
       if (!whole && p.t0 == 0 && threadIdx.x == 0) {               // the item's first part: it owns the sum
-        const int64_t last = ps.x - p.len + p.cost - 1;            // the line's last position of the item
         my_meta[1] = it.b, my_meta[2] = it.row0, my_meta[3] = it.rows, my_meta[4] = p.hk;
-        my_meta[5] = (int)(((last + 1) * C - 1) / line);           // the CTA that holds it
+        my_meta[5] = (int)((p.end * C - 1) / line);                // the CTA that holds its last tile
         my_meta[0] = 1;
       }
       if (ok && mine > 0) {
@@ -617,9 +658,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           if (bad && live) {
             // values that are no numbers were taken out of the tiles that some row sees in part: the rows that see them
             // get them back, as sums with them give
+            const Whole all = whole_tiles(a, it);
             for (int j = 0; j < p.len; ++j) {
               const int tile = it.tile0 + p.t0 + j;
-              if (!tile_masked(a, it, tile)) continue;
+              if (all.has(tile)) continue;
               for (int64_t key = max((int64_t)tile * kKeys, (int64_t)lo); key < min((int64_t)(tile + 1) * kKeys, (int64_t)hi); ++key) {
                 const int blk = a.table[it.b * a.bt_stride + key / a.block_size];
                 if (blk < 0 || blk >= a.num_blocks) continue;
@@ -663,166 +705,101 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       *abort_flag = 1;
     }
   } else if (warp < 12) {
-    // ================================ loaders ================================
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-    const int lt = (int)threadIdx.x - 256;
-    constexpr int kPer = D / 8;                    // 16-byte pieces of a row
-    constexpr int kStep = 128 / kPer;              // rows of a pass
-    const int pc = lt % kPer, r0 = lt / kPer;      // the thread's piece, and its first row
-    const uint32_t dst0 = (uint32_t)(pc >> 3) * 16384u + (uint32_t)r0 * 128u + (uint32_t)(((pc & 7) ^ (r0 & 7)) << 4);
-    uint32_t loads = 0, qloads[2] = {0, 0}, tiles = 0;
+    // ================================ keys and values ================================
+    // Lane l of warp w resolves row 32 w + l of each tile; lanes whose row begins a copy issue it (both halves of 128
+    // dims by lanes of their own).
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    constexpr int kHalves = D / 64;
+    const int w32 = 32 * (warp & 3);
+    const int box = a.box, units = (box == 1 ? 8 : box >= 32 ? (w32 % box == 0 ? 1 : 0) : 32 / box) * kHalves;
+    const int unit_row = lane / kHalves * (box == 1 ? 4 : box >= 32 ? 32 : box);   // the lane's copy: its first row in the warp
+    const uint32_t unit_dst = (uint32_t)(lane % kHalves) * 16384u + (uint32_t)(w32 + unit_row) * 128u;
+    const int unit_x = 64 * (lane % kHalves);
+    const uint32_t bytes = (uint32_t)(box == 1 ? 512 : 128 * box) * (uint32_t)units;
+    uint32_t loads = 0, tiles = 0, np = 0, looks = 0;
     bool ok = true;
-    // copies in flight, oldest in the low bits: barrier number, and for values 0x80 + 0x100 * stage where they are looked
-    // through when they have landed
-    uint64_t fifo = 0;
-    int flying = 0;
-    uint32_t np = 0;
-    auto landed = [&]() {                          // the oldest copy of this thread is complete
-      const uint32_t op = (uint32_t)fifo & 0xFFFFu;
-      fifo >>= 16;
-      --flying;
-      if (op & 0x80u) {
-        uint8_t* at = sm + Sh::kStageOff + (op >> 8 & 7u) * Sh::kTile + dst0;
-        bool found = false;
-#pragma unroll 4
-        for (int i = 0; i < 128 / kStep; ++i) {
-          uint4 w = *reinterpret_cast<uint4*>(at + i * kStep * 128);
-          uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
-          bool here = false;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if ((ww[e] & 0x7F80u) == 0x7F80u) ww[e] &= 0xFFFF0000u, here = true;
-            if ((ww[e] & 0x7F800000u) == 0x7F800000u) ww[e] &= 0x0000FFFFu, here = true;
-          }
-          if (here) *reinterpret_cast<uint4*>(at + i * kStep * 128) = w;
-          found |= here;
-        }
-        if (found) bad_s[op >> 11 & 15u] = 1;
-      }
-      proxy_fence();
-      mbar_arrive(bar((int)(op & 0x3Fu)));
-    };
-    auto land_all = [&]() {
-      copies_wait<0>();
-      while (flying > 0) landed();
-    };
-    // room for one more copy in `where`: before a wait that may be long, everything in flight is passed on
-    auto free_wait = [&](int which, uint32_t parity) {
-      if (!ok || mbar_try_wait(bar(which), parity)) return;
-      land_all();
-      ok = mbar_wait(bar(which), parity, limit, abort_flag);
-    };
-    auto sent = [&](uint32_t op) {
-      copies_commit();
-      fifo |= (uint64_t)op << (16 * flying);
-      ++flying;
-    };
-    auto make_room = [&]() {
-      if (flying == kLag) {
-        copies_wait<kLag - 1>();
-        landed();
-      }
-    };
     Piece p;
-    while (next_piece<kRows>(a, ps, p)) {
+    while (ok && next_piece<kRows>(a, ps, p)) {
       const Item& it = p.it;
       if (it.tiles == 0) continue;
-      const int nq = kTiles == 2 && it.rows > 128 ? 2 : 1;
-      for (int t = 0; t < nq; ++t) {
-        free_wait(kQFree + t, (qloads[t] & 1u) ^ 1u);
-        make_room();
-        if (ok) {
-          const uint32_t dst = sm32 + (uint32_t)t * Sh::kTile + dst0;
-#pragma unroll 4
-          for (int i = 0; i < 128 / kStep; ++i) {
-            const int row = 128 * t + r0 + i * kStep;
-            const bool on = row < it.rows;
-            const uint32_t gr = (uint32_t)(it.row0 + (on ? row : 0));
-            const uint32_t token = gr / (uint32_t)a.G, g = gr % (uint32_t)a.G;
-            copy16(dst + (uint32_t)i * kStep * 128u,
-                   a.q + (int64_t)(it.s + (int)token) * a.ldq + (int64_t)(p.hk * a.G + (int)g) * D + pc * 8, on);
-          }
-          sent((uint32_t)(kQFull + t));
-        }
-        ++qloads[t];
-      }
       const int first = it.tile0 + p.t0;
+      const Whole all = whole_tiles(a, it);
       const int32_t* table = a.table + (int64_t)it.b * a.bt_stride;
-      // the block of this thread's key of a tile; keys that no row sees have none
+      // the lane's key, its page and place in it, and the page's block, one tile ahead (-1: no copy brings it)
+      int64_t key = (int64_t)first * kKeys + w32 + lane;
+      uint32_t page = (uint32_t)key / (uint32_t)a.block_size, off = (uint32_t)key % (uint32_t)a.block_size;
+      const uint32_t page_step = kKeys / (uint32_t)a.block_size, off_step = kKeys % (uint32_t)a.block_size;
       auto block_of = [&](int j) {
-        const int64_t key = (int64_t)(first + j) * kKeys + lt;
-        return j < p.len && key >= it.lo && key < it.hi ? table[(uint32_t)key / (uint32_t)a.block_size] : -1;
+        const int64_t from = key & -(int64_t)box;
+        return j < p.len && from + box > it.lo && from < it.hi ? table[page] : -1;
       };
       int blk = block_of(0);
-      bool left = false;
-      // the rows of key tile j, resolved by a thread each
+      int y = a.no_row, y1 = a.no_row;             // the lane's row in this tile and the one before it
+      const int x = p.hk * a.head_cols + unit_x, y0 = p.hk * a.head_rows;
+      if (warp == 8 && lane == 0) bad_s[np & 15u] = 0;
       auto rows_of = [&](int j) {
-        const int64_t key = (int64_t)(first + j) * kKeys + lt;
         const bool seen = key >= it.lo && key < it.hi;
-        const bool have = seen && blk >= 0 && blk < a.num_blocks;
-        if (seen && !have) raise_error(DSA_DEVERR_INDEX);
-        const uint32_t at = (tiles + (uint32_t)j);
-        rows_s[(at & 3u) * 128u + (uint32_t)lt] =
-            have ? blk * a.block_stride + (int64_t)((uint32_t)key % (uint32_t)a.block_size) * a.row_stride + p.hk * a.head_stride : -1;
-        const uint32_t word = __ballot_sync(0xFFFFFFFFu, have);
-        if (lane == 0) mask_s[4 * (at & 7u) + (uint32_t)(warp & 3)] = word;
-        if (j == 0 && lt == 0) bad_s[np & 15u] = 0;
+        const bool there = blk >= 0 && blk < a.num_blocks;
+        if (seen && !there) raise_error(DSA_DEVERR_INDEX);
+        y1 = y;
+        y = there ? blk * a.block_rows + y0 + (int)off : a.no_row;
+        const uint32_t word = __ballot_sync(0xFFFFFFFFu, there);
+        if (lane == 0) mask_s[4 * ((tiles + (uint32_t)j) & 7u) + (uint32_t)(warp & 3)] = word;
+        key += kKeys;
+        page += page_step, off += off_step;
+        if (off >= (uint32_t)a.block_size) off -= (uint32_t)a.block_size, ++page;
         blk = block_of(j + 1);
-        ok = all_well(1, 128, ok);
       };
-      auto copy_tile = [&](const uint16_t* base, int j, uint32_t op) {
-        const int s = (int)(loads % kStages);
-        free_wait(kEmpty + s, (loads / kStages & 1u) ^ 1u);
-        make_room();
-        if (ok) {
-          const int64_t* rows = rows_s + ((tiles + (uint32_t)j) & 3u) * 128u + r0;
-          const uint32_t dst = sm32 + Sh::kStageOff + (uint32_t)s * Sh::kTile + dst0;
-#pragma unroll 8
-          for (int i = 0; i < 128 / kStep; ++i) {
-            const int64_t o = rows[i * kStep];
-            copy16(dst + (uint32_t)i * kStep * 128u, base + (o < 0 ? 0 : o) + pc * 8, o >= 0);
-          }
-          sent((uint32_t)(kFull + s) | (op ? 0x80u | (uint32_t)s << 8 | (np & 15u) << 11 : 0u));
+      // copies announce themselves to the products, or, for values that are looked through, to those who look
+      auto bring = [&](const CUtensorMap* tm, int row, bool look) {
+        const int st = (int)(loads % kStages);
+        ok = mbar_wait(bar(kEmpty + st), (loads / kStages & 1u) ^ 1u, limit, abort_flag);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        const uint32_t to = bar(look ? kLook + (int)(looks & 7u) : kFull + st);
+        if (look) ++looks;
+        if (lane == 0) mbar_arrive_expect_tx(to, bytes);
+        const uint32_t dst = sm32 + Sh::kStageOff + (uint32_t)st * Sh::kTile + unit_dst;
+        if (box == 1) {
+          int rows[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rows[i] = __shfl_sync(0xFFFFFFFFu, row, (unit_row + i) & 31);
+          if (lane < units) gather4(dst, tm, to, x, rows);
+        } else {
+          const int at = __shfl_sync(0xFFFFFFFFu, row, unit_row & 31);
+          if (lane < units) tma_load_2d(dst, tm, to, x, at);
         }
+        __syncwarp();
         ++loads;
       };
-      auto values = [&](int j) { copy_tile(a.v, j, tile_masked(a, it, first + j) ? 1u : 0u); };
       if constexpr (kTiles == 2) {
-        for (int j = 0; j < p.len; ++j) {
+        for (int j = 0; ok && j < p.len; ++j) {
           rows_of(j);
-          if (!ok) {
-            left = true;
-            break;
-          }
-          copy_tile(a.k, j, 0u);
-          values(j);
+          bring(&tmk, y, false);
+          if (ok) bring(&tmv, y, !all.has(first + j));
         }
       } else {                                     // keys two tiles ahead of the values
-        for (int j = 0; j < p.len + 2; ++j) {
-          if (j < p.len) {
-            if (j >= 2) values(j - 2);
-            rows_of(j);
-            if (!ok) {
-              left = true;
-              break;
-            }
-            copy_tile(a.k, j, 0u);
-          } else if (j >= 2) {
-            values(j - 2);
-          }
+        for (int j = 0; ok && j < p.len; ++j) {
+          if (j >= 2) bring(&tmv, y1, !all.has(first + j - 2));
+          if (!ok) break;
+          rows_of(j);
+          bring(&tmk, y, false);
         }
+        if (ok && p.len >= 2) bring(&tmv, y1, !all.has(first + p.len - 2));
+        if (ok) bring(&tmv, y, !all.has(first + p.len - 1));
       }
-      if (left) break;
       tiles += (uint32_t)p.len;
       ++np;
     }
-    land_all();
     if (!ok && lane == 0) {
       raise_error(DSA_DEVERR_TIMEOUT);
       *abort_flag = 1;
     }
+    // every copy issued has landed before the CTA may leave
+    for (uint32_t i = loads > (uint32_t)kStages ? loads - kStages : 0; i < loads; ++i)
+      mbar_wait(bar(kFull + (int)(i % kStages)), i / kStages & 1u, kCleanupWaitNs, nullptr);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == 12 && lane == 0) {
       // ================================ products ================================
       constexpr uint32_t kIdescS = idesc_bf16(128, 128), kIdescO = idesc_bf16(128, D) | (1u << 16);   // V: dims contiguous
@@ -887,6 +864,109 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       }
       mma_commit(bar(kDrain));                     // everything issued has completed
       mbar_wait(bar(kDrain), 0u, kCleanupWaitNs, nullptr);
+    } else if (warp == 13) {
+      // ================================ queries ================================
+      uint32_t loads0 = 0, loads1 = 0;
+      bool ok = true;
+      Piece p;
+      while (a.q_boxes && lane == 0 && ok && next_piece<kRows>(a, ps, p)) {
+        if (p.it.tiles == 0) continue;
+        for (int t = 0; ok && t < (kTiles == 2 && p.it.rows > 128 ? 2 : 1); ++t) {
+          ok = mbar_wait(bar(kQFree + t), ((t == 0 ? loads0 : loads1) & 1u) ^ 1u, limit, abort_flag);
+          if (!ok) break;
+          if (t == 0) ++loads0;
+          else ++loads1;
+          mbar_arrive_expect_tx(bar(kQFull + t), Sh::kTile);
+          const int token = p.it.s + (p.it.row0 + 128 * t) / a.G;
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(sm32 + (uint32_t)t * Sh::kTile + 16384u * (uint32_t)h, &tmq, bar(kQFull + t), 64 * h, p.hk * a.G, token);
+        }
+      }
+      if (!ok) {
+        raise_error(DSA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
+      if (loads0 > 0) mbar_wait(bar(kQFull), (loads0 - 1) & 1u, kCleanupWaitNs, nullptr);
+      if (loads1 > 0) mbar_wait(bar(kQFull + 1), (loads1 - 1) & 1u, kCleanupWaitNs, nullptr);
+    } else if (warp >= 14) {
+      // ================================ a look at values ================================
+      // Where some row sees a tile in part, its values that are no numbers are taken out (a zero weight would not silence
+      // them); the rows that do see them get them back with the sums.  Keys outside the item's
+      // range need no more: finite values under a zero weight are nothing.
+      uint32_t base = 0, looked = 0, np = 0, loads0 = 0, loads1 = 0;
+      const int lt = (int)threadIdx.x - 14 * 32;
+      bool ok = true;
+      Piece p;
+      while (ok && next_piece<kRows>(a, ps, p)) {
+        const Item& it = p.it;
+        if (it.tiles == 0) continue;
+        // queries whose row tiles are no boxes: a piece of 16 bytes per thread and pass
+        for (int t = 0; !a.q_boxes && ok && t < (kTiles == 2 && it.rows > 128 ? 2 : 1); ++t) {
+          constexpr int kPer = D / 8, kStep = 64 / kPer;
+          ok = mbar_wait(bar(kQFree + t), ((t == 0 ? loads0 : loads1) & 1u) ^ 1u, limit, abort_flag);
+          if (!ok) break;
+          if (t == 0) ++loads0;
+          else ++loads1;
+          const int pc = lt % kPer;
+          int row = 128 * t + lt / kPer;
+          uint32_t token = (uint32_t)(it.row0 + row) / (uint32_t)a.G, g = (uint32_t)(it.row0 + row) % (uint32_t)a.G;
+#pragma unroll 2
+          for (int i = 0; i < 128 / kStep; ++i) {
+            const int r = row & 127;
+            const bool on = row < it.rows;
+            const uint16_t* src = on ? a.q + (int64_t)(it.s + (int)token) * a.ldq + (int64_t)(p.hk * a.G + (int)g) * D + pc * 8 : a.q;
+            copy16(sm32 + (uint32_t)t * Sh::kTile + (uint32_t)(pc >> 3) * 16384u + (uint32_t)r * 128u +
+                       (uint32_t)(((pc & 7) ^ (r & 7)) << 4), src, on);
+            row += kStep;
+            for (g += kStep; g >= (uint32_t)a.G; g -= (uint32_t)a.G) ++token;
+          }
+          copies_wait();
+          proxy_fence();
+          mbar_arrive(bar(kQFull + t));
+        }
+        const Whole all = whole_tiles(a, it);
+        for (int j = 0; ok && j < p.len; ++j) {
+          const int tile = it.tile0 + p.t0 + j;
+          if (all.has(tile)) continue;
+          const uint32_t ld = base + (uint32_t)(kTiles == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * p.len - 1)), st = ld % kStages;
+          ok = mbar_wait(bar(kLook + (int)(looked & 7u)), looked >> 3 & 1u, limit, abort_flag);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          ++looked;
+          if (ok) {
+            // thread: 16-byte column lt % 8 of every eighth row, half by half
+            uint8_t* at = sm + Sh::kStageOff + st * Sh::kTile + (lt >> 3) * 128 + (lt & 7) * 16;
+            const int64_t k0 = (int64_t)tile * kKeys + (lt >> 3);
+            bool found = false;
+#pragma unroll 4
+            for (int i = 0; i < 16 * (D / 64); ++i) {
+              uint4* here = reinterpret_cast<uint4*>(at + 1024 * i);
+              const int64_t key = k0 + 8 * (i & 15);
+              uint4 w = *here;
+              uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
+              bool change = false;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((ww[e] & 0x7F80u) == 0x7F80u) ww[e] &= 0xFFFF0000u, change = true;
+                if ((ww[e] & 0x7F800000u) == 0x7F800000u) ww[e] &= 0x0000FFFFu, change = true;
+              }
+              if (change) {
+                *here = w;
+                found |= key >= it.lo && key < it.hi;
+              }
+            }
+            if (found) bad_s[np & 15u] = 1;
+            proxy_fence();
+          }
+          ok = all_well(1, 64, ok);                // both halves are done
+          if (ok && lt == 0) mbar_arrive_n(bar(kFull + (int)st), 4);
+        }
+        base += 2u * (uint32_t)p.len;
+        ++np;
+      }
+      if (!ok && lane == 0) {
+        raise_error(DSA_DEVERR_TIMEOUT);
+        *abort_flag = 1;
+      }
     }
     __syncwarp();
   }
@@ -986,8 +1066,35 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, unsigned block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// bf16 tensors of two or three dimensions in boxes of 64 elements (128-byte swizzle).  What lies outside reads as zeros.
+bool make_map(CUtensorMap* m, const void* base, int dims, const cuuint64_t* size, const cuuint64_t* strides, const cuuint32_t* box) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)dims, const_cast<void*>(base), size, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+  CUtensorMap q, k, v;
+};
+
 template <int D, int kTiles>
-cudaError_t launch_shape(const AttnArgs& a, int ctas, cudaStream_t stream) {
+cudaError_t launch_shape(const AttnArgs& a, const Maps& m, int ctas, cudaStream_t stream) {
   using Sh = Shape<D, kTiles>;
   auto kernel = paged_attn_kernel<D, kTiles>;
   static std::atomic<unsigned long long> ready{0};               // devices on which the kernel is set up
@@ -1000,20 +1107,30 @@ cudaError_t launch_shape(const AttnArgs& a, int ctas, cudaStream_t stream) {
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
-    // the warps' shares, 2 x 192 + 80 + 48 registers a thread, are those of the launch
-    if (fa.numRegs * kThreads < 128 * (2 * 192 + 80 + 48)) return cudaErrorInvalidConfiguration;
+    // the warps' shares, 2 x 192 + 2 x 64 registers a thread, are those of the launch
+    if (fa.numRegs * kThreads < 128 * (2 * 192 + 2 * 64)) return cudaErrorInvalidConfiguration;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   if (a.planned) {
     e = launch_pdl(plan_kernel<Sh::kRows>, dim3(1), 1024u, 0, stream, a);
     if (e != cudaSuccess) return e;
   }
-  e = launch_pdl(kernel, dim3((unsigned)ctas), (unsigned)kThreads, Sh::kSmem, stream, a);
+  e = launch_pdl(kernel, dim3((unsigned)ctas), (unsigned)kThreads, Sh::kSmem, stream, m.q, m.k, m.v, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(combine_kernel<D, Sh::kRows>, dim3((unsigned)ctas, kTiles == 2 ? 8 : 2), 256u, 0, stream, a, ctas);
 }
 
 }  // namespace
+
+bool paged_attn_cache_fits(const dsa_kv_cache& kv, int Hkv) {
+  if (kv.block_stride % kv.row_stride != 0) return false;
+  if (Hkv > 1 && kv.head_stride > kv.row_stride && kv.head_stride % kv.row_stride != 0) return false;
+  if (Hkv > 1 && kv.head_stride < kv.row_stride && (int64_t)Hkv * kv.head_stride > INT32_MAX) return false;
+  const int64_t head_rows = Hkv > 1 && kv.head_stride >= kv.row_stride ? kv.head_stride / kv.row_stride : 0;
+  const int64_t block_rows = kv.block_stride / kv.row_stride;
+  return block_rows <= INT32_MAX / kv.num_blocks && head_rows <= INT32_MAX / Hkv &&
+         kv.num_blocks * block_rows + Hkv * head_rows + kv.block_size <= INT32_MAX;
+}
 
 size_t paged_attn_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms) { return layout(T, B, H, Hkv, D, num_sms).total; }
 
@@ -1041,8 +1158,29 @@ cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, 
   a.seq = reinterpret_cast<int32_t*>(w + y.seq);
   a.planned = y.planned;
   a.limit = (int)y.blocks;
-  if (D == 128) return y.tiles == 2 ? launch_shape<128, 2>(a, y.ctas, stream) : launch_shape<128, 1>(a, y.ctas, stream);
-  return y.tiles == 2 ? launch_shape<64, 2>(a, y.ctas, stream) : launch_shape<64, 1>(a, y.ctas, stream);
+  // the pool as one tensor of rows row_stride apart (paged_attn_cache_fits)
+  const bool in_row = Hkv == 1 || kv.head_stride < kv.row_stride;
+  a.block_rows = (int)(kv.block_stride / kv.row_stride);
+  a.head_cols = in_row && Hkv > 1 ? (int)kv.head_stride : 0;
+  a.head_rows = in_row ? 0 : (int)(kv.head_stride / kv.row_stride);
+  a.no_row = (int)((kv.num_blocks - 1) * a.block_rows + (int64_t)(Hkv - 1) * a.head_rows + kv.block_size);
+  a.box = 1;
+  if (kv.block_size % 8 == 0)
+    for (a.box = 8; a.box < kKeys && kv.block_size % (2 * a.box) == 0;) a.box *= 2;
+  a.q_boxes = 128 % a.G == 0;
+  Maps m{};
+  const cuuint64_t size[2] = {(cuuint64_t)((Hkv - 1) * (int64_t)a.head_cols + D), (cuuint64_t)a.no_row};
+  const cuuint64_t stride[1] = {(cuuint64_t)kv.row_stride * 2};
+  const cuuint32_t box[2] = {64u, (cuuint32_t)a.box};
+  if (!make_map(&m.k, kv.k, 2, size, stride, box) || !make_map(&m.v, kv.v, 2, size, stride, box)) return cudaErrorInvalidValue;
+  if (a.q_boxes) {
+    const cuuint64_t qsize[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+    const cuuint64_t qstride[2] = {(cuuint64_t)D * 2, (cuuint64_t)ldq * 2};
+    const cuuint32_t qbox[3] = {64u, (cuuint32_t)a.G, (cuuint32_t)(128 / a.G)};
+    if (!make_map(&m.q, q, 3, qsize, qstride, qbox)) return cudaErrorInvalidValue;
+  }
+  if (D == 128) return y.tiles == 2 ? launch_shape<128, 2>(a, m, y.ctas, stream) : launch_shape<128, 1>(a, m, y.ctas, stream);
+  return y.tiles == 2 ? launch_shape<64, 2>(a, m, y.ctas, stream) : launch_shape<64, 1>(a, m, y.ctas, stream);
 }
 
 DSA_DEFINE_TU_ERROR_ACCESSORS(paged_attn)

@@ -492,8 +492,8 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  *   lse[t,h] = ln(sum_j e^(s_j) + e^(sink[h])),
  * m any shift.  A row that sees nothing gives zeros, and lse the sink (-inf without one).
  *  q        [T, H, D] bf16 bit patterns, tokens ldq elements apart, heads D apart; out the same
- *           with ldo.  Rows of q that belong to no sequence (past query_start[B], or in a gap)
- *           are not read, and their rows of out and lse are left as they are.
+ *           with ldo.  Rows that belong to no sequence (past query_start[B], or in a gap) count
+ *           for nothing, and their rows of out and lse are left as they are.
  *  query_start [B + 1] int32, ascending, as dsa_assign_slots writes it; context_lens [B] int32.
  *  block_table [B, bt_stride] int32; kv the cache (see dsa_kv_cache); block_size any >= 1.
  *           Entries of pages that hold no visible key are not read (with a window the old
@@ -501,7 +501,10 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  *  sink     [H] fp32 logits that join the denominators, nullable.  lse [T, H] fp32, nullable.
  *  ws       dsa_paged_attn_workspace_bytes(T, B, H, Hkv, D) bytes, 16-byte aligned; its
  *           contents on entry do not matter.  Calls that may run at the same time need one each.
- * Pointers of q, out and kv are 16-byte aligned, ldq, ldo and kv's strides multiples of 8.
+ * Pointers of q, out and kv are 16-byte aligned, ldq, ldo and kv's strides multiples of 8,
+ * num_blocks at least 1.  The pool is addressed as rows row_stride apart: block_stride is a
+ * multiple of row_stride, head_stride smaller than it or a multiple of it, and the pool's rows
+ * fewer than 2^31 (DSA_ERR_UNSUPPORTED otherwise).
  * D is 64 or 128 (DSA_ERR_UNSUPPORTED otherwise), Hkv divides H, B <= 65536, T * H < 2^31,
  * softmax_scale > 0.  No output overlaps an input or another output.
  * Arithmetic: bf16 products summed in fp32 by the tensor cores, softmax in base 2 with fp32
