@@ -23,8 +23,8 @@
 // The denominator sums the unrounded weights: P's rounding (2^-9 of each weight on average, as often up as down) then
 // touches the output as the output's own rounding does, and the lse not at all.
 //
-// Warps: 0-3 and 4-7 softmax, 8-11 bring keys and values (32 rows of each tile per warp) by tensor copies, 12 issues the
-// products, 13 brings the queries, 14 and 15 look through the values of tiles that some row sees in part.  Where the page
+// Warps: 0-3 and 4-7 softmax, 8-11 bring keys and values (32 rows of each tile per warp) by tensor copies, 12 and 13
+// issue a stream's products each, 14 and 15 bring the queries and look through the values of tiles that some row sees in part.  Where the page
 // size is a multiple of 8, a copy's box is as many rows as divide both a page and a tile; other pages are gathered row by
 // row, four to a copy.  What no row of the item sees is asked for past the tensor's end, which reads as zeros.  Tensor
 // memory: S_t 2 x 128 columns, O_t 2 x 128.
@@ -280,21 +280,35 @@ __device__ __forceinline__ Whole whole_tiles(const AttnArgs& a, const Item& it) 
 }
 
 // ------------------------------------------------------------------ tensor memory and barriers
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr >> 4) & 0x3FFFu);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
+// Shared-memory descriptors (128-byte swizzle) in two words: the high one holds the stride of 8-row groups (1024 bytes),
+// the version and the swizzle; the low one the address and the stride of 64-element blocks, which only V's tiles use
+// (dims contiguous).  Steps within a tile are additions to the low word.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t block) { return (addr >> 4) | (block >> 4) << 16; }
+
+// One thread of the warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
 }
 
-// D += A B with A [128 rows][16 elements] in tensor memory: row r in lane r, elements 2c and 2c + 1 in column c.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D (+)= A B, both from shared memory.
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t tmem_d, uint32_t a, uint32_t b, uint32_t idesc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p;\n .reg .b64 da, db;\n mov.b64 da, {%1, %3};\n mov.b64 db, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n}" ::"r"(tmem_d),
+      "r"(a), "r"(b), "r"(kDescHigh), "r"(idesc), "n"(kAdd ? 1 : 0)
+      : "memory");
+}
+
+// D (+)= A B with A [128 rows][16 elements] in tensor memory: row r in lane r, elements 2c and 2c + 1 in column c.
+__device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_t b, uint32_t idesc, uint32_t add) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 db;\n mov.b64 db, {%2, %3};\n setp.ne.b32 p, %5, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n}" ::"r"(tmem_d),
+      "r"(tmem_a), "r"(b), "r"(kDescHigh), "r"(idesc), "r"(add)
       : "memory");
 }
 
@@ -387,7 +401,7 @@ struct Shape {
   static constexpr uint32_t kBadOff = kMaskOff + 8 * 16;            // values that are no numbers, per piece [16]
   static constexpr uint32_t kStatOff = kBadOff + 64;                // (m, l) of both streams [2][128]
   static constexpr uint32_t kBarOff = kStatOff + 2048;
-  static constexpr int kBars = 2 * kStages + 2 * 5 + 8 + 1;
+  static constexpr int kBars = 2 * kStages + 2 * 5 + 8 + 2;
   static constexpr uint32_t kCtlOff = kBarOff + 8 * 48;             // abort, TMEM base
   static constexpr uint32_t kScanOff = kCtlOff + 16;
   static constexpr size_t kSmem = 1024 + kScanOff + 16 * 8;
@@ -422,17 +436,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(bar(kFull + i), 4);
-      mbar_init(bar(kEmpty + i), 1);
+      mbar_init(bar(kEmpty + i), 2);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kQFull + t), a.q_boxes ? 1 : 64);
-      mbar_init(bar(kQFree + t), 1);
+      mbar_init(bar(kQFree + t), kTiles == 2 ? 1 : 2);
       mbar_init(bar(kSFull + t), 1);
       mbar_init(bar(kPFull + t), 4);
       mbar_init(bar(kODone + t), 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(bar(kLook + i), 4);
     mbar_init(bar(kDrain), 1);
+    mbar_init(bar(kDrain + 1), 1);
     ctl[0] = 0;
     if (a.q_boxes) tma_prefetch_desc(&tmq);
     tma_prefetch_desc(&tmk);
@@ -800,96 +815,99 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       mbar_wait(bar(kFull + (int)(i % kStages)), i / kStages & 1u, kCleanupWaitNs, nullptr);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 12 && lane == 0) {
+    if (warp <= 13) {
       // ================================ products ================================
+      // A warp per stream; its control flow is the same for all lanes (and the compiler can tell: what it depends on is
+      // broadcast), so that the operands of a product are uniform and cost an addition each.  With one thread branching
+      // off on its own, issuing the products of a tile took 3.4 times as long, and longer than the products.
       constexpr uint32_t kIdescS = idesc_bf16(128, 128), kIdescO = idesc_bf16(128, D) | (1u << 16);   // V: dims contiguous
-      uint32_t base = 0, qs[2] = {0, 0}, jobs[2] = {0, 0};
+      const uint32_t t = (uint32_t)__shfl_sync(0xFFFFFFFFu, warp - 12, 0), tq = kTiles == 2 ? t : 0;
+      const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tmem, 0), smb = __shfl_sync(0xFFFFFFFFu, sm32, 0);
+      const uint32_t bs = smb + Sh::kBarOff;
+      const bool mine = elect_one();
+      // Every stage is released by both streams, also by one that has no use for it: a barrier's phases are told apart by
+      // their parity, so whoever waits on one has to pass all of them.
+      uint32_t base = 0, pieces = 0, jobs = 0, next = 0;
       bool ok = true;
+      auto wait = [&](uint32_t which, uint32_t parity) -> bool {
+        return (bool)__all_sync(0xFFFFFFFFu, mbar_wait(bs + 8u * which, parity, limit, abort_flag));
+      };
       Piece p;
       while (ok && next_piece<kRows>(a, ps, p)) {
-        if (p.it.tiles == 0) continue;
-        const int act = kTiles == 2 && p.it.rows <= 128 ? 1 : 2;   // streams in turn
-        const int turns = kTiles == 2 ? p.len * act : p.len;
-        // turn u: which stream and key tile; loads come in the order K0 V0 K1 V1 .. or K0 K1 V0 K2 V1 ..
-        auto stream = [&](int u) { return act == 2 ? u & 1 : 0; };
-        auto tile = [&](int u) { return kTiles == 2 ? (act == 2 ? u >> 1 : u) : u; };
-        auto k_load = [&](int j) { return base + (uint32_t)(kTiles == 2 ? 2 * j : j < 2 ? j : 2 * j - 1); };
-        auto v_load = [&](int j) { return base + (uint32_t)(kTiles == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * p.len - 1)); };
-        auto scores = [&](int u) {
-          const int t = stream(u), j = tile(u), tq = kTiles == 2 ? t : 0;
-          const uint32_t ld = k_load(j), s = ld % kStages;
-          if (u < 2) {                             // the item's queries
-            if (!mbar_wait(bar(kQFull + tq), qs[tq] & 1u, limit, abort_flag)) return false;
+        const uint32_t len = __shfl_sync(0xFFFFFFFFu, p.len, 0);
+        const bool two = __shfl_sync(0xFFFFFFFFu, p.it.rows, 0) > 128, empty = __shfl_sync(0xFFFFFFFFu, p.it.tiles, 0) == 0;
+        if (empty) continue;
+        const uint32_t n = kTiles == 2 ? (t == 0 || two ? len : 0) : (len + 1 - t) / 2;   // the stream's jobs
+        auto take = [&](uint32_t ld) {             // waits for a load, releasing the other stream's before it
+          for (; next < ld; ++next) {
+            if (!wait(kFull + next % kStages, next / kStages & 1u)) return false;
+            if (mine) mbar_arrive(bs + 8u * (kEmpty + next % kStages));
           }
-          if (!mbar_wait(bar(kFull + (int)s), ld / kStages & 1u, limit, abort_flag)) return false;
+          return wait(kFull + ld % kStages, ld / kStages & 1u);
+        };
+        auto scores = [&](uint32_t i) {            // S of job i
+          const uint32_t j = kTiles == 2 ? i : 2 * i + t;
+          const uint32_t ld = base + (kTiles == 2 ? 2 * j : j < 2 ? j : 2 * j - 1), s = ld % kStages;
+          if (!take(ld)) return false;
+          next = ld + 1;
           tc_fence_after();
-          const uint32_t qa = sm32 + (uint32_t)tq * Sh::kTile, ka = sm32 + Sh::kStageOff + s * Sh::kTile;
+          const uint32_t qa = desc_low(smb + tq * Sh::kTile, 0), ka = desc_low(smb + Sh::kStageOff + s * Sh::kTile, 0);
+          if (mine) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u;
-            mma_bf16(tmem + 128u * (uint32_t)t, desc_sw128(qa + off, 16u, 1024u), desc_sw128(ka + off, 16u, 1024u), kIdescS,
-                     kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = ((uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u) >> 4;
+              if (kk == 0) mma_ss<false>(tb + 128u * t, qa, ka, kIdescS);
+              else mma_ss<true>(tb + 128u * t, qa + off, ka + off, kIdescS);
+            }
+            mma_commit(bs + 8u * (kSFull + t));
+            mma_commit(bs + 8u * (kEmpty + s));
+            if (i == n - 1) mma_commit(bs + 8u * (kQFree + tq));
           }
-          mma_commit(bar(kSFull + t));
-          if (kTiles == 1 || t == act - 1) mma_commit(bar(kEmpty + (int)s));
-          if (kTiles == 2 ? j == p.len - 1 : u == turns - 1) mma_commit(bar(kQFree + tq));
+          __syncwarp();
           return true;
         };
-        for (int u = 0; ok && u < act && u < turns; ++u) ok = scores(u);
-        for (int u = 0; ok && u < turns; ++u) {
-          const int t = stream(u), j = tile(u);
-          const uint32_t ld = v_load(j), s = ld % kStages;
-          ok = mbar_wait(bar(kPFull + t), jobs[t] & 1u, limit, abort_flag) &&
-               mbar_wait(bar(kFull + (int)s), ld / kStages & 1u, limit, abort_flag);
+        if (n > 0 || kTiles == 1) {
+          ok = wait(kQFull + tq, pieces & 1u);
+          ++pieces;
+          if (ok && n > 0) ok = scores(0);
+          else if (ok && mine) mbar_arrive(bs + 8u * kQFree);
+        }
+        for (uint32_t i = 0; ok && i < n; ++i) {
+          const uint32_t j = kTiles == 2 ? i : 2 * i + t;
+          // loads come in the order K0 V0 K1 V1 .. or K0 K1 V0 K2 V1 ..
+          const uint32_t ld = base + (kTiles == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * len - 1)), s = ld % kStages;
+          ok = take(ld) && wait(kPFull + t, jobs & 1u);
           if (!ok) break;
-          ++jobs[t];
+          next = ld + 1;
+          ++jobs;
           tc_fence_after();
-          const uint32_t va = sm32 + Sh::kStageOff + s * Sh::kTile;
-          const bool fresh = u < act;              // the stream's first tile of the item
+          const uint32_t va = desc_low(smb + Sh::kStageOff + s * Sh::kTile, 16384u);
+          if (mine) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16_ta(tmem + 256u + 128u * (uint32_t)t, tmem + 128u * (uint32_t)t + 8u * (uint32_t)kk,
-                        desc_sw128(va + (uint32_t)kk * 2048u, 16384u, 1024u), kIdescO, fresh && kk == 0 ? 0u : 1u);
-          mma_commit(bar(kODone + t));
-          if (kTiles == 1 || t == act - 1) mma_commit(bar(kEmpty + (int)s));
-          if (u + act < turns) ok = scores(u + act);
+            for (int kk = 0; kk < 8; ++kk)
+              mma_ts(tb + 256u + 128u * t, tb + 128u * t + 8u * (uint32_t)kk, va + (uint32_t)kk * (2048u >> 4), kIdescO,
+                     kk == 0 ? (i > 0 ? 1u : 0u) : 1u);
+            mma_commit(bs + 8u * (kODone + t));
+            mma_commit(bs + 8u * (kEmpty + s));
+          }
+          __syncwarp();
+          if (i + 1 < n) ok = scores(i + 1);
         }
-        base += 2u * (uint32_t)p.len;
-        ++qs[0];
-        if (kTiles == 2 && act == 2) ++qs[1];
+        base += 2u * len;
+        if (ok && next < base) {                   // what the other stream has left
+          ok = take(base - 1);
+          if (ok && mine) mbar_arrive(bs + 8u * (kEmpty + (base - 1) % kStages));
+          next = base;
+        }
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         raise_error(DSA_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
-      mma_commit(bar(kDrain));                     // everything issued has completed
-      mbar_wait(bar(kDrain), 0u, kCleanupWaitNs, nullptr);
-    } else if (warp == 13) {
-      // ================================ queries ================================
-      uint32_t loads0 = 0, loads1 = 0;
-      bool ok = true;
-      Piece p;
-      while (a.q_boxes && lane == 0 && ok && next_piece<kRows>(a, ps, p)) {
-        if (p.it.tiles == 0) continue;
-        for (int t = 0; ok && t < (kTiles == 2 && p.it.rows > 128 ? 2 : 1); ++t) {
-          ok = mbar_wait(bar(kQFree + t), ((t == 0 ? loads0 : loads1) & 1u) ^ 1u, limit, abort_flag);
-          if (!ok) break;
-          if (t == 0) ++loads0;
-          else ++loads1;
-          mbar_arrive_expect_tx(bar(kQFull + t), Sh::kTile);
-          const int token = p.it.s + (p.it.row0 + 128 * t) / a.G;
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sm32 + (uint32_t)t * Sh::kTile + 16384u * (uint32_t)h, &tmq, bar(kQFull + t), 64 * h, p.hk * a.G, token);
-        }
-      }
-      if (!ok) {
-        raise_error(DSA_DEVERR_TIMEOUT);
-        *abort_flag = 1;
-      }
-      if (loads0 > 0) mbar_wait(bar(kQFull), (loads0 - 1) & 1u, kCleanupWaitNs, nullptr);
-      if (loads1 > 0) mbar_wait(bar(kQFull + 1), (loads1 - 1) & 1u, kCleanupWaitNs, nullptr);
+      if (mine) mma_commit(bs + 8u * (kDrain + t));      // everything issued has completed
+      mbar_wait(bs + 8u * (kDrain + t), 0u, kCleanupWaitNs, nullptr);
     } else if (warp >= 14) {
-      // ================================ a look at values ================================
+      // ================================ queries, and a look at values ================================
       // Where some row sees a tile in part, its values that are no numbers are taken out (a zero weight would not silence
       // them); the rows that do see them get them back with the sums.  Keys outside the item's
       // range need no more: finite values under a zero weight are nothing.
@@ -900,13 +918,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       while (ok && next_piece<kRows>(a, ps, p)) {
         const Item& it = p.it;
         if (it.tiles == 0) continue;
-        // queries whose row tiles are no boxes: a piece of 16 bytes per thread and pass
-        for (int t = 0; !a.q_boxes && ok && t < (kTiles == 2 && it.rows > 128 ? 2 : 1); ++t) {
+        for (int t = 0; ok && t < (kTiles == 2 && it.rows > 128 ? 2 : 1); ++t) {
           constexpr int kPer = D / 8, kStep = 64 / kPer;
           ok = mbar_wait(bar(kQFree + t), ((t == 0 ? loads0 : loads1) & 1u) ^ 1u, limit, abort_flag);
           if (!ok) break;
           if (t == 0) ++loads0;
           else ++loads1;
+          if (a.q_boxes) {
+            if (lt == 0) {
+              mbar_arrive_expect_tx(bar(kQFull + t), Sh::kTile);
+              const int token = it.s + (it.row0 + 128 * t) / a.G;
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(sm32 + (uint32_t)t * Sh::kTile + 16384u * (uint32_t)h, &tmq, bar(kQFull + t), 64 * h, p.hk * a.G, token);
+            }
+            continue;
+          }
+          // row tiles that are no boxes: a piece of 16 bytes per thread and pass
           const int pc = lt % kPer;
           int row = 128 * t + lt / kPer;
           uint32_t token = (uint32_t)(it.row0 + row) / (uint32_t)a.G, g = (uint32_t)(it.row0 + row) % (uint32_t)a.G;
@@ -924,6 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           proxy_fence();
           mbar_arrive(bar(kQFull + t));
         }
+        ok = all_well(1, 64, ok);
         const Whole all = whole_tiles(a, it);
         for (int j = 0; ok && j < p.len; ++j) {
           const int tile = it.tile0 + p.t0 + j;
@@ -967,6 +995,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         raise_error(DSA_DEVERR_TIMEOUT);
         *abort_flag = 1;
       }
+      if (a.q_boxes && loads0 > 0) mbar_wait(bar(kQFull), (loads0 - 1) & 1u, kCleanupWaitNs, nullptr);
+      if (a.q_boxes && loads1 > 0) mbar_wait(bar(kQFull + 1), (loads1 - 1) & 1u, kCleanupWaitNs, nullptr);
     }
     __syncwarp();
   }
@@ -980,39 +1010,55 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 //   M = max(m_p, sink), out = sum_p 2^(m_p - M) O_p / (sum_p 2^(m_p - M) l_p + 2^(sink - M)).
 // Block c: the item whose first part is CTA c's (at most one); a warp per row.
 template <int D, int kRows>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a, int C) {
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ AttnArgs a) {
   grid_launch_dependents();
   grid_dependency_wait();
-  const int c = (int)blockIdx.x;
-  const int32_t* meta = a.meta + 8 * (c + 1);
-  if (meta[0] == 0) return;
-  const int b = meta[1], row0 = meta[2], rows = meta[3], hk = meta[4], last = meta[5];
-  const int lane = (int)threadIdx.x & 31;
-  for (int row = (int)(blockIdx.y * 8 + (threadIdx.x >> 5)); row < rows; row += (int)gridDim.y * 8) {
-    const int token = (row0 + row) / a.G, head = hk * a.G + (row0 + row) % a.G;
+  const int c = (int)blockIdx.x, lane = (int)threadIdx.x & 31;
+  const int4* meta = reinterpret_cast<const int4*>(a.meta) + 2 * (c + 1);
+  const int4 m0 = meta[0], m1 = meta[1];           // split, sequence, first row, rows; key head, last CTA
+  if (m0.x == 0) return;
+  const int hk = m1.x, parts = m1.y - c + 1;
+  const int s0 = a.start[m0.y];
+  const float2* ml = reinterpret_cast<const float2*>(a.ml);
+  // part i is in the owner's second slot or CTA c + i's first; a CTA without tiles (more CTAs than tiles) has none
+  auto slot_of = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+  for (int row = (int)(blockIdx.y * 8 + (threadIdx.x >> 5)); row < m0.w; row += (int)gridDim.y * 8) {
+    const int token = (m0.z + row) / a.G, head = hk * a.G + (m0.z + row) % a.G;
     const float sn = a.sink != nullptr ? a.sink[head] : -INFINITY, sk = sn * kLog2e;
-    const float2* ml = reinterpret_cast<const float2*>(a.ml);
-    // a CTA without a piece (more CTAs than tiles) has left nothing: its slot is marked
-    auto slot_of = [&](int p) { return p == c ? 2 * c + 1 : 2 * p; };
-    float M = sk;
-    for (int p = c; p <= last; ++p) {
-      if (p > c && a.meta[8 * (p + 1) + 6] == 0) continue;
-      M = fmaxf(M, ml[(int64_t)slot_of(p) * kRows + row].x);
-    }
-    float acc[D / 32], den = M == -INFINITY ? 0.f : ex2(sk - M);
+    float acc[D / 32], M = sk, den = 0.f;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
-    for (int p = c; p <= last; ++p) {
-      if (p > c && a.meta[8 * (p + 1) + 6] == 0) continue;
-      const float2 s = ml[(int64_t)slot_of(p) * kRows + row];
-      const float f = M == -INFINITY ? 1.f : ex2(s.x - M);
-      den = fmaf(s.y, f, den);
-      const float* o = a.part + ((int64_t)slot_of(p) * kRows + row) * D + lane * (D / 32);
+    // 32 parts at a time, their statistics a lane each; the sums so far move with the maximum
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+      const int i = i0 + lane;
+      const bool there = i < parts && (i == 0 || a.meta[8 * (c + i + 1) + 6] != 0);
+      const float2 s = there ? ml[(int64_t)slot_of(i) * kRows + row] : make_float2(-INFINITY, 0.f);
+      float top = s.x;
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(o[e], f, acc[e]);
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      top = fmaxf(top, M);
+      const float old = top == M ? 1.f : ex2(M - top);
+      M = top;
+      const float w = M == -INFINITY ? 1.f : ex2(s.x - M);
+      float part = there ? s.y * w : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
+      den = den * old + part;
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] *= old;
+      const uint32_t have = __ballot_sync(0xFFFFFFFFu, there);
+      const int n = min(32, parts - i0);
+#pragma unroll 8
+      for (int k = 0; k < n; ++k) {
+        const float f = __shfl_sync(0xFFFFFFFFu, w, k);
+        if (!(have >> k & 1u)) continue;
+        const float* o = a.part + ((int64_t)slot_of(i0 + k) * kRows + row) * D + lane * (D / 32);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(o[e], f, acc[e]);
+      }
     }
-    const int s0 = a.start[b];
     const bool none = M == -INFINITY && !(den != den);
+    den += M == -INFINITY ? 0.f : ex2(sk - M);
     const float inv = none ? 0.f : 1.f / den;
     uint16_t* dst = a.out + (int64_t)(s0 + token) * a.ldo + (int64_t)head * D + lane * (D / 32);
 #pragma unroll
@@ -1117,7 +1163,7 @@ cudaError_t launch_shape(const AttnArgs& a, const Maps& m, int ctas, cudaStream_
   }
   e = launch_pdl(kernel, dim3((unsigned)ctas), (unsigned)kThreads, Sh::kSmem, stream, m.q, m.k, m.v, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel<D, Sh::kRows>, dim3((unsigned)ctas, kTiles == 2 ? 8 : 2), 256u, 0, stream, a, ctas);
+  return launch_pdl(combine_kernel<D, Sh::kRows>, dim3((unsigned)ctas, kTiles == 2 ? 8 : 2), 256u, 0, stream, a);
 }
 
 }  // namespace
