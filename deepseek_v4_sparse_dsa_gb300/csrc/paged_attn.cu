@@ -15,19 +15,21 @@
 // In a CTA, two streams alternate on the tensor cores: while one's softmax runs, the other's products do.  With two row
 // tiles each is a stream, and both use every key tile; with one, the streams take the even and the odd key tiles with
 // sums of their own, joined at the item's end.
-//   S_t = Q_t K^T        128 x 128, both operands from shared memory
+//   S_t = Q_t K^T        128 x 64, half a key tile at a time, both operands from shared memory
 //   P_t = 2^(S c - m)    by the stream's four softmax warps, a row per thread: fp32 statistics, P rounded to bf16 and
-//                        written over S in tensor memory; the maximum moves only when a tile exceeds it by more than 8
-//                        in base 2 (P <= 2^8 loses nothing in bf16), and only then are the sums O_t rescaled
+//                        written over S in tensor memory; the maximum moves only when a half tile exceeds it by more
+//                        than 8 in base 2 (P <= 2^8 loses nothing in bf16), and only then are the sums O_t rescaled
 //   O_t += P_t V         A from tensor memory, V as stored (dims contiguous)
+// S_t has two buffers: the next half tile's scores are made while the softmax of this one runs, so that neither waits for
+// the other (with one buffer of a whole key tile per stream a tile of 256 rows took 4350 cycles).
 // The denominator sums the unrounded weights: P's rounding (2^-9 of each weight on average, as often up as down) then
 // touches the output as the output's own rounding does, and the lse not at all.
 //
 // Warps: 0-3 and 4-7 softmax, 8-11 bring keys and values (32 rows of each tile per warp) by tensor copies, 12 and 13
-// issue a stream's products each, 14 and 15 bring the queries and look through the values of tiles that some row sees in part.  Where the page
-// size is a multiple of 8, a copy's box is as many rows as divide both a page and a tile; other pages are gathered row by
-// row, four to a copy.  What no row of the item sees is asked for past the tensor's end, which reads as zeros.  Tensor
-// memory: S_t 2 x 128 columns, O_t 2 x 128.
+// issue a stream's products each, 14 and 15 bring the queries and look through the values of tiles that some row sees in
+// part.  Where the page size is a multiple of 8, a copy's box is as many rows as divide both a page and a tile; other
+// pages are gathered row by row, four to a copy.  What no row of the item sees is asked for past the tensor's end, which
+// reads as zeros.  Tensor memory: S_t 2 x 2 x 64 columns, O_t 2 x 128.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -312,34 +314,46 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint32_
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// Consecutive 32-bit columns of the thread's own lane: load (complete on return) and store (complete at the wait).
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
-      "{\n tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      " tcgen05.wait::ld.sync.aligned;\n}"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      "{\n tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n tcgen05.wait::ld.sync.aligned;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
+}
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+__device__ __forceinline__ void tmem_load(uint32_t taddr, uint32_t (&r)[64]) {
+  tmem_ld64_issue(taddr, r);
+  tmem_ld64_wait(r);
 }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Two fp32 operations at once.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Named barrier over n threads that also tells whether all of them are well.
@@ -399,12 +413,12 @@ struct Shape {
   static constexpr uint32_t kPlanOff = kStageOff + kStages * kTile;          // prefix, first, seq
   static constexpr uint32_t kMaskOff = kPlanOff + 8 * (kPlanMax + 8) + 4 * kPlanMax * 2;  // keys that exist [8][4] words
   static constexpr uint32_t kBadOff = kMaskOff + 8 * 16;            // values that are no numbers, per piece [16]
-  static constexpr uint32_t kStatOff = kBadOff + 64;                // (m, l) of both streams [2][128]
+  static constexpr uint32_t kStatOff = kBadOff + 64;                // (m, l) [stream][128]
   static constexpr uint32_t kBarOff = kStatOff + 2048;
-  static constexpr int kBars = 2 * kStages + 2 * 5 + 8 + 2;
+  static constexpr int kBars = 2 * kStages + 2 * 8 + 8 + 2;
   static constexpr uint32_t kCtlOff = kBarOff + 8 * 48;             // abort, TMEM base
   static constexpr uint32_t kScanOff = kCtlOff + 16;
-  static constexpr size_t kSmem = 1024 + kScanOff + 16 * 8;
+  static constexpr size_t kSmem = 1024 + kScanOff + kThreads / 32 * 8;
   static_assert(kBars <= 48 && kStages <= 8 && kSmem <= 232448, "shared memory");
 };
 
@@ -428,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   const uint32_t bars = sm32 + Sh::kBarOff;
   // barrier numbers: stages full, stages empty, then per stream, then a ring of the tiles that are looked through
   constexpr int kFull = 0, kEmpty = kStages, kQFull = 2 * kStages, kQFree = kQFull + 2, kSFull = kQFree + 2,
-                kPFull = kSFull + 2, kODone = kPFull + 2, kLook = kODone + 2, kDrain = kLook + 8;
+                kPFull = kSFull + 4, kODone = kPFull + 4, kLook = kODone + 4, kDrain = kLook + 8;
   auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
 
   const int warp = (int)threadIdx.x >> 5, lane = (int)threadIdx.x & 31;
@@ -441,9 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kQFull + t), a.q_boxes ? 1 : 64);
       mbar_init(bar(kQFree + t), kTiles == 2 ? 1 : 2);
-      mbar_init(bar(kSFull + t), 1);
-      mbar_init(bar(kPFull + t), 4);
-      mbar_init(bar(kODone + t), 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(kSFull + 2 * t + h), 1);
+        mbar_init(bar(kPFull + 2 * t + h), 4);
+        mbar_init(bar(kODone + 2 * t + h), 1);
+      }
     }
     for (int i = 0; i < 8; ++i) mbar_init(bar(kLook + i), 4);
     mbar_init(bar(kDrain), 1);
@@ -479,21 +495,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
   if (warp < 8) {
     // ================================ softmax ================================
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     const int t = warp >> 2;                       // stream
     const int r = 32 * (warp & 3) + lane;          // row in its tile = TMEM lane
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t tS = tl + 128u * (uint32_t)t, tO = tl + 256u + 128u * (uint32_t)t;
-    uint32_t jobs = 0;                             // of this stream so far
+    uint32_t jobs = 0;                             // key tiles of this stream so far
     uint32_t tiles_before = 0;                     // key tiles of the pieces before
+    uint32_t np = 0;                               // pieces so far that see any key
     bool ok = true;
     int32_t* my_meta = a.meta + 8 * (c + 1);
     if (threadIdx.x == 0) {
       my_meta[0] = 0;
       my_meta[6] = ps.end > ps.x;                  // whether it has any of the line
     }
+    const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+    auto stream_wait = [&](int which, uint32_t parity) -> bool {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar(which), parity & 1u, limit, abort_flag));
+    };
     Piece p;
-    uint32_t np = 0;                               // pieces so far that see any key
     while (ok && next_piece<kRows>(a, ps, p)) {
       const Item& it = p.it;
       const int row = (kTiles == 2 ? 128 * t : 0) + r;             // row of the item
@@ -504,94 +524,87 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       const int lo = low_key(a, pos), hi = high_key(a, it.L, pos);
       const bool warp_live = (kTiles == 2 ? 128 * t : 0) + 32 * (warp & 3) < it.rows;
       const bool empty = it.tiles == 0;
+      const Whole all = whole_tiles(a, it);
       const int step = kTiles == 2 ? 1 : 2, j0 = kTiles == 2 ? 0 : t;
-      const int mine = empty ? 0 : kTiles == 2 ? (128 * t < it.rows ? p.len : 0) : (p.len + 1 - t) / 2;   // jobs
+      const int mine = empty ? 0 : kTiles == 2 ? (128 * t < it.rows ? p.len : 0) : (p.len + 1 - t) / 2;   // key tiles
       float m = -INFINITY, l = 0.f;
       for (int i = 0; ok && i < mine; ++i, ++jobs) {
-        const int j = j0 + step * i;
-        ok = mbar_wait(bar(kSFull + t), jobs & 1u, limit, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (warp_live) {
-          tc_fence_after();
-          uint32_t s0[64], s1[64];
-          tmem_ld64_issue(tS, s0);
-          tmem_ld64_issue(tS + 64u, s1);
-          tmem_ld64_wait(s0);
-          tmem_ld64_wait(s1);
-          const int k0 = (it.tile0 + p.t0 + j) * kKeys;
-          const uint4 have = *reinterpret_cast<const uint4*>(mask_s + 4 * ((tiles_before + (uint32_t)j) & 7u));
-          const uint32_t w0 = have.x & bits_between(lo - k0, hi - k0), w1 = have.y & bits_between(lo - k0 - 32, hi - k0 - 32),
-                         w2 = have.z & bits_between(lo - k0 - 64, hi - k0 - 64), w3 = have.w & bits_between(lo - k0 - 96, hi - k0 - 96);
-          if (__any_sync(0xFFFFFFFFu, (w0 & w1 & w2 & w3) != ~0u)) {
-            const uint32_t none = __float_as_uint(-INFINITY);
+        const int j = j0 + step * i, tile = it.tile0 + p.t0 + j;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {              // half a tile: 64 keys, buffer h
+          ok = ok && stream_wait(kSFull + 2 * t + h, jobs);
+          if (!ok) break;
+          if (warp_live) {
+            tc_fence_after();
+            uint32_t x[64];
+            tmem_load(tS + 64u * (uint32_t)h, x);
+            // which of the keys the row sees
+            const uint2 have = *reinterpret_cast<const uint2*>(mask_s + 4 * ((tiles_before + (uint32_t)j) & 7u) + 2 * h);
+            uint32_t see0 = have.x, see1 = have.y;
+            if (!all.has(tile)) {
+              const int k0 = tile * kKeys + 64 * h;
+              see0 &= bits_between(lo - k0, hi - k0);
+              see1 &= bits_between(lo - k0 - 32, hi - k0 - 32);
+            }
+            if (__any_sync(0xFFFFFFFFu, (see0 & see1) != ~0u)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                x[e] = (see0 >> e) & 1u ? x[e] : __float_as_uint(-INFINITY);
+                x[32 + e] = (see1 >> e) & 1u ? x[32 + e] : __float_as_uint(-INFINITY);
+              }
+            }
+            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int e = 0; e < 64; e += 8)
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                top[q] = fmaxf(fmaxf(top[q], __uint_as_float(x[e + q])), __uint_as_float(x[e + 4 + q]));
+            const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+            const bool moves = mt > m + kLazy;
+            if (__any_sync(0xFFFFFFFFu, moves)) {
+              const float f = moves ? ex2(m - mt) : 1.f;
+              if (moves) {
+                m = mt;
+                l *= f;
+              }
+              if (i > 0 || h > 0) {                // the products of the half tile before have added to O
+                ok = h == 0 ? stream_wait(kODone + 2 * t + 1, jobs - 1u) : stream_wait(kODone + 2 * t, jobs);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int cc = 0; cc < D; cc += 32) {
+                  uint32_t o[32];
+                  tmem_load(tO + (uint32_t)cc, o);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_store(tO + (uint32_t)cc, o);
+                }
+              }
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            const uint64_t neg = pack2(-mm, -mm);
+            uint64_t sum2 = 0;
+            uint32_t pw[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              s0[e] = (w0 >> e) & 1u ? s0[e] : none;
-              s0[32 + e] = (w1 >> e) & 1u ? s0[32 + e] : none;
-              s1[e] = (w2 >> e) & 1u ? s1[e] : none;
-              s1[32 + e] = (w3 >> e) & 1u ? s1[32 + e] : none;
+              float pa, pb;
+              unpack2(fma2(pack2(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), scale2, neg), pa, pb);
+              pa = ex2(pa);
+              pb = ex2(pb);
+              sum2 = add2(sum2, pack2(pa, pb));
+              const __nv_bfloat162 w = __floats2bfloat162_rn(pa, pb);
+              pw[e] = *reinterpret_cast<const uint32_t*>(&w);
             }
+            tmem_store(tS + 64u * (uint32_t)h, pw);
+            float la, lb;
+            unpack2(sum2, la, lb);
+            l += la + lb;
+            tmem_st_wait();
+            tc_fence_before();
           }
-          float x0 = -INFINITY, x1 = -INFINITY, x2 = -INFINITY, x3 = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 64; e += 4) {
-            x0 = fmaxf(fmaxf(x0, __uint_as_float(s0[e])), __uint_as_float(s1[e]));
-            x1 = fmaxf(fmaxf(x1, __uint_as_float(s0[e + 1])), __uint_as_float(s1[e + 1]));
-            x2 = fmaxf(fmaxf(x2, __uint_as_float(s0[e + 2])), __uint_as_float(s1[e + 2]));
-            x3 = fmaxf(fmaxf(x3, __uint_as_float(s0[e + 3])), __uint_as_float(s1[e + 3]));
-          }
-          const float mt = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * a.scale_log2;
-          const bool moves = mt > m + kLazy;
-          const float f = moves ? ex2(m - mt) : 1.f;
-          if (moves) {
-            m = mt;
-            l *= f;
-          }
-          if (i > 0 && __any_sync(0xFFFFFFFFu, moves)) {
-            // the products of the job before have added to O
-            ok = mbar_wait(bar(kODone + t), (jobs - 1) & 1u, limit, abort_flag);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int cc = 0; cc < D; cc += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + (uint32_t)cc, o);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st32(tO + (uint32_t)cc, o);
-            }
-          }
-          const float mm = m == -INFINITY ? 0.f : m;
-          float l0 = 0.f, l1 = 0.f;
-          uint32_t pw[32];
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float pa = ex2(fmaf(__uint_as_float(s0[2 * e]), a.scale_log2, -mm));
-            const float pb = ex2(fmaf(__uint_as_float(s0[2 * e + 1]), a.scale_log2, -mm));
-            l0 += pa;
-            l1 += pb;
-            const __nv_bfloat162 h = __floats2bfloat162_rn(pa, pb);
-            pw[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          tmem_st32(tS, pw);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float pa = ex2(fmaf(__uint_as_float(s1[2 * e]), a.scale_log2, -mm));
-            const float pb = ex2(fmaf(__uint_as_float(s1[2 * e + 1]), a.scale_log2, -mm));
-            l0 += pa;
-            l1 += pb;
-            const __nv_bfloat162 h = __floats2bfloat162_rn(pa, pb);
-            pw[e] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          tmem_st32(tS + 32u, pw);
-          l += l0 + l1;
-          tmem_st_wait();
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kPFull + 2 * t + h));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPFull + t));
       }
       // ---- the item's rows (or its part of them)
       const bool whole = p.t0 == 0 && p.len == p.cost;
@@ -601,36 +614,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         my_meta[5] = (int)((p.end * C - 1) / line);                // the CTA that holds its last tile
         my_meta[0] = 1;
       }
-      if (ok && mine > 0) {
-        ok = mbar_wait(bar(kODone + t), (jobs - 1) & 1u, limit, abort_flag);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-      }
-      float m2 = -INFINITY, l2 = 0.f;                              // the other stream's
-      bool other = false;
+      if (ok && mine > 0) ok = stream_wait(kODone + 2 * t + 1, jobs - 1u);
+      float m2 = -INFINITY, l2 = 0.f;                              // one row tile: the other stream's
       if constexpr (kTiles == 1) {
         stat_s[128 * t + r] = make_float2(m, l);
         ok = all_well(2, 256, ok);
-        if (!ok) break;
         const float2 o = stat_s[128 * (t ^ 1) + r];
         m2 = o.x, l2 = o.y;
-        other = !empty && p.len > 1;                               // both streams had tiles
       }
       if (!ok) break;
       tc_fence_after();
       if (warp_live) {
-        // weights of the two streams' sums, and the joint statistics
-        const float M = fmaxf(m, m2);
-        float f = 1.f, f2 = 0.f;
+        // weights of the streams' sums (two where each has had tiles), and the joint statistics
+        const bool other = kTiles == 1 && !empty && p.len > 1;
+        float f0 = 1.f, f1 = 0.f;                                  // of the only sum, or of stream 0's and 1's
         if (kTiles == 1) {
-          f = M == -INFINITY ? 1.f : ex2(m - M);
-          f2 = M == -INFINITY ? 1.f : ex2(m2 - M);
-          l = l * f + l2 * f2;
+          const float M = fmaxf(m, m2);
+          const float fm = M == -INFINITY ? 1.f : ex2(m - M), fo = M == -INFINITY ? 1.f : ex2(m2 - M);
+          l = t == 0 ? l * fm + l2 * fo : l2 * fo + l * fm;
+          f0 = t == 0 ? fm : fo;
+          f1 = t == 0 ? fo : fm;
           m = M;
         }
+        const bool writer = kTiles == 2 || t == 0;
         const float sn = a.sink != nullptr ? a.sink[head] : -INFINITY, sk = sn * kLog2e;
-        float inv = 1.f;
         if (whole) {
           const float top = fmaxf(m, sk);
+          float inv;
           if (top == -INFINITY && !(l != l)) {
             inv = 0.f;
             l = -INFINITY;                                         // lse
@@ -639,41 +649,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             inv = g / den;
             l = (sk >= m ? sn : m * kLn2) + logf(den);
           }
-          if (a.lse != nullptr && live && (kTiles == 2 || t == 0)) a.lse[(int64_t)(it.s + token) * a.H + head] = l;
-        } else if (live && (kTiles == 2 || t == 0)) {
+          f0 *= inv, f1 *= inv;
+          if (a.lse != nullptr && live && writer) a.lse[(int64_t)(it.s + token) * a.H + head] = l;
+        } else if (live && writer) {
           reinterpret_cast<float2*>(a.ml)[(int64_t)slot * kRows + row] = make_float2(m, l);
         }
-        f *= inv, f2 *= inv;
         const bool bad = !empty && bad_s[np & 15u] != 0;
         constexpr int kCols = kTiles == 2 ? D : D / 2;             // of this warp; one row tile: half each
+        constexpr int kW = 32;
         const int c0 = kTiles == 2 ? 0 : t * kCols;
-        // which sums exist: with one tile the second stream has none
-        const bool has0 = !empty, has1 = other;
+        const uint32_t tA = kTiles == 2 ? tO : tl + 256u;          // the only sum, or stream 0's
 #pragma unroll
-        for (int cc = 0; cc < kCols; cc += 32) {
-          float o[32];
+        for (int cc = 0; cc < kCols; cc += kW) {
+          float o[kW];
           {
-            uint32_t w[32];
-            if (has0) {
-              tmem_ld32(kTiles == 2 ? tO + (uint32_t)cc : tl + 256u + (uint32_t)(c0 + cc), w);
-              const float g = kTiles == 2 || t == 0 ? f : f2;
+            uint32_t w[kW];
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(w[e]) * g;
-            } else {
+            for (int e = 0; e < kW; ++e) o[e] = 0.f;
+            if (!empty) {
+              tmem_load(tA + (uint32_t)(c0 + cc), w);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
+              for (int e = 0; e < kW; ++e) o[e] = __uint_as_float(w[e]) * f0;
             }
-            if (kTiles == 1 && has1) {
-              tmem_ld32(tl + 384u + (uint32_t)(c0 + cc), w);
-              const float g = t == 0 ? f2 : f;
+            if (other) {
+              tmem_load(tl + 384u + (uint32_t)(c0 + cc), w);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = fmaf(__uint_as_float(w[e]), g, o[e]);
+              for (int e = 0; e < kW; ++e) o[e] = fmaf(__uint_as_float(w[e]), f1, o[e]);
             }
           }
           if (bad && live) {
             // values that are no numbers were taken out of the tiles that some row sees in part: the rows that see them
             // get them back, as sums with them give
-            const Whole all = whole_tiles(a, it);
             for (int j = 0; j < p.len; ++j) {
               const int tile = it.tile0 + p.t0 + j;
               if (all.has(tile)) continue;
@@ -682,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 if (blk < 0 || blk >= a.num_blocks) continue;
                 const uint16_t* v = a.v + blk * a.block_stride + key % a.block_size * a.row_stride + p.hk * a.head_stride + c0 + cc;
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
+                for (int e = 0; e < kW; ++e)
                   if ((v[e] & 0x7F80u) == 0x7F80u) o[e] += __uint_as_float((uint32_t)v[e] << 16);
               }
             }
@@ -691,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             if (whole) {
               uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)(it.s + token) * a.ldo + (int64_t)head * D + c0 + cc);
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) {
+              for (int e = 0; e < kW; e += 8) {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -703,7 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             } else {
               float4* dst = reinterpret_cast<float4*>(a.part + ((int64_t)slot * kRows + row) * D + c0 + cc);
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+              for (int e = 0; e < kW; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
         }
@@ -723,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     // ================================ keys and values ================================
     // Lane l of warp w resolves row 32 w + l of each tile; lanes whose row begins a copy issue it (both halves of 128
     // dims by lanes of their own).
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     constexpr int kHalves = D / 64;
     const int w32 = 32 * (warp & 3);
     const int box = a.box, units = (box == 1 ? 8 : box >= 32 ? (w32 % box == 0 ? 1 : 0) : 32 / box) * kHalves;
@@ -814,13 +820,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     for (uint32_t i = loads > (uint32_t)kStages ? loads - kStages : 0; i < loads; ++i)
       mbar_wait(bar(kFull + (int)(i % kStages)), i / kStages & 1u, kCleanupWaitNs, nullptr);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp <= 13) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp < 14) {
       // ================================ products ================================
       // A warp per stream; its control flow is the same for all lanes (and the compiler can tell: what it depends on is
       // broadcast), so that the operands of a product are uniform and cost an addition each.  With one thread branching
       // off on its own, issuing the products of a tile took 3.4 times as long, and longer than the products.
-      constexpr uint32_t kIdescS = idesc_bf16(128, 128), kIdescO = idesc_bf16(128, D) | (1u << 16);   // V: dims contiguous
+      constexpr uint32_t kIdescS = idesc_bf16(128, 64), kIdescO = idesc_bf16(128, D) | (1u << 16);   // V: dims contiguous
       const uint32_t t = (uint32_t)__shfl_sync(0xFFFFFFFFu, warp - 12, 0), tq = kTiles == 2 ? t : 0;
       const uint32_t tb = __shfl_sync(0xFFFFFFFFu, tmem, 0), smb = __shfl_sync(0xFFFFFFFFu, sm32, 0);
       const uint32_t bs = smb + Sh::kBarOff;
@@ -845,23 +851,29 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           }
           return wait(kFull + ld % kStages, ld / kStages & 1u);
         };
-        auto scores = [&](uint32_t i) {            // S of job i
-          const uint32_t j = kTiles == 2 ? i : 2 * i + t;
-          const uint32_t ld = base + (kTiles == 2 ? 2 * j : j < 2 ? j : 2 * j - 1), s = ld % kStages;
-          if (!take(ld)) return false;
-          next = ld + 1;
-          tc_fence_after();
-          const uint32_t qa = desc_low(smb + tq * Sh::kTile, 0), ka = desc_low(smb + Sh::kStageOff + s * Sh::kTile, 0);
+        // job 2 i + h: keys 64 h .. of the stream's key tile i, buffer h.  Loads come in the order K0 V0 K1 V1 .. or
+        // K0 K1 V0 K2 V1 ..
+        auto tile = [&](uint32_t i) { return kTiles == 2 ? i : 2 * i + t; };
+        auto scores = [&](uint32_t i, uint32_t h) -> bool {
+          const uint32_t j = tile(i), ld = base + (kTiles == 2 ? 2 * j : j < 2 ? j : 2 * j - 1), s = ld % kStages;
+          if (h == 0) {
+            if (!take(ld)) return false;
+            next = ld + 1;
+            tc_fence_after();
+          }
+          const uint32_t qa = desc_low(smb + tq * Sh::kTile, 0), ka = desc_low(smb + Sh::kStageOff + s * Sh::kTile + 8192u * h, 0);
           if (mine) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((uint32_t)(kk >> 2) * 16384u + (uint32_t)(kk & 3) * 32u) >> 4;
-              if (kk == 0) mma_ss<false>(tb + 128u * t, qa, ka, kIdescS);
-              else mma_ss<true>(tb + 128u * t, qa + off, ka + off, kIdescS);
+              if (kk == 0) mma_ss<false>(tb + 128u * t + 64u * h, qa, ka, kIdescS);
+              else mma_ss<true>(tb + 128u * t + 64u * h, qa + off, ka + off, kIdescS);
             }
-            mma_commit(bs + 8u * (kSFull + t));
-            mma_commit(bs + 8u * (kEmpty + s));
-            if (i == n - 1) mma_commit(bs + 8u * (kQFree + tq));
+            mma_commit(bs + 8u * (kSFull + 2 * t + h));
+            if (h == 1) {
+              mma_commit(bs + 8u * (kEmpty + s));
+              if (i == n - 1) mma_commit(bs + 8u * (kQFree + tq));
+            }
           }
           __syncwarp();
           return true;
@@ -869,29 +881,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         if (n > 0 || kTiles == 1) {
           ok = wait(kQFull + tq, pieces & 1u);
           ++pieces;
-          if (ok && n > 0) ok = scores(0);
+          if (ok && n > 0) ok = scores(0, 0) && scores(0, 1);
           else if (ok && mine) mbar_arrive(bs + 8u * kQFree);
         }
-        for (uint32_t i = 0; ok && i < n; ++i) {
-          const uint32_t j = kTiles == 2 ? i : 2 * i + t;
-          // loads come in the order K0 V0 K1 V1 .. or K0 K1 V0 K2 V1 ..
+        for (uint32_t i = 0; ok && i < n; ++i, ++jobs) {
+          const uint32_t j = tile(i);
           const uint32_t ld = base + (kTiles == 2 ? 2 * j + 1 : min(2 * j + 2, 2 * len - 1)), s = ld % kStages;
-          ok = take(ld) && wait(kPFull + t, jobs & 1u);
-          if (!ok) break;
+          ok = take(ld);
           next = ld + 1;
-          ++jobs;
-          tc_fence_after();
           const uint32_t va = desc_low(smb + Sh::kStageOff + s * Sh::kTile, 16384u);
-          if (mine) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              mma_ts(tb + 256u + 128u * t, tb + 128u * t + 8u * (uint32_t)kk, va + (uint32_t)kk * (2048u >> 4), kIdescO,
-                     kk == 0 ? (i > 0 ? 1u : 0u) : 1u);
-            mma_commit(bs + 8u * (kODone + t));
-            mma_commit(bs + 8u * (kEmpty + s));
+          for (uint32_t h = 0; h < 2; ++h) {
+            ok = ok && wait(kPFull + 2 * t + h, jobs & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            if (mine) {
+#pragma unroll
+              for (uint32_t kk = 0; kk < 4; ++kk)
+                mma_ts(tb + 256u + 128u * t, tb + 128u * t + 64u * h + 8u * kk, va + (4 * h + kk) * (2048u >> 4), kIdescO,
+                       h == 0 && kk == 0 ? (i > 0 ? 1u : 0u) : 1u);
+              mma_commit(bs + 8u * (kODone + 2 * t + h));
+              if (h == 1) mma_commit(bs + 8u * (kEmpty + s));
+            }
+            __syncwarp();
+            if (i + 1 < n) ok = scores(i + 1, h);
           }
-          __syncwarp();
-          if (i + 1 < n) ok = scores(i + 1);
         }
         base += 2u * len;
         if (ok && next < base) {                   // what the other stream has left
@@ -906,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       }
       if (mine) mma_commit(bs + 8u * (kDrain + t));      // everything issued has completed
       mbar_wait(bs + 8u * (kDrain + t), 0u, kCleanupWaitNs, nullptr);
-    } else if (warp >= 14) {
+    } else {
       // ================================ queries, and a look at values ================================
       // Where some row sees a tile in part, its values that are no numbers are taken out (a zero weight would not silence
       // them); the rows that do see them get them back with the sums.  Keys outside the item's
@@ -921,6 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         for (int t = 0; ok && t < (kTiles == 2 && it.rows > 128 ? 2 : 1); ++t) {
           constexpr int kPer = D / 8, kStep = 64 / kPer;
           ok = mbar_wait(bar(kQFree + t), ((t == 0 ? loads0 : loads1) & 1u) ^ 1u, limit, abort_flag);
+          ok = all_well(1, 64, ok);                // both warps have seen it: the copy may bring its next phase about
           if (!ok) break;
           if (t == 0) ++loads0;
           else ++loads1;
@@ -951,7 +966,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           proxy_fence();
           mbar_arrive(bar(kQFull + t));
         }
-        ok = all_well(1, 64, ok);
         const Whole all = whole_tiles(a, it);
         for (int j = 0; ok && j < p.len; ++j) {
           const int tile = it.tile0 + p.t0 + j;
@@ -1153,8 +1167,8 @@ cudaError_t launch_shape(const AttnArgs& a, const Maps& m, int ctas, cudaStream_
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, kernel);
     if (e != cudaSuccess) return e;
-    // the warps' shares, 2 x 192 + 2 x 64 registers a thread, are those of the launch
-    if (fa.numRegs * kThreads < 128 * (2 * 192 + 2 * 64)) return cudaErrorInvalidConfiguration;
+    // the warps' shares, 2 x 168 + 2 x 88 registers a thread, are those of the launch
+    if (fa.numRegs * kThreads < 128 * (2 * 168 + 2 * 88)) return cudaErrorInvalidConfiguration;
     if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
   }
   if (a.planned) {
