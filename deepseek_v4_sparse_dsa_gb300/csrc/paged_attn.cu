@@ -47,7 +47,7 @@ constexpr int kThreads = 512;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;                // base-2 headroom before the running maximum moves
-constexpr int kPlanMax = 1024;               // items (and sequences) that a CTA plans by itself
+constexpr int kPlanMax = 512;                // row blocks (and sequences) that a CTA plans by itself
 constexpr int kItemCost = 2;                 // an item's fixed cost, in key tiles
 
 struct AttnArgs {
@@ -243,6 +243,7 @@ struct Piece {
   int hk;                      // key head
   int t0, len, cost;           // key tiles t0 .. t0 + len - 1 of the item's `cost`
   int64_t end;                 // where the item ends on the line
+  int block = -1;              // the row block that `it` describes (that of several key heads in a row)
 };
 
 template <int kRows>
@@ -261,9 +262,12 @@ __device__ __forceinline__ bool next_piece(const AttnArgs& a, Pieces& ps, Piece&
     p.end = ps.x + (length - to);
     if (p.hk == ps.Hkv - 1 && to == length) ++ps.e;
     if (p.len == 0) continue;                      // the slice ends within the item's fixed cost
-    const int b = ps.seq[e];
-    bool bad = false;
-    p.it = make_item<kRows>(a, sequence(a, b, bad), b, e - ps.first[b]);
+    if (e != p.block) {
+      const int b = ps.seq[e];
+      bool bad = false;
+      p.it = make_item<kRows>(a, sequence(a, b, bad), b, e - ps.first[b]);
+      p.block = e;
+    }
     return true;
   }
   return false;
@@ -413,7 +417,8 @@ struct Shape {
   static constexpr uint32_t kPlanOff = kStageOff + kStages * kTile;          // prefix, first, seq
   static constexpr uint32_t kMaskOff = kPlanOff + 8 * (kPlanMax + 8) + 4 * kPlanMax * 2;  // keys that exist [8][4] words
   static constexpr uint32_t kBadOff = kMaskOff + 8 * 16;            // values that are no numbers, per piece [16]
-  static constexpr uint32_t kStatOff = kBadOff + 64;                // (m, l) [stream][128]
+  static constexpr uint32_t kOutOff = kBadOff + 64;                 // results on their way out, 2 KB per softmax warp
+  static constexpr uint32_t kStatOff = kOutOff + 8 * 2048;              // (m, l) [stream][128]
   static constexpr uint32_t kBarOff = kStatOff + 2048;
   static constexpr int kBars = 2 * kStages + 2 * 8 + 8 + 2;
   static constexpr uint32_t kCtlOff = kBarOff + 8 * 48;             // abort, TMEM base
@@ -510,6 +515,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       my_meta[6] = ps.end > ps.x;                  // whether it has any of the line
     }
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
+    uint8_t* stage = sm + Sh::kOutOff + 2048 * warp;   // 64 bytes of 32 rows
+    int block = -1, token = 0, group = 0, lo = 0, hi = 0;      // of the row, while the row block is the same
+    Whole all{0, 0};
     auto stream_wait = [&](int which, uint32_t parity) -> bool {
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar(which), parity & 1u, limit, abort_flag));
     };
@@ -518,13 +526,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       const Item& it = p.it;
       const int row = (kTiles == 2 ? 128 * t : 0) + r;             // row of the item
       const bool live = row < it.rows;
-      const int gr = it.row0 + (live ? row : 0);
-      const int token = gr / a.G, head = p.hk * a.G + gr % a.G;
-      const int pos = it.L - it.n + token;
-      const int lo = low_key(a, pos), hi = high_key(a, it.L, pos);
+      if (p.block != block) {
+        block = p.block;
+        const int gr = it.row0 + (live ? row : 0);
+        token = gr / a.G, group = gr - token * a.G;
+        const int pos = it.L - it.n + token;
+        lo = low_key(a, pos), hi = high_key(a, it.L, pos);
+        all = whole_tiles(a, it);
+      }
+      const int head = p.hk * a.G + group;
       const bool warp_live = (kTiles == 2 ? 128 * t : 0) + 32 * (warp & 3) < it.rows;
       const bool empty = it.tiles == 0;
-      const Whole all = whole_tiles(a, it);
       const int step = kTiles == 2 ? 1 : 2, j0 = kTiles == 2 ? 0 : t;
       const int mine = empty ? 0 : kTiles == 2 ? (128 * t < it.rows ? p.len : 0) : (p.len + 1 - t) / 2;   // key tiles
       float m = -INFINITY, l = 0.f;
@@ -655,9 +667,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           reinterpret_cast<float2*>(a.ml)[(int64_t)slot * kRows + row] = make_float2(m, l);
         }
         const bool bad = !empty && bad_s[np & 15u] != 0;
+        const int least_hi = bad ? high_key(a, it.L, it.L - it.n + it.row0 / a.G) : 0;
+        const int most_lo = bad ? low_key(a, it.L - it.n + (it.row0 + it.rows - 1) / a.G) : 0;
         constexpr int kCols = kTiles == 2 ? D : D / 2;             // of this warp; one row tile: half each
         constexpr int kW = 32;
         const int c0 = kTiles == 2 ? 0 : t * kCols;
+        // where the rows that the lane writes begin, and how many rows the warp has
+        const int live_rows = min(32, it.rows - (row - lane));
+        const int64_t at = (int64_t)(it.s + token) * a.ldo + (int64_t)head * D;
+        int64_t to[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = __shfl_sync(0xFFFFFFFFu, at, 8 * i + (lane >> 2));
         const uint32_t tA = kTiles == 2 ? tO : tl + 256u;          // the only sum, or stream 0's
 #pragma unroll
         for (int cc = 0; cc < kCols; cc += kW) {
@@ -684,6 +704,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
               const int tile = it.tile0 + p.t0 + j;
               if (all.has(tile)) continue;
               for (int64_t key = max((int64_t)tile * kKeys, (int64_t)lo); key < min((int64_t)(tile + 1) * kKeys, (int64_t)hi); ++key) {
+                // (values of 32 keys that every row sees were left in their place)
+                if (key / 32 * 32 >= most_lo && key / 32 * 32 + 32 <= least_hi) continue;
                 const int blk = a.table[it.b * a.bt_stride + key / a.block_size];
                 if (blk < 0 || blk >= a.num_blocks) continue;
                 const uint16_t* v = a.v + blk * a.block_stride + key % a.block_size * a.row_stride + p.hk * a.head_stride + c0 + cc;
@@ -693,23 +715,43 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
               }
             }
           }
-          if (live) {
-            if (whole) {
-              uint4* dst = reinterpret_cast<uint4*>(a.out + (int64_t)(it.s + token) * a.ldo + (int64_t)head * D + c0 + cc);
+          // 64 bytes of each row go through shared memory, so that four lanes write a row's 64 neighbouring bytes (a row
+          // per lane made the writes of 256 rows take 5 us): piece q of row r at q ^ (r / 2 % 4), free of conflicts
+          auto put = [&](const uint4 (&v)[4], auto place) {
 #pragma unroll
-              for (int e = 0; e < kW; e += 8) {
-                uint32_t w[4];
+            for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(stage + 64 * lane + 16 * (q ^ (lane >> 1 & 3))) = v[q];
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const __nv_bfloat162 h = __floats2bfloat162_rn(o[e + 2 * i], o[e + 2 * i + 1]);
-                  w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                dst[e / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i) {
+              const int rr = 8 * i + (lane >> 2), q = lane & 3;
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + 64 * rr + 16 * (q ^ (rr >> 1 & 3)));
+              if (rr < live_rows) *reinterpret_cast<uint4*>(place(i, rr) + 16 * q) = w;
+            }
+            __syncwarp();
+          };
+          uint4 v[4];
+          if (whole) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(o[8 * q + 2 * i], o[8 * q + 2 * i + 1]);
+                w[i] = *reinterpret_cast<const uint32_t*>(&h);
               }
-            } else {
-              float4* dst = reinterpret_cast<float4*>(a.part + ((int64_t)slot * kRows + row) * D + c0 + cc);
+              v[q] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            put(v, [&](int i, int) { return reinterpret_cast<uint8_t*>(a.out + to[i] + c0 + cc); });
+          } else {
 #pragma unroll
-              for (int e = 0; e < kW; e += 4) dst[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 32; e += 16) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                v[q] = make_uint4(__float_as_uint(o[e + 4 * q]), __float_as_uint(o[e + 4 * q + 1]),
+                                  __float_as_uint(o[e + 4 * q + 2]), __float_as_uint(o[e + 4 * q + 3]));
+              put(v, [&](int, int rr) {
+                return reinterpret_cast<uint8_t*>(a.part + ((int64_t)slot * kRows + row - lane + rr) * D + c0 + cc + e);
+              });
             }
           }
         }
@@ -927,6 +969,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       // range need no more: finite values under a zero weight are nothing.
       uint32_t base = 0, looked = 0, np = 0, loads0 = 0, loads1 = 0;
       const int lt = (int)threadIdx.x - 14 * 32;
+      int block = -1, least_hi = 0, most_lo = 0;
+      Whole all{0, 0};
       bool ok = true;
       Piece p;
       while (ok && next_piece<kRows>(a, ps, p)) {
@@ -966,7 +1010,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           proxy_fence();
           mbar_arrive(bar(kQFull + t));
         }
-        const Whole all = whole_tiles(a, it);
+        if (p.block != block) {
+          block = p.block;
+          all = whole_tiles(a, it);
+          least_hi = high_key(a, it.L, it.L - it.n + it.row0 / a.G);
+          most_lo = low_key(a, it.L - it.n + (it.row0 + it.rows - 1) / a.G);
+        }
         for (int j = 0; ok && j < p.len; ++j) {
           const int tile = it.tile0 + p.t0 + j;
           if (all.has(tile)) continue;
@@ -975,25 +1024,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           ok = __all_sync(0xFFFFFFFFu, ok);
           ++looked;
           if (ok) {
-            // thread: 16-byte column lt % 8 of every eighth row, half by half
+            // Thread: 16-byte column lt % 8 of every eighth row, half by half.  A half word is no number where its
+            // exponent's bits are all set: then adding one in the lowest of them carries into the sign's place.
             uint8_t* at = sm + Sh::kStageOff + st * Sh::kTile + (lt >> 3) * 128 + (lt & 7) * 16;
             const int64_t k0 = (int64_t)tile * kKeys + (lt >> 3);
             bool found = false;
-#pragma unroll 4
-            for (int i = 0; i < 16 * (D / 64); ++i) {
-              uint4* here = reinterpret_cast<uint4*>(at + 1024 * i);
-              const int64_t key = k0 + 8 * (i & 15);
-              uint4 w = *here;
-              uint32_t* ww = reinterpret_cast<uint32_t*>(&w);
-              bool change = false;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 16; i0 += 4) {   // 32 keys; those that every row sees need no look
+              const int64_t first = (int64_t)tile * kKeys + 8 * i0;
+              if (first >= most_lo && first + 32 <= least_hi) continue;
+              uint4 w[4 * (D / 64)];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((ww[e] & 0x7F80u) == 0x7F80u) ww[e] &= 0xFFFF0000u, change = true;
-                if ((ww[e] & 0x7F800000u) == 0x7F800000u) ww[e] &= 0x0000FFFFu, change = true;
-              }
-              if (change) {
-                *here = w;
-                found |= key >= it.lo && key < it.hi;
+              for (int i = 0; i < 4 * (D / 64); ++i) w[i] = *reinterpret_cast<uint4*>(at + 1024 * (i0 + (i & 3) + 16 * (i >> 2)));
+              uint32_t any = 0;
+#pragma unroll
+              for (int i = 0; i < 4 * (D / 64); ++i)
+                any |= ((w[i].x & 0x7F807F80u) + 0x00800080u) | ((w[i].y & 0x7F807F80u) + 0x00800080u) |
+                       ((w[i].z & 0x7F807F80u) + 0x00800080u) | ((w[i].w & 0x7F807F80u) + 0x00800080u);
+              if ((any & 0x80008000u) == 0) continue;
+#pragma unroll 1
+              for (int i = 0; i < 4 * (D / 64); ++i) {
+                const int64_t key = k0 + 8 * (i0 + (i & 3));
+                uint32_t* here = reinterpret_cast<uint32_t*>(at + 1024 * (i0 + (i & 3) + 16 * (i >> 2)));
+                for (int e = 0; e < 4; ++e) {
+                  const uint32_t v = here[e];
+                  uint32_t u = v;
+                  if ((u & 0x7F80u) == 0x7F80u) u &= 0xFFFF0000u;
+                  if ((u & 0x7F800000u) == 0x7F800000u) u &= 0x0000FFFFu;
+                  if (u != v) {
+                    here[e] = u;
+                    found |= key >= it.lo && key < it.hi;
+                  }
+                }
               }
             }
             if (found) bad_s[np & 15u] = 1;
@@ -1177,7 +1239,7 @@ cudaError_t launch_shape(const AttnArgs& a, const Maps& m, int ctas, cudaStream_
   }
   e = launch_pdl(kernel, dim3((unsigned)ctas), (unsigned)kThreads, Sh::kSmem, stream, m.q, m.k, m.v, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel<D, Sh::kRows>, dim3((unsigned)ctas, kTiles == 2 ? 8 : 2), 256u, 0, stream, a);
+  return launch_pdl(combine_kernel<D, Sh::kRows>, dim3((unsigned)ctas, Sh::kRows / 8), 256u, 0, stream, a);
 }
 
 }  // namespace
