@@ -565,12 +565,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 x[32 + e] = (see1 >> e) & 1u ? x[32 + e] : __float_as_uint(-INFINITY);
               }
             }
-            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float top[8];
 #pragma unroll
-            for (int e = 0; e < 64; e += 8)
+            for (int q = 0; q < 8; ++q) top[q] = fmaxf(__uint_as_float(x[q]), __uint_as_float(x[8 + q]));
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
-                top[q] = fmaxf(fmaxf(top[q], __uint_as_float(x[e + q])), __uint_as_float(x[e + 4 + q]));
+            for (int e = 16; e < 64; e += 16)
+#pragma unroll
+              for (int q = 0; q < 8; ++q) top[q] = fmaxf(fmaxf(top[q], __uint_as_float(x[e + q])), __uint_as_float(x[e + 8 + q]));
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top[q] = fmaxf(top[q], top[4 + q]);
             const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
             const bool moves = mt > m + kLazy;
             if (__any_sync(0xFFFFFFFFu, moves)) {
