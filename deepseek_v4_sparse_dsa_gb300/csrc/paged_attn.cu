@@ -496,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   }
   const int64_t C = gridDim.x, c = blockIdx.x;
   const int64_t line = count > 0 ? ps.prefix[count] * a.Hkv : 0;
-  ps.begin(count, line * c / C, line * (c + 1) / C);
+  if (line < (1 << 22)) ps.begin(count, (uint32_t)line * (uint32_t)c / (uint32_t)C, (uint32_t)line * (uint32_t)(c + 1) / (uint32_t)C);
+  else ps.begin(count, line * c / C, line * (c + 1) / C);      // (a 64-bit division takes several times as long)
 
   if (warp < 8) {
     // ================================ softmax ================================
@@ -999,7 +1000,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           const int pc = lt % kPer;
           int row = 128 * t + lt / kPer;
           uint32_t token = (uint32_t)(it.row0 + row) / (uint32_t)a.G, g = (uint32_t)(it.row0 + row) % (uint32_t)a.G;
-#pragma unroll 2
+          const uint32_t more = (uint32_t)kStep / (uint32_t)a.G, left = (uint32_t)kStep % (uint32_t)a.G;
+#pragma unroll 4
           for (int i = 0; i < 128 / kStep; ++i) {
             const int r = row & 127;
             const bool on = row < it.rows;
@@ -1007,7 +1009,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             copy16(sm32 + (uint32_t)t * Sh::kTile + (uint32_t)(pc >> 3) * 16384u + (uint32_t)r * 128u +
                        (uint32_t)(((pc & 7) ^ (r & 7)) << 4), src, on);
             row += kStep;
-            for (g += kStep; g >= (uint32_t)a.G; g -= (uint32_t)a.G) ++token;
+            token += more, g += left;
+            if (g >= (uint32_t)a.G) g -= (uint32_t)a.G, ++token;
           }
           copies_wait();
           proxy_fence();

@@ -21,7 +21,9 @@ namespace {
 // An angle is needed modulo a turn only.  With W_i = f_i / 2 pi turns as a 64-bit binary fraction, the product p W_i
 // modulo 2^64 is the angle's fraction of a turn, exact but for W's own rounding (p 2^-65 turns): far positions lose
 // nothing and no 64-bit floating point is needed.  The nearest quarter turn is taken off before the conversion to
-// fp32, so that what is left, at most 1/8 turn, keeps 24 significant bits.
+// fp32, so that what is left, at most 1/8 turn, keeps 24 significant bits; there the Taylor polynomials of degree 9 and 8
+// are within 2.5e-8 of the sine and the cosine (the terms left out: x^11 / 11!, x^10 / 10! at pi / 4).
+// Bound by the writes once a pair costs few enough instructions: 1 M positions x 64 took 74 us with sincospi.
 struct TableArgs {
   uint64_t turn[128];        // f_i / 2 pi in units of 2^-64 turns
   int64_t pos0, n;
@@ -32,15 +34,16 @@ struct TableArgs {
 };
 
 __device__ __forceinline__ void write_angle(const TableArgs& a, int64_t row, int i, uint64_t phase) {
-  const uint64_t quarter = (phase + (1ull << 61)) >> 62;                   // nearest quarter turn (0..3, wrapping)
-  const float x = (float)(int64_t)(phase - (quarter << 62)) * 0x1p-63f;    // in half turns, |x| <= 1/4
-  float s, c;
-  sincospif(x, &s, &c);
+  const uint32_t high = (uint32_t)(phase >> 32), quarter = (high + 0x20000000u) >> 30;      // nearest quarter turn
+  const int64_t rest = (int64_t)((uint64_t)(high - (quarter << 30)) << 32 | (uint32_t)phase);
+  const float x = (float)rest * 0x1.921fb6p-62f, z = x * x;                                  // 2 pi / 2^64
+  const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
   const bool swap = (quarter & 1u) != 0u;
   const float cv = swap ? s : c, sv = swap ? c : s;
   float* o = a.out + row * (2 * a.half) + i;
-  o[0] = a.amplitude * ((quarter == 1u || quarter == 2u) ? -cv : cv);
-  o[a.half] = a.amplitude * (quarter >= 2u ? -sv : sv);
+  o[0] = a.amplitude * ((quarter + 1u & 2u) ? -cv : cv);
+  o[a.half] = a.amplitude * ((quarter & 2u) ? -sv : sv);
 }
 
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs a) {
@@ -79,7 +82,7 @@ struct HeadArgs {
   int R, off, D;
   float sign;                // -1: the rotation is taken back
   int64_t T;
-  int chunks;                // vector kernel: groups of kHeadsPer heads of a token
+  int chunks, q_chunks, k_chunks;   // vector kernel: groups of kHeadsPer heads of a token, of queries, of keys
 };
 
 constexpr int kHeadsPer = 4;                       // heads a lane group takes at a time, their loads in flight together
@@ -135,14 +138,15 @@ __device__ __forceinline__ void store4(void* base, int64_t at, const float (&f)[
 
 // A group of 2^kLg lanes holds a head, two units of four elements per lane, so that both elements of every pair are in
 // one lane: in the half layout unit a of the first half and its partner of the second; interleaved pairs lie within a
-// unit.  Both ways a warp's access covers whole neighbouring sectors.  A group takes kHeadsPer heads of one token at a
-// time: their loads are in flight together, and the token's cos and sin are read once for them.
+// unit.  Both ways a warp's access covers whole neighbouring sectors.  A group takes kHeadsPer heads of one token and one
+// kind (query, key, value) at a time: their loads are in flight together, and addresses, cos, sin and the gains are found
+// once for them.
 template <bool F32, bool kNorm, bool kHalf, int kLg>
 __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__ HeadArgs a) {
   using U = Unit<F32>;
   const int l = (int)threadIdx.x & ((1 << kLg) - 1);
   const int units = a.D >> 2;
-  // the lane's units (-1: none), and whether they turn
+  // the lane's units, and whether they turn
   int ua, ub;
   bool ra, rb;
   if constexpr (kHalf) {
@@ -157,7 +161,7 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
       ra = rb = false;
     }
   } else {
-    ua = 2 * l < units ? l : -1, ub = l + (units >> 1);
+    ua = l, ub = l + (units >> 1);
     ra = 4 * ua >= a.off && 4 * ua < a.off + a.R;
     rb = 4 * ub >= a.off && 4 * ub < a.off + a.R;
   }
@@ -167,40 +171,32 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
   grid_launch_dependents();
   grid_dependency_wait();
 
-  float gq[8], gk[8];
-  if constexpr (kNorm) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      gq[e] = live && a.H > 0 ? a.gq[da + e] : 0.f, gq[4 + e] = live && a.H > 0 ? a.gq[db + e] : 0.f;
-      gk[e] = live && a.Hkv > 0 ? a.gk[da + e] : 0.f, gk[4 + e] = live && a.Hkv > 0 ? a.gk[db + e] : 0.f;
-    }
-  }
   const uint32_t total = (uint32_t)(a.T * a.chunks);
   const uint32_t step = gridDim.x * (256u >> kLg);
   for (uint32_t c = blockIdx.x * (256u >> kLg) + (threadIdx.x >> kLg); __any_sync(0xFFFFFFFFu, c < total); c += step) {
     const bool on = live && c < total;
-    const uint32_t t = c / (uint32_t)a.chunks;
-    const int h0 = (int)(c - t * (uint32_t)a.chunks) * kHeadsPer;
+    const int64_t t = c / (uint32_t)a.chunks;
+    const int j = (int)(c - (uint32_t)t * (uint32_t)a.chunks);
+    const int kind = j < a.q_chunks ? 0 : j < a.q_chunks + a.k_chunks ? 1 : 2;
+    const int h0 = (kind == 0 ? j : kind == 1 ? j - a.q_chunks : j - a.q_chunks - a.k_chunks) * kHeadsPer;
+    const int n = on ? min(kHeadsPer, (kind == 0 ? a.H : a.Hkv) - h0) : 0;
+    const int64_t hop = kind == 0 ? a.hq : a.D;    // from head to head
+    const int64_t from = (kind == 0 ? t * a.ldq : kind == 1 ? t * a.ldk : t * a.ldv) + h0 * hop;
+    const char* src = static_cast<const char*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + from * U::kSize;
     typename U::Raw xa[kHeadsPer], xb[kHeadsPer];
 #pragma unroll
     for (int u = 0; u < kHeadsPer; ++u) {
-      const int h = h0 + u;
-      if (on && h < a.heads) {
-        const char* p;
-        if (h < a.H) p = static_cast<const char*>(a.q) + ((int64_t)t * a.ldq + h * a.hq) * U::kSize;
-        else if (h < a.H + a.Hkv) p = static_cast<const char*>(a.k) + ((int64_t)t * a.ldk + (int64_t)(h - a.H) * a.D) * U::kSize;
-        else p = static_cast<const char*>(a.v) + ((int64_t)t * a.ldv + (int64_t)(h - a.H - a.Hkv) * a.D) * U::kSize;
-        xa[u] = *reinterpret_cast<const typename U::Raw*>(p + da * U::kSize);
-        xb[u] = *reinterpret_cast<const typename U::Raw*>(p + db * U::kSize);
-      } else {
-        xa[u] = typename U::Raw{};
-        xb[u] = typename U::Raw{};
+      xa[u] = typename U::Raw{};
+      xb[u] = typename U::Raw{};
+      if (u < n) {
+        xa[u] = *reinterpret_cast<const typename U::Raw*>(src + (u * hop + da) * U::kSize);
+        xb[u] = *reinterpret_cast<const typename U::Raw*>(src + (u * hop + db) * U::kSize);
       }
     }
     // cos and sin of the lane's pairs: pair j of unit a (of both units in the half layout) at cs[j], sn[j]
     float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
     bool known = true;
-    if (on && (ra || rb) && h0 < a.H + a.Hkv) {
+    if (on && (ra || rb) && kind < 2) {
       const int64_t pos = a.positions[t];
       known = pos >= 0 && pos < a.max_pos;
       if (known) {
@@ -224,81 +220,94 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) sn[e] *= a.sign;
-      } else {
+      } else {                                     // rotated dims become zeros
         raise_error(DSA_DEVERR_INDEX);
       }
     }
-    int64_t at = -1;
-    if (on && a.kv.k != nullptr && h0 + kHeadsPer > a.H) at = cache_offset(a, t);
+    // where the heads go: rows of `type`, rows of the cache, both
+    char* dst = nullptr;
+    int64_t dst_hop = a.D;
+    uint16_t* page = nullptr;
+    if (on) {
+      if (kind == 0) {
+        dst = static_cast<char*>(a.qo) + (t * a.ldqo + h0 * a.hqo) * U::kSize;
+        dst_hop = a.hqo;
+      } else {
+        if (kind == 1 && a.ko != nullptr) dst = static_cast<char*>(a.ko) + (t * a.ldko + (int64_t)h0 * a.D) * U::kSize;
+        if (a.kv.k != nullptr) {
+          const int64_t at = cache_offset(a, t);
+          if (at >= 0) page = static_cast<uint16_t*>(kind == 1 ? a.kv.k : a.kv.v) + at + h0 * a.kv.head_stride;
+        }
+      }
+    }
+    float ga[4], gb[4];
+    if constexpr (kNorm) {
+      const float* gain = kind == 0 ? a.gq : a.gk;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        ga[e] = on && kind < 2 ? gain[da + e] : 1.f;
+        gb[e] = on && kind < 2 ? gain[db + e] : 1.f;
+      }
+    }
 #pragma unroll
     for (int u = 0; u < kHeadsPer; ++u) {
-      const int h = h0 + u;
       float f[4], g[4];
       U::widen(xa[u], f);
       U::widen(xb[u], g);
-      const bool turns = h < a.H + a.Hkv;
       if constexpr (kNorm) {
         float ss = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) ss = fmaf(f[e], f[e], fmaf(g[e], g[e], ss));
 #pragma unroll
         for (int o = 1 << kLg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (turns) {
+        if (kind < 2) {
           const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            f[e] *= r * (h < a.H ? gq[e] : gk[e]);
-            g[e] *= r * (h < a.H ? gq[4 + e] : gk[4 + e]);
+            f[e] *= r * ga[e];
+            g[e] *= r * gb[e];
           }
         }
       }
-      if (turns) {
-        if constexpr (kHalf) {
+      if constexpr (kHalf) {
+        if (ra) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x0 = f[e], x1 = g[e];
+            f[e] = x0 * cs[e] - x1 * sn[e];
+            g[e] = x0 * sn[e] + x1 * cs[e];
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
           if (ra) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x0 = f[e], x1 = g[e];
-              f[e] = known ? x0 * cs[e] - x1 * sn[e] : 0.f;
-              g[e] = known ? x0 * sn[e] + x1 * cs[e] : 0.f;
-            }
+            const float x0 = f[2 * k], x1 = f[2 * k + 1];
+            f[2 * k] = x0 * cs[k] - x1 * sn[k];
+            f[2 * k + 1] = x0 * sn[k] + x1 * cs[k];
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (ra) {
-              const float x0 = f[2 * j], x1 = f[2 * j + 1];
-              f[2 * j] = known ? x0 * cs[j] - x1 * sn[j] : 0.f;
-              f[2 * j + 1] = known ? x0 * sn[j] + x1 * cs[j] : 0.f;
-            }
-            if (rb) {
-              const float x0 = g[2 * j], x1 = g[2 * j + 1];
-              g[2 * j] = known ? x0 * cs[2 + j] - x1 * sn[2 + j] : 0.f;
-              g[2 * j + 1] = known ? x0 * sn[2 + j] + x1 * cs[2 + j] : 0.f;
-            }
+          if (rb) {
+            const float x0 = g[2 * k], x1 = g[2 * k + 1];
+            g[2 * k] = x0 * cs[2 + k] - x1 * sn[2 + k];
+            g[2 * k + 1] = x0 * sn[2 + k] + x1 * cs[2 + k];
           }
         }
       }
-      if (!on || h >= a.heads) continue;
-      if (h < a.H) {
-        const int64_t o = (int64_t)t * a.ldqo + h * a.hqo;
-        store4<F32>(a.qo, o + da, f);
-        store4<F32>(a.qo, o + db, g);
-      } else if (h < a.H + a.Hkv) {
-        const int kh = h - a.H;
-        if (a.ko != nullptr) {
-          const int64_t o = (int64_t)t * a.ldko + (int64_t)kh * a.D;
-          store4<F32>(a.ko, o + da, f);
-          store4<F32>(a.ko, o + db, g);
+      if (!known) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (ra) f[e] = 0.f;
+          if (rb) g[e] = 0.f;
         }
-        if (at >= 0) {
-          const int64_t o = at + kh * a.kv.head_stride;
-          store4_bf16(a.kv.k, o + da, f);
-          store4_bf16(a.kv.k, o + db, g);
-        }
-      } else if (at >= 0) {
-        const int64_t o = at + (h - a.H - a.Hkv) * a.kv.head_stride;
-        store4_bf16(a.kv.v, o + da, f);
-        store4_bf16(a.kv.v, o + db, g);
+      }
+      if (u >= n) continue;
+      if (dst != nullptr) {
+        store4<F32>(dst, u * dst_hop + da, f);
+        store4<F32>(dst, u * dst_hop + db, g);
+      }
+      if (page != nullptr) {
+        store4_bf16(page, u * a.kv.head_stride + da, f);
+        store4_bf16(page, u * a.kv.head_stride + db, g);
       }
     }
   }
@@ -432,7 +441,9 @@ bool units_fit(const HeadArgs& a, bool f32, bool halves) {
 
 cudaError_t launch_heads(HeadArgs a, bool f32, bool norm, bool halves, int num_sms, cudaStream_t stream) {
   a.heads = a.H + a.Hkv + (a.v != nullptr ? a.Hkv : 0);
-  a.chunks = (a.heads + kHeadsPer - 1) / kHeadsPer;
+  a.q_chunks = (a.H + kHeadsPer - 1) / kHeadsPer;
+  a.k_chunks = (a.Hkv + kHeadsPer - 1) / kHeadsPer;
+  a.chunks = a.q_chunks + a.k_chunks * (a.v != nullptr ? 2 : 1);
   a.inv_d = 1.f / (float)a.D;
   if (units_fit(a, f32, halves)) {
     if (f32) {
