@@ -23,27 +23,30 @@ namespace {
 // nothing and no 64-bit floating point is needed.  The nearest quarter turn is taken off before the conversion to
 // fp32, so that what is left, at most 1/8 turn, keeps 24 significant bits; there the Taylor polynomials of degree 9 and 8
 // are within 2.5e-8 of the sine and the cosine (the terms left out: x^11 / 11!, x^10 / 10! at pi / 4).
-// Bound by the writes once a pair costs few enough instructions: 1 M positions x 64 took 74 us with sincospi.
+// Bound by the writes once a pair costs few enough instructions: 1 M positions x 64 took 74 us with sincospi and the
+// remainder converted as one 64-bit number.
 struct TableArgs {
   uint64_t turn[128];        // f_i / 2 pi in units of 2^-64 turns
   int64_t pos0, n;
   int half;                  // R / 2
   int rows;                  // rows of a block's pass: as many as its threads cover
-  float amplitude;
+  float sine[5], cosine[5];  // the polynomials' coefficients times the amplitude, lowest first
   float* out;
 };
 
 __device__ __forceinline__ void write_angle(const TableArgs& a, int64_t row, int i, uint64_t phase) {
-  const uint32_t high = (uint32_t)(phase >> 32), quarter = (high + 0x20000000u) >> 30;      // nearest quarter turn
-  const int64_t rest = (int64_t)((uint64_t)(high - (quarter << 30)) << 32 | (uint32_t)phase);
-  const float x = (float)rest * 0x1.921fb6p-62f, z = x * x;                                  // 2 pi / 2^64
-  const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
-  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320.f, -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
-  const bool swap = (quarter & 1u) != 0u;
-  const float cv = swap ? s : c, sv = swap ? c : s;
+  const uint32_t high = (uint32_t)(phase >> 32), quarter = (high + 0x20000000u) & 0xC0000000u;   // nearest quarter turn
+  // what is left, in two words (a 64-bit conversion takes several times as long as two): units of 2 pi / 2^32 and / 2^64
+  const float x = fmaf((float)(int32_t)(high - quarter), 0x1.921fb6p-30f, (float)(uint32_t)phase * 0x1.921fb6p-62f);
+  const float z = x * x;
+  const float s = x * fmaf(z, fmaf(z, fmaf(z, fmaf(z, a.sine[4], a.sine[3]), a.sine[2]), a.sine[1]), a.sine[0]);
+  const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, a.cosine[4], a.cosine[3]), a.cosine[2]), a.cosine[1]), a.cosine[0]);
+  const bool swap = (quarter & 0x40000000u) != 0u;
+  const uint32_t cv = __float_as_uint(swap ? s : c) ^ ((quarter + 0x40000000u) & 0x80000000u);
+  const uint32_t sv = __float_as_uint(swap ? c : s) ^ (quarter & 0x80000000u);
   float* o = a.out + row * (2 * a.half) + i;
-  o[0] = a.amplitude * ((quarter + 1u & 2u) ? -cv : cv);
-  o[a.half] = a.amplitude * ((quarter & 2u) ? -sv : sv);
+  o[0] = __uint_as_float(cv);
+  o[a.half] = __uint_as_float(sv);
 }
 
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs a) {
@@ -85,7 +88,7 @@ struct HeadArgs {
   int chunks, q_chunks, k_chunks;   // vector kernel: groups of kHeadsPer heads of a token, of queries, of keys
 };
 
-constexpr int kHeadsPer = 4;                       // heads a lane group takes at a time, their loads in flight together
+constexpr int kHeadsPer = 8;                       // heads a lane group takes at a time, their loads in flight together
 
 // The pool row of a token, or -1: none (a negative slot) or out of range.
 __device__ __forceinline__ int64_t cache_offset(const HeadArgs& a, int64_t t) {
@@ -240,13 +243,31 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
         }
       }
     }
-    float ga[4], gb[4];
+    // Behind a norm every element is r (x p + partner q): p and q hold the gains and the rotation, and are found once.
+    // (For dims that do not turn, q and what it multiplies are zero.)
+    float pa[4], pb[4], qa[4], qb[4];
     if constexpr (kNorm) {
-      const float* gain = kind == 0 ? a.gq : a.gk;
+      float ga[4] = {1.f, 1.f, 1.f, 1.f}, gb[4] = {1.f, 1.f, 1.f, 1.f};
+      if (on && kind < 2) {
+        const float4 u4 = *reinterpret_cast<const float4*>((kind == 0 ? a.gq : a.gk) + da);
+        const float4 v4 = *reinterpret_cast<const float4*>((kind == 0 ? a.gq : a.gk) + db);
+        ga[0] = u4.x, ga[1] = u4.y, ga[2] = u4.z, ga[3] = u4.w;
+        gb[0] = v4.x, gb[1] = v4.y, gb[2] = v4.z, gb[3] = v4.w;
+      }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        ga[e] = on && kind < 2 ? gain[da + e] : 1.f;
-        gb[e] = on && kind < 2 ? gain[db + e] : 1.f;
+        const int other = kHalf ? e : e ^ 1;
+        const float c0 = kHalf ? cs[e] : cs[e >> 1], s0 = kHalf ? sn[e] : sn[e >> 1];
+        const float c1 = kHalf ? cs[e] : cs[2 + (e >> 1)], s1 = kHalf ? sn[e] : sn[2 + (e >> 1)];
+        pa[e] = ga[e] * c0;
+        pb[e] = gb[e] * c1;
+        if constexpr (kHalf) {
+          qa[e] = -gb[other] * s0;
+          qb[e] = ga[other] * s1;
+        } else {
+          qa[e] = (e & 1 ? ga[other] : -ga[other]) * s0;
+          qb[e] = (e & 1 ? gb[other] : -gb[other]) * s1;
+        }
       }
     }
 #pragma unroll
@@ -262,14 +283,19 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
         for (int o = 1 << kLg >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         if (kind < 2) {
           const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+          float x[4], y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            f[e] *= r * ga[e];
-            g[e] *= r * gb[e];
+            x[e] = ra ? f[e] : 0.f;
+            y[e] = rb ? g[e] : 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = r * fmaf(kHalf ? y[e] : x[e ^ 1], qa[e], f[e] * pa[e]);
+            g[e] = r * fmaf(kHalf ? x[e] : y[e ^ 1], qb[e], g[e] * pb[e]);
           }
         }
-      }
-      if constexpr (kHalf) {
+      } else if constexpr (kHalf) {
         if (ra) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -293,7 +319,7 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
           }
         }
       }
-      if (!known) {
+      if (!known) {                                // zeros, whatever the head holds
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (ra) f[e] = 0.f;
@@ -430,7 +456,9 @@ bool units_fit(const HeadArgs& a, bool f32, bool halves) {
   const uintptr_t al = f32 ? 16 : 8;
   const auto ok = [&](const void* p, int64_t ld) { return p == nullptr || (reinterpret_cast<uintptr_t>(p) % al == 0 && ld % 4 == 0); };
   if (a.D % 8 != 0 || a.off % 4 != 0 || a.R % (halves ? 8 : 4) != 0) return false;
-  if (reinterpret_cast<uintptr_t>(a.cos_sin) % 16 != 0) return false;
+  if (reinterpret_cast<uintptr_t>(a.cos_sin) % 16 != 0 || reinterpret_cast<uintptr_t>(a.gq) % 16 != 0 ||
+      reinterpret_cast<uintptr_t>(a.gk) % 16 != 0)
+    return false;
   if (a.H > 0 && (!ok(a.q, a.ldq) || !ok(a.qo, a.ldqo) || a.hq % 4 != 0 || a.hqo % 4 != 0)) return false;
   if (a.Hkv > 0 && (!ok(a.k, a.ldk) || !ok(a.ko, a.ldko) || !ok(a.v, a.ldv))) return false;
   if (a.kv.k != nullptr && (reinterpret_cast<uintptr_t>(a.kv.k) % 8 != 0 || reinterpret_cast<uintptr_t>(a.kv.v) % 8 != 0 ||
@@ -489,7 +517,11 @@ cudaError_t launch_rope_table(const dsa_rope_params& p, int R, int64_t pos0, int
     a.turn[i] = (uint64_t)f;                                  // base > 1: less than a turn
   }
   a.pos0 = pos0, a.n = n, a.half = R / 2, a.out = out;
-  a.amplitude = (float)p.amplitude;
+  double odd = p.amplitude, even = p.amplitude;
+  for (int k = 0; k < 5; odd /= -(2.0 * k + 2.0) * (2.0 * k + 3.0), even /= -(2.0 * k + 1.0) * (2.0 * k + 2.0), ++k) {
+    a.sine[k] = (float)odd;                                   // (-1)^k / (2k + 1)!
+    a.cosine[k] = (float)even;                                // (-1)^k / (2k)!
+  }
   a.rows = 256 / a.half;
   const int64_t blocks = (n + a.rows - 1) / a.rows, most = (int64_t)num_sms * 8;
   return launch_pdl(rope_table_kernel, (unsigned)(blocks < most ? blocks : most), 256u, stream, a);

@@ -445,7 +445,7 @@ dsa_status dsa_rope_table(dsa_rope_params params, int rope_dim, int64_t pos0, in
  * |hy| >= D where H > 1, token strides any.  Any
  * element-aligned pointers and strides work; heads move in units of four elements where D is a
  * multiple of 8, rope_off of 4, rope_dim of 4 (HALF: 8), the strides of 4, and pointers are
- * aligned to four elements (the table to 16 bytes).
+ * aligned to four elements (the table and gains to 16 bytes).
  * fp32 arithmetic, one rounding to `type` at the end.
  */
 dsa_status dsa_rope(const void* x, int64_t ldx, int64_t hx, const int32_t* positions, const float* cos_sin,

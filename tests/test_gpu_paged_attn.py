@@ -428,3 +428,25 @@ def test_a_layer_step():
                 assert float((got - o).abs().max()) <= 0.5
             at += new[b]
         cached = [a + b for a, b in zip(cached, new)]
+
+
+def test_many_calls_in_a_row():
+    # calls one behind the other, whose CTAs start as soon as the last ones' leave, with pieces of few tiles, all rows of
+    # a tile in use, and windows: nothing waits for what has already passed, and nothing changes
+    cases = [Case([2] * 32, [4096 * (b + 1) for b in range(32)], 64, 1, 128, bs=64, window=4096, sink=True, seed=1),
+             Case([1] * 40, [100 + 37 * b for b in range(40)], 64, 1, 64, bs=16, seed=2),
+             Case([130, 7, 64], [300, 70, 640], 6, 2, 128, bs=20, seed=3)]
+    for c in cases:
+        c.check()
+        out, lse = c.out.clone(), c.lse.clone()
+        for _ in range(100):
+            c.run()
+        assert dsa.dsa_device_error() == 0
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+
+
+def test_gathered_pages_of_any_size():
+    # page sizes that no copy of several rows fits: 1, 3, 12 and 100 rows; heads side by side, apart, and within a row
+    for i, bs in enumerate((1, 3, 12, 100)):
+        for D in (64, 128):
+            Case([3, 150], [500, 400], 8, 2, D, bs=bs, seed=i, head_major=bool(i % 2), window=0 if i < 2 else 170).check()
