@@ -48,7 +48,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;                // base-2 headroom before the running maximum moves
 constexpr int kPlanMax = 512;                // row blocks (and sequences) that a CTA plans by itself
-constexpr int kItemCost = 2;                 // an item's fixed cost, in key tiles
+constexpr int kItemCost = 3;                 // an item's fixed cost, in key tiles (8192-token prompt: 2 840, 3 744, 4 751, 6 769 us)
 
 struct AttnArgs {
   const uint16_t* q;
@@ -76,7 +76,7 @@ struct AttnArgs {
   int64_t ldo;
   float* lse;                  // nullable
   // workspace
-  int32_t* meta;               // [CTAs][8]
+  int32_t* meta;               // [1 + CTAs][12]
   float* ml;                   // [2 * CTAs][rows][2]
   float* part;                 // [2 * CTAs][rows][D]
   int64_t* prefix;             // the plan, where it is not made in shared memory
@@ -140,21 +140,22 @@ __device__ __forceinline__ Item make_item(const AttnArgs& a, const Seq& q, int b
 }
 
 // Exclusive prefix sum over the NT threads of the block; returns the sum of the threads before, `total` of all.
-template <int NT>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_s, int64_t& total) {
+template <int NT, typename V>
+__device__ __forceinline__ V block_scan(V v, int64_t* scratch, V& total) {
+  V* warp_s = reinterpret_cast<V*>(scratch);
   const int lane = (int)threadIdx.x & 31, w = (int)threadIdx.x >> 5;
-  int64_t incl = v;
+  V incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    const V y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
     if (lane >= o) incl += y;
   }
   if (lane == 31) warp_s[w] = incl;
   __syncthreads();
-  int64_t before = 0, all = 0;
+  V before = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < NT / 32; ++i) {
-    const int64_t c = warp_s[i];
+    const V c = warp_s[i];
     if (i < w) before += c;
     all += c;
   }
@@ -167,25 +168,28 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_s, int64_
 // of the row blocks before it, each kItemCost and its key tiles (at least one, so that a block that sees nothing still
 // has its turn).  A row block has an item per key head; these lie side by side on the line, whose length is
 // prefix[count] * Hkv.
-template <int kRows, int NT>
-__device__ int make_plan(const AttnArgs& a, int64_t* prefix, int32_t* first, int32_t* seq, int64_t* warp_s, bool tell) {
-  int64_t carry = 0, total;
+// V is wide enough for the line: 32 bits where a CTA plans (at most kPlanMax row blocks of at most 2^22 key tiles).
+template <int kRows, int NT, typename V>
+__device__ int make_plan(const AttnArgs& a, V* prefix, int32_t* first, int32_t* seq, int64_t* scratch, bool tell) {
+  int64_t many = 0;
   bool bad = false;
   for (int b0 = 0; b0 < a.B; b0 += NT) {
     const int b = b0 + (int)threadIdx.x;
     int64_t c = 0;
     if (b < a.B) c = ((int64_t)sequence(a, b, bad).n * a.G + kRows - 1) / kRows;
-    const int64_t before = block_scan<NT>(c, warp_s, total);
-    if (b < a.B) first[b] = (int32_t)min(carry + before, (int64_t)INT32_MAX);
-    carry += total;
+    // (more than there can be counts as one more: then the sequences overlap)
+    V total;
+    const V before = block_scan<NT, V>((V)min(c, (int64_t)a.limit + 1), scratch, total);
+    if (b < a.B) first[b] = (int32_t)min(many + (int64_t)before, (int64_t)INT32_MAX);
+    many = min(many + (int64_t)total, (int64_t)1 << 40);
   }
   __syncthreads();
-  const int count = (int)min(carry, (int64_t)a.limit);
-  if (carry > a.limit) bad = true;
-  carry = 0;
+  const int count = (int)min(many, (int64_t)a.limit);
+  if (many > a.limit) bad = true;
+  V carry = 0;
   for (int e0 = 0; e0 < count; e0 += NT) {
     const int e = e0 + (int)threadIdx.x;
-    int64_t c = 0;
+    V c = 0;
     if (e < count) {
       int lo = 0, hi = a.B;                        // the last sequence with first[b] <= e
       while (hi - lo > 1) {
@@ -196,10 +200,11 @@ __device__ int make_plan(const AttnArgs& a, int64_t* prefix, int32_t* first, int
       seq[e] = lo;
       const Seq q = sequence(a, lo, bad);
       const Item it = make_item<kRows>(a, q, lo, e - first[lo]);
-      c = kItemCost + max(it.tiles, 1);
+      c = (V)(kItemCost + max(it.tiles, 1));
       if (it.L > a.cap) bad = true;                // keys past the block table's row
     }
-    const int64_t before = block_scan<NT>(c, warp_s, total);
+    V total;
+    const V before = block_scan<NT, V>(c, scratch, total);
     if (e < count) prefix[e] = carry + before;
     carry += total;
   }
@@ -214,24 +219,30 @@ __global__ void __launch_bounds__(1024) plan_kernel(const AttnArgs a) {
   __shared__ int64_t warp_s[32];
   grid_launch_dependents();
   grid_dependency_wait();
-  const int count = make_plan<kRows, 1024>(a, a.prefix, a.first, a.seq, warp_s, true);
+  const int count = make_plan<kRows, 1024, int64_t>(a, a.prefix, a.first, a.seq, warp_s, true);
   if (threadIdx.x == 0) a.meta[7] = count;
 }
 
 // One CTA's pieces of the line, in order.
 struct Pieces {
-  const int64_t* prefix;
-  const int32_t* first;
-  const int32_t* seq;
-  int Hkv, e;
+  const uint32_t* plan_s;      // the CTA's own plan: prefix, first, seq (kPlanMax + 8, kPlanMax, kPlanMax)
+  int e;
   int64_t x, end;
 
-  __device__ __forceinline__ void begin(int count, int64_t from, int64_t to) {
+  __device__ __forceinline__ int64_t prefix(const AttnArgs& a, int i) const { return a.planned ? a.prefix[i] : (int64_t)plan_s[i]; }
+  __device__ __forceinline__ int first(const AttnArgs& a, int b) const {
+    return a.planned ? a.first[b] : (int)plan_s[kPlanMax + 8 + b];
+  }
+  __device__ __forceinline__ int seq(const AttnArgs& a, int i) const {
+    return a.planned ? a.seq[i] : (int)plan_s[2 * kPlanMax + 8 + i];
+  }
+
+  __device__ __forceinline__ void begin(const AttnArgs& a, int count, int64_t from, int64_t to) {
     x = from, end = to;
     int lo = 0, hi = count;
     while (hi - lo > 1) {                          // the row block that holds x
       const int mid = (lo + hi) >> 1;
-      if (prefix[mid] * Hkv <= x) lo = mid;
+      if (prefix(a, mid) * a.Hkv <= x) lo = mid;
       else hi = mid;
     }
     e = lo;
@@ -242,16 +253,15 @@ struct Piece {
   Item it;
   int hk;                      // key head
   int t0, len, cost;           // key tiles t0 .. t0 + len - 1 of the item's `cost`
-  int64_t end;                 // where the item ends on the line
   int block = -1;              // the row block that `it` describes (that of several key heads in a row)
 };
 
 template <int kRows>
 __device__ __forceinline__ bool next_piece(const AttnArgs& a, Pieces& ps, Piece& p) {
   while (ps.x < ps.end) {
-    const int64_t base = ps.prefix[ps.e];
-    const int length = (int)(ps.prefix[ps.e + 1] - base);
-    const uint32_t rem = (uint32_t)(ps.x - base * ps.Hkv);
+    const int64_t base = ps.prefix(a, ps.e);
+    const int length = (int)(ps.prefix(a, ps.e + 1) - base);
+    const uint32_t rem = (uint32_t)(ps.x - base * a.Hkv);
     p.hk = (int)(rem / (uint32_t)length);
     const int from = (int)(rem % (uint32_t)length), to = (int)min((int64_t)length, from + (ps.end - ps.x));
     p.cost = length - kItemCost;
@@ -259,13 +269,12 @@ __device__ __forceinline__ bool next_piece(const AttnArgs& a, Pieces& ps, Piece&
     p.len = max(to - kItemCost, 0) - p.t0;
     const int e = ps.e;
     ps.x += to - from;
-    p.end = ps.x + (length - to);
-    if (p.hk == ps.Hkv - 1 && to == length) ++ps.e;
+    if (p.hk == a.Hkv - 1 && to == length) ++ps.e;
     if (p.len == 0) continue;                      // the slice ends within the item's fixed cost
     if (e != p.block) {
-      const int b = ps.seq[e];
+      const int b = ps.seq(a, e);
       bool bad = false;
-      p.it = make_item<kRows>(a, sequence(a, b, bad), b, e - ps.first[b]);
+      p.it = make_item<kRows>(a, sequence(a, b, bad), b, e - ps.first(a, b));
       p.block = e;
     }
     return true;
@@ -415,7 +424,7 @@ struct Shape {
   static constexpr int kStages = (D == 128 ? 4 : 8) + (kTiles == 1 ? 1 : 0) - (D == 64 ? 1 : 0);
   static constexpr uint32_t kStageOff = kTiles * kTile;
   static constexpr uint32_t kPlanOff = kStageOff + kStages * kTile;          // prefix, first, seq
-  static constexpr uint32_t kMaskOff = kPlanOff + 8 * (kPlanMax + 8) + 4 * kPlanMax * 2;  // keys that exist [8][4] words
+  static constexpr uint32_t kMaskOff = kPlanOff + 4 * (kPlanMax + 8) + 4 * kPlanMax * 2;  // keys that exist [8][4] words
   static constexpr uint32_t kBadOff = kMaskOff + 8 * 16;            // values that are no numbers, per piece [16]
   static constexpr uint32_t kOutOff = kBadOff + 64;                 // results on their way out, 2 KB per softmax warp
   static constexpr uint32_t kStatOff = kOutOff + 8 * 2048;              // (m, l) [stream][128]
@@ -436,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t sm32 = smem_u32(sm);
-  int64_t* prefix_s = reinterpret_cast<int64_t*>(sm + Sh::kPlanOff);
+  uint32_t* prefix_s = reinterpret_cast<uint32_t*>(sm + Sh::kPlanOff);
   int32_t* first_s = reinterpret_cast<int32_t*>(prefix_s + kPlanMax + 8);
   int32_t* seq_s = first_s + kPlanMax;
   uint32_t* mask_s = reinterpret_cast<uint32_t*>(sm + Sh::kMaskOff);
@@ -485,19 +494,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
   // the plan, and this CTA's slice of the line
   Pieces ps;
-  ps.Hkv = a.Hkv;
+  ps.plan_s = prefix_s;
   int count;
   if (a.planned) {
-    ps.prefix = a.prefix, ps.first = a.first, ps.seq = a.seq;
     count = *reinterpret_cast<volatile int32_t*>(a.meta + 7);
   } else {
-    count = make_plan<kRows, kThreads>(a, prefix_s, first_s, seq_s, reinterpret_cast<int64_t*>(sm + Sh::kScanOff), blockIdx.x == 0);
-    ps.prefix = prefix_s, ps.first = first_s, ps.seq = seq_s;
+    count = make_plan<kRows, kThreads, uint32_t>(a, prefix_s, first_s, seq_s, reinterpret_cast<int64_t*>(sm + Sh::kScanOff), blockIdx.x == 0);
   }
-  const int64_t C = gridDim.x, c = blockIdx.x;
-  const int64_t line = count > 0 ? ps.prefix[count] * a.Hkv : 0;
-  if (line < (1 << 22)) ps.begin(count, (uint32_t)line * (uint32_t)c / (uint32_t)C, (uint32_t)line * (uint32_t)(c + 1) / (uint32_t)C);
-  else ps.begin(count, line * c / C, line * (c + 1) / C);      // (a 64-bit division takes several times as long)
+  const int64_t C = gridDim.x;
+  const int c = (int)blockIdx.x;
+  const int64_t line = count > 0 ? ps.prefix(a, count) * a.Hkv : 0;
+  if (line < (1 << 22)) ps.begin(a, count, (uint32_t)line * (uint32_t)c / (uint32_t)C, (uint32_t)line * (uint32_t)(c + 1) / (uint32_t)C);
+  else ps.begin(a, count, line * c / C, line * (c + 1) / C);      // (a 64-bit division takes several times as long)
 
   if (warp < 8) {
     // ================================ softmax ================================
@@ -510,11 +518,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
     uint32_t tiles_before = 0;                     // key tiles of the pieces before
     uint32_t np = 0;                               // pieces so far that see any key
     bool ok = true;
-    int32_t* my_meta = a.meta + 8 * (c + 1);
-    if (threadIdx.x == 0) {
-      my_meta[0] = 0;
-      my_meta[6] = ps.end > ps.x;                  // whether it has any of the line
-    }
+    int32_t* my_meta = a.meta + 12 * (c + 1);
+    if (threadIdx.x == 0) my_meta[0] = 0;
     const uint64_t scale2 = pack2(a.scale_log2, a.scale_log2);
     uint8_t* stage = sm + Sh::kOutOff + 2048 * warp;   // 64 bytes of 32 rows
     int block = -1, token = 0, group = 0, lo = 0, hi = 0;      // of the row, while the row block is the same
@@ -543,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       float m = -INFINITY, l = 0.f;
       for (int i = 0; ok && i < mine; ++i, ++jobs) {
         const int j = j0 + step * i, tile = it.tile0 + p.t0 + j;
-#pragma unroll
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {              // half a tile: 64 keys, buffer h
           ok = ok && stream_wait(kSFull + 2 * t + h, jobs);
           if (!ok) break;
@@ -624,10 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       }
       // ---- the item's rows (or its part of them)
       const bool whole = p.t0 == 0 && p.len == p.cost;
-      const int slot = p.t0 == 0 ? 2 * (int)c + 1 : 2 * (int)c;
+      const int slot = p.t0 == 0 ? 2 * c + 1 : 2 * c;
       if (!whole && p.t0 == 0 && threadIdx.x == 0) {               // the item's first part: it owns the sum
-        my_meta[1] = it.b, my_meta[2] = it.row0, my_meta[3] = it.rows, my_meta[4] = p.hk;
-        my_meta[5] = (int)((p.end * C - 1) / line);                // the CTA that holds its last tile
+        my_meta[1] = it.s, my_meta[2] = it.row0, my_meta[3] = it.rows, my_meta[4] = p.hk;
+        my_meta[5] = (int)(((ps.x + (p.cost - p.t0 - p.len)) * C - 1) / line);                // the CTA that holds its last tile
+        my_meta[8] = (int32_t)(uint32_t)line, my_meta[9] = (int32_t)(line >> 32);
         my_meta[0] = 1;
       }
       if (ok && mine > 0) ok = stream_wait(kODone + 2 * t + 1, jobs - 1u);
@@ -1096,63 +1102,79 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   grid_launch_dependents();
   grid_dependency_wait();
   const int c = (int)blockIdx.x, lane = (int)threadIdx.x & 31;
-  const int4* meta = reinterpret_cast<const int4*>(a.meta) + 2 * (c + 1);
-  const int4 m0 = meta[0], m1 = meta[1];           // split, sequence, first row, rows; key head, last CTA
+  const int4* meta = reinterpret_cast<const int4*>(a.meta) + 3 * (c + 1);
+  const int4 m0 = meta[0], m1 = meta[1], m2 = meta[2];       // split, first token's row, first row, rows; key head, last CTA; line
   if (m0.x == 0) return;
   const int hk = m1.x, parts = m1.y - c + 1;
-  const int s0 = a.start[m0.y];
+  const int64_t line = (int64_t)(uint32_t)m2.x | (int64_t)m2.y << 32, C = gridDim.x;
   const float2* ml = reinterpret_cast<const float2*>(a.ml);
-  // part i is in the owner's second slot or CTA c + i's first; a CTA without tiles (more CTAs than tiles) has none
+  // Part i is in the owner's second slot or CTA c + i's first; a CTA without any of the line (more CTAs than tiles) has none.
   auto slot_of = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
+  auto is_part = [&](int i) { return i < parts && (i == 0 || line >= C || line * (c + i) / C < line * (c + i + 1) / C); };
+  constexpr int kE = D / 32, kAhead = 8;
   for (int row = (int)(blockIdx.y * 8 + (threadIdx.x >> 5)); row < m0.w; row += (int)gridDim.y * 8) {
     const int token = (m0.z + row) / a.G, head = hk * a.G + (m0.z + row) % a.G;
     const float sn = a.sink != nullptr ? a.sink[head] : -INFINITY, sk = sn * kLog2e;
-    float acc[D / 32], M = sk, den = 0.f;
+    float acc[kE], M = sk, den = 0.f;
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) acc[e] = 0.f;
+    for (int e = 0; e < kE; ++e) acc[e] = 0.f;
     // 32 parts at a time, their statistics a lane each; the sums so far move with the maximum
     for (int i0 = 0; i0 < parts; i0 += 32) {
-      const int i = i0 + lane;
-      const bool there = i < parts && (i == 0 || a.meta[8 * (c + i + 1) + 6] != 0);
-      const float2 s = there ? ml[(int64_t)slot_of(i) * kRows + row] : make_float2(-INFINITY, 0.f);
-      float top = s.x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      top = fmaxf(top, M);
-      const float old = top == M ? 1.f : ex2(M - top);
-      M = top;
-      const float w = M == -INFINITY ? 1.f : ex2(s.x - M);
-      float part = there ? s.y * w : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, o);
-      den = den * old + part;
-#pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] *= old;
+      const bool there = is_part(i0 + lane);
       const uint32_t have = __ballot_sync(0xFFFFFFFFu, there);
+      const float2 s = there ? ml[(int64_t)slot_of(i0 + lane) * kRows + row] : make_float2(-INFINITY, 0.f);
       const int n = min(32, parts - i0);
-#pragma unroll 8
-      for (int k = 0; k < n; ++k) {
-        const float f = __shfl_sync(0xFFFFFFFFu, w, k);
-        if (!(have >> k & 1u)) continue;
-        const float* o = a.part + ((int64_t)slot_of(i0 + k) * kRows + row) * D + lane * (D / 32);
+      float w = 1.f;
+      for (int k0 = 0; k0 < n; k0 += kAhead) {
+        float o[kAhead][kE];                       // on their way while the weights are found
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(o[e], f, acc[e]);
+        for (int k = 0; k < kAhead; ++k) {
+          const bool on = k0 + k < n && (have >> (k0 + k) & 1u);
+          const float* from = a.part + ((int64_t)slot_of(on ? i0 + k0 + k : 0) * kRows + row) * D + lane * kE;
+          if constexpr (kE == 4) {
+            const float4 v = on ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[k][0] = v.x, o[k][1] = v.y, o[k][2] = v.z, o[k][3] = v.w;
+          } else {
+            const float2 v = on ? *reinterpret_cast<const float2*>(from) : make_float2(0.f, 0.f);
+            o[k][0] = v.x, o[k][1] = v.y;
+          }
+        }
+        if (k0 == 0) {
+          float top = s.x;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          top = fmaxf(top, M);
+          const float old = top == M ? 1.f : ex2(M - top);
+          M = top;
+          w = !there ? 0.f : M == -INFINITY ? 1.f : ex2(s.x - M);
+          float part = there ? s.y * w : 0.f;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) part += __shfl_xor_sync(0xFFFFFFFFu, part, d);
+          den = den * old + part;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) acc[e] *= old;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          const float f = __shfl_sync(0xFFFFFFFFu, w, (k0 + k) & 31);
+#pragma unroll
+          for (int e = 0; e < kE; ++e) acc[e] = fmaf(o[k][e], k0 + k < n ? f : 0.f, acc[e]);
+        }
       }
     }
     const bool none = M == -INFINITY && !(den != den);
     den += M == -INFINITY ? 0.f : ex2(sk - M);
     const float inv = none ? 0.f : 1.f / den;
-    uint16_t* dst = a.out + (int64_t)(s0 + token) * a.ldo + (int64_t)head * D + lane * (D / 32);
+    uint16_t* dst = a.out + (int64_t)(m0.y + token) * a.ldo + (int64_t)head * D + lane * kE;
 #pragma unroll
-    for (int e = 0; e < D / 32; e += 2)
+    for (int e = 0; e < kE; e += 2)
       *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-    if (a.lse != nullptr && lane == 0) a.lse[(int64_t)(s0 + token) * a.H + head] = none ? -INFINITY : (sk >= M ? sn : M * kLn2) + logf(den);
+    if (a.lse != nullptr && lane == 0) a.lse[(int64_t)(m0.y + token) * a.H + head] = none ? -INFINITY : (sk >= M ? sn : M * kLn2) + logf(den);
   }
 }
 
 struct Layout {
   int tiles, rows, ctas;
-  bool planned;
   int64_t blocks;
   size_t meta, ml, part, prefix, first, seq, total;
 };
@@ -1166,15 +1188,14 @@ Layout layout(int64_t T, int B, int H, int Hkv, int D, int num_sms) {
   y.ctas = num_sms;
   const int64_t blocks = T * G / y.rows + (B < T ? B : T);        // at most so many row blocks
   y.blocks = blocks;
-  y.planned = blocks > kPlanMax || B > kPlanMax;
   const auto up = [](size_t n) { return (n + 255) & ~(size_t)255; };
   y.meta = 0;
-  y.ml = up(32 * (size_t)(y.ctas + 1));
+  y.ml = up(48 * (size_t)(y.ctas + 1));
   y.part = y.ml + up((size_t)2 * y.ctas * y.rows * 8);
   y.prefix = y.part + up((size_t)2 * y.ctas * y.rows * D * 4);
-  y.first = y.prefix + (y.planned ? up(8 * (size_t)(blocks + 1)) : 0);
-  y.seq = y.first + (y.planned ? up(4 * (size_t)B) : 0);
-  y.total = y.seq + (y.planned ? up(4 * (size_t)blocks) : 0);
+  y.first = y.prefix + up(8 * (size_t)(blocks + 1));
+  y.seq = y.first + up(4 * (size_t)B);
+  y.total = y.seq + up(4 * (size_t)blocks);
   return y;
 }
 
@@ -1284,7 +1305,8 @@ cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, 
   a.prefix = reinterpret_cast<int64_t*>(w + y.prefix);
   a.first = reinterpret_cast<int32_t*>(w + y.first);
   a.seq = reinterpret_cast<int32_t*>(w + y.seq);
-  a.planned = y.planned;
+  // a CTA plans by itself what fits its shared memory and 32-bit sums
+  a.planned = y.blocks > kPlanMax || B > kPlanMax || a.cap > 1 << 29;
   a.limit = (int)y.blocks;
   // the pool as one tensor of rows row_stride apart (paged_attn_cache_fits)
   const bool in_row = Hkv == 1 || kv.head_stride < kv.row_stride;

@@ -88,7 +88,7 @@ struct HeadArgs {
   int chunks, q_chunks, k_chunks;   // vector kernel: groups of kHeadsPer heads of a token, of queries, of keys
 };
 
-constexpr int kHeadsPer = 8;                       // heads a lane group takes at a time, their loads in flight together
+constexpr int kHeadsPer = 4;                       // heads a lane group takes at a time, their loads in flight together
 
 // The pool row of a token, or -1: none (a negative slot) or out of range.
 __device__ __forceinline__ int64_t cache_offset(const HeadArgs& a, int64_t t) {
