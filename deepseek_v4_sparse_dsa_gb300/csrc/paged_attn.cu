@@ -261,9 +261,10 @@ __device__ __forceinline__ bool next_piece(const AttnArgs& a, Pieces& ps, Piece&
   while (ps.x < ps.end) {
     const int64_t base = ps.prefix(a, ps.e);
     const int length = (int)(ps.prefix(a, ps.e + 1) - base);
-    const uint32_t rem = (uint32_t)(ps.x - base * a.Hkv);
-    p.hk = (int)(rem / (uint32_t)length);
-    const int from = (int)(rem % (uint32_t)length), to = (int)min((int64_t)length, from + (ps.end - ps.x));
+    const int64_t rem = ps.x - base * a.Hkv;
+    if (a.Hkv <= 128) p.hk = (int)((uint32_t)rem / (uint32_t)length);      // length <= 2^24 + kItemCost
+    else p.hk = (int)(rem / length);
+    const int from = (int)(rem - (int64_t)p.hk * length), to = (int)min((int64_t)length, from + (ps.end - ps.x));
     p.cost = length - kItemCost;
     p.t0 = max(from - kItemCost, 0);
     p.len = max(to - kItemCost, 0) - p.t0;
@@ -869,8 +870,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
       *abort_flag = 1;
     }
     // every copy issued has landed before the CTA may leave
+    // (where others have given up, a stage may never fill; after one such wait all have landed)
     for (uint32_t i = loads > (uint32_t)kStages ? loads - kStages : 0; i < loads; ++i)
-      mbar_wait(bar(kFull + (int)(i % kStages)), i / kStages & 1u, kCleanupWaitNs, nullptr);
+      if (!mbar_wait(bar(kFull + (int)(i % kStages)), i / kStages & 1u, kCleanupWaitNs, nullptr)) break;
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp < 14) {

@@ -518,6 +518,7 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  * Flagged with DSA_DEVERR_INDEX, never accessed out of range: a block id outside [0,
  * num_blocks) or a page at or past bt_stride (its keys are seen by no row); a negative length
  * (0); rows of a sequence outside [0, T) (left out); overlapping sequences (rows are lost).
+ * A device-side wait that expires sets DSA_DEVERR_TIMEOUT.
  */
 size_t dsa_paged_attn_workspace_bytes(int64_t T, int B, int H, int Hkv, int D);
 dsa_status dsa_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* query_start,

@@ -450,3 +450,28 @@ def test_gathered_pages_of_any_size():
     for i, bs in enumerate((1, 3, 12, 100)):
         for D in (64, 128):
             Case([3, 150], [500, 400], 8, 2, D, bs=bs, seed=i, head_major=bool(i % 2), window=0 if i < 2 else 170).check()
+
+
+@pytest.mark.parametrize("case", [dict(new=[1, 1, 3], lens=[9000, 100, 3000], H=8, Hkv=2, D=128, bs=64),
+                                  dict(new=[1] * 12, lens=[50000] * 12, H=16, Hkv=4, D=128, bs=64),
+                                  dict(new=[300, 40], lens=[800, 700], H=8, Hkv=1, D=64, bs=16),
+                                  dict(new=[300, 40], lens=[800, 700], H=6, Hkv=2, D=128, bs=20, window=100)])
+def test_expired_waits_are_told_and_leave_the_context_usable(case):
+    c = Case(**case).check()
+    right, told = c.out.clone(), 0
+    for limit in (1, 1000, 5000, 1):
+        dsa.dsa_set_wait_limit_ns(limit)
+        try:
+            for _ in range(2):
+                c.run()                                      # the sums of parts then read whatever is there
+            err = dsa.dsa_device_error()
+        finally:
+            dsa.dsa_set_wait_limit_ns(0)
+        # (the clock ticks less often than some waits last: a call all of whose waits were short is a right one)
+        assert err in (0, dsa.DSA_DEVERR_TIMEOUT) and (err or torch.equal(c.out, right))
+        told |= err
+    assert told or sum(case["lens"]) < 100000                # work of many microseconds does not pass unnoticed
+    c.out.fill_(-7)
+    c.lse.fill_(-7)
+    c.ws.fill_(255)
+    c.check()
