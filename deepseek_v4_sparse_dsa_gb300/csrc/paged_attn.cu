@@ -559,13 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             tmem_load(tS + 64u * (uint32_t)h, x);
             // which of the keys the row sees
             const uint2 have = *reinterpret_cast<const uint2*>(mask_s + 4 * ((tiles_before + (uint32_t)j) & 7u) + 2 * h);
-            uint32_t see0 = have.x, see1 = have.y;
-            if (!all.has(tile)) {
+            if (!all.has(tile) || (have.x & have.y) != ~0u) {      // (the same for every lane)
               const int k0 = tile * kKeys + 64 * h;
-              see0 &= bits_between(lo - k0, hi - k0);
-              see1 &= bits_between(lo - k0 - 32, hi - k0 - 32);
-            }
-            if (__any_sync(0xFFFFFFFFu, (see0 & see1) != ~0u)) {
+              const uint32_t see0 = have.x & bits_between(lo - k0, hi - k0), see1 = have.y & bits_between(lo - k0 - 32, hi - k0 - 32);
 #pragma unroll
               for (int e = 0; e < 32; ++e) {
                 x[e] = (see0 >> e) & 1u ? x[e] : __float_as_uint(-INFINITY);
