@@ -1105,14 +1105,18 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
   if (m0.x == 0) return;
   const int hk = m1.x, parts = m1.y - c + 1;
   const int64_t line = (int64_t)(uint32_t)m2.x | (int64_t)m2.y << 32, C = gridDim.x;
-  const float2* ml = reinterpret_cast<const float2*>(a.ml);
   // Part i is in the owner's second slot or CTA c + i's first; a CTA without any of the line (more CTAs than tiles) has none.
-  auto slot_of = [&](int i) { return i == 0 ? 2 * c + 1 : 2 * (c + i); };
-  auto is_part = [&](int i) { return i < parts && (i == 0 || line >= C || line * (c + i) / C < line * (c + i + 1) / C); };
-  constexpr int kE = D / 32, kAhead = 8;
+  const auto slot = [](int i) { return i == 0 ? 1 : 2 * i; };        // from the owner's first
+  const bool dense = line >= C;
+  const auto is_part = [&](int i) {
+    return i < parts && (i == 0 || dense || line * (c + i) / C < line * (c + i + 1) / C);
+  };
+  constexpr int kE = D / 32, kAhead = 4;
   for (int row = (int)(blockIdx.y * 8 + (threadIdx.x >> 5)); row < m0.w; row += (int)gridDim.y * 8) {
     const int token = (m0.z + row) / a.G, head = hk * a.G + (m0.z + row) % a.G;
     const float sn = a.sink != nullptr ? a.sink[head] : -INFINITY, sk = sn * kLog2e;
+    const float2* ml = reinterpret_cast<const float2*>(a.ml) + (int64_t)2 * c * kRows + row;
+    const float* sums = a.part + ((int64_t)2 * c * kRows + row) * D + lane * kE;
     float acc[kE], M = sk, den = 0.f;
 #pragma unroll
     for (int e = 0; e < kE; ++e) acc[e] = 0.f;
@@ -1120,21 +1124,24 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
     for (int i0 = 0; i0 < parts; i0 += 32) {
       const bool there = is_part(i0 + lane);
       const uint32_t have = __ballot_sync(0xFFFFFFFFu, there);
-      const float2 s = there ? ml[(int64_t)slot_of(i0 + lane) * kRows + row] : make_float2(-INFINITY, 0.f);
+      const float2 s = there ? ml[slot(i0 + lane) * kRows] : make_float2(-INFINITY, 0.f);
       const int n = min(32, parts - i0);
       float w = 1.f;
       for (int k0 = 0; k0 < n; k0 += kAhead) {
         float o[kAhead][kE];                       // on their way while the weights are found
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
-          const bool on = k0 + k < n && (have >> (k0 + k) & 1u);
-          const float* from = a.part + ((int64_t)slot_of(on ? i0 + k0 + k : 0) * kRows + row) * D + lane * kE;
-          if constexpr (kE == 4) {
-            const float4 v = on ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
-            o[k][0] = v.x, o[k][1] = v.y, o[k][2] = v.z, o[k][3] = v.w;
-          } else {
-            const float2 v = on ? *reinterpret_cast<const float2*>(from) : make_float2(0.f, 0.f);
-            o[k][0] = v.x, o[k][1] = v.y;
+#pragma unroll
+          for (int e = 0; e < kE; ++e) o[k][e] = 0.f;
+          if (have >> (k0 + k) & 1u) {             // (k0 + k <= 31)
+            const float* from = sums + slot(i0 + k0 + k) * (kRows * D);
+            if constexpr (kE == 4) {
+              const float4 v = *reinterpret_cast<const float4*>(from);
+              o[k][0] = v.x, o[k][1] = v.y, o[k][2] = v.z, o[k][3] = v.w;
+            } else {
+              const float2 v = *reinterpret_cast<const float2*>(from);
+              o[k][0] = v.x, o[k][1] = v.y;
+            }
           }
         }
         if (k0 == 0) {
@@ -1153,10 +1160,10 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
           for (int e = 0; e < kE; ++e) acc[e] *= old;
         }
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const float f = __shfl_sync(0xFFFFFFFFu, w, (k0 + k) & 31);
+        for (int k = 0; k < kAhead; ++k) {         // (lanes past the parts hold no weight)
+          const float f = __shfl_sync(0xFFFFFFFFu, w, k0 + k);
 #pragma unroll
-          for (int e = 0; e < kE; ++e) acc[e] = fmaf(o[k][e], k0 + k < n ? f : 0.f, acc[e]);
+          for (int e = 0; e < kE; ++e) acc[e] = fmaf(o[k][e], f, acc[e]);
         }
       }
     }
