@@ -30,6 +30,10 @@
 // part.  Where the page size is a multiple of 8, a copy's box is as many rows as divide both a page and a tile; other
 // pages are gathered row by row, four to a copy.  What no row of the item sees is asked for past the tensor's end, which
 // reads as zeros.  Tensor memory: S_t 2 x 2 x 64 columns, O_t 2 x 128.
+//
+// Measured (64 query heads, 8 key heads of 128): a prompt of 8192 tokens 733 us = 1.5 PFLOP/s, bound by the softmax's
+// latency (1250 cycles per half tile and stream, 2800 a key tile; the products need 2560); 64 single tokens over contexts
+// up to 32K 643 us, the rate of a copy; one token over 4096 keys 13.9 us, nearly all of it latency.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -428,7 +432,7 @@ struct Shape {
   static constexpr uint32_t kMaskOff = kPlanOff + 4 * (kPlanMax + 8) + 4 * kPlanMax * 2;  // keys that exist [8][4] words
   static constexpr uint32_t kBadOff = kMaskOff + 8 * 16;            // values that are no numbers, per piece [16]
   static constexpr uint32_t kOutOff = kBadOff + 64;                 // results on their way out, 2 KB per softmax warp
-  static constexpr uint32_t kStatOff = kOutOff + 8 * 2048;              // (m, l) [stream][128]
+  static constexpr uint32_t kStatOff = kOutOff + 8 * 2048;          // (m, l) [stream][128]
   static constexpr uint32_t kBarOff = kStatOff + 2048;
   static constexpr int kBars = 2 * kStages + 2 * 8 + 8 + 2;
   static constexpr uint32_t kCtlOff = kBarOff + 8 * 48;             // abort, TMEM base

@@ -514,7 +514,8 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  * Long rows are cut where the work of all sequences divides evenly among the SMs, and the parts
  * added in order: results depend on the batch and the device's SM count, but not on timing.
  * Keys and values that a row does not see never touch it, whatever they hold.  An infinity or a
- * NaN that it sees gives what the formula gives (at a value: an infinity or NaN in its dim).
+ * NaN that it sees gives what the formula gives (at a value: an infinity or NaN in its dim),
+ * but a row all of whose scores are -infinity counts as one that sees nothing.
  * Flagged with DSA_DEVERR_INDEX, never accessed out of range: a block id outside [0,
  * num_blocks) or a page at or past bt_stride (its keys are seen by no row); a negative length
  * (0); rows of a sequence outside [0, T) (left out); overlapping sequences (rows are lost).

@@ -142,6 +142,13 @@ def test_more_key_heads_than_pieces_and_wide_groups():
     Case([2, 1], [50, 400], 130, 1, 128, seed=3).check()
 
 
+def test_no_new_tokens_and_many_key_heads():
+    c = Case([0, 0], [5, 9], 8, 2, 64).check()               # nothing to do: nothing is written
+    assert bool((c.out == -7).all())
+    Case([2, 1], [30, 200], 260, 260, 64, bs=8, seed=1).check()
+    Case([1], [3000], 520, 130, 128, bs=64, sink=True, seed=2).check()
+
+
 def test_plan_of_many_sequences():
     # more sequences, and more row blocks, than a CTA plans by itself
     new = [i % 3 for i in range(1500)]
