@@ -33,7 +33,7 @@
 //
 // Measured (64 query heads, 8 key heads of 128): a prompt of 8192 tokens 733 us = 1.5 PFLOP/s, bound by the softmax's
 // latency (1250 cycles per half tile and stream, 2800 a key tile; the products need 2560); 64 single tokens over contexts
-// up to 32K 643 us, the rate of a copy; one token over 4096 keys 13.9 us, nearly all of it latency.
+// up to 32K 636 us, the rate of a copy; one token over 4096 keys 12.8 us, nearly all of it latency.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -52,7 +52,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;                // base-2 headroom before the running maximum moves
 constexpr int kPlanMax = 512;                // row blocks (and sequences) that a CTA plans by itself
-constexpr int kItemCost = 3;                 // an item's fixed cost, in key tiles (8192-token prompt: 2 840, 3 744, 4 751, 6 769 us)
+constexpr int kItemCost = 3;                 // an item's fixed cost, in key tiles (8192-token prompt: 2 747, 3 736, 4 744 us)
 
 // n / d for 0 <= n < 2^31 as a product and a shift (Granlund and Montgomery: with 2^(s-1) < d <= 2^s and mul =
 // ceil(2^(31+s) / d) the excess mul d - 2^(31+s) < 2^s is too small to reach the next quotient).  Every role finds its
@@ -229,7 +229,8 @@ __device__ int make_plan(const AttnArgs& a, V* prefix, int32_t* first, int32_t* 
 }
 
 // The same plan for at most 32 sequences of few row blocks by one warp, a sequence and then a row block per lane: one trip
-// to memory and no barrier but the last (2 us less for a batch of 12 than by all warps).
+// to memory and no barrier but the last.  One token over 4096 keys 12.8 us, by all warps 13.3; 32 x 2 tokens 23.7 and 24.4;
+// with 58 and more row blocks no difference.
 constexpr int kWarpPlan = 96;
 template <int kRows>
 __device__ int make_small_plan(const AttnArgs& a, uint32_t* prefix, int32_t* first, int32_t* seq, int* count_s, bool tell) {
@@ -481,7 +482,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
                "r"(on ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Bits [lo, hi) of a word, for any lo and hi.
@@ -1076,24 +1076,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             continue;
           }
           // row tiles that are no boxes: a piece of 16 bytes per thread and pass
-          const int pc = lt % kPer;
-          int row = 128 * t + lt / kPer;
-          uint32_t token = (uint32_t)a.by_group.of(it.row0 + row), g = (uint32_t)(it.row0 + row) - token * (uint32_t)a.G;
-          const uint32_t more = (uint32_t)a.by_group.of(kStep), left = (uint32_t)kStep - more * (uint32_t)a.G;
+          const int pc = lt % kPer, r0 = lt / kPer;
+          const int first = it.row0 + 128 * t + r0, left = it.rows - 128 * t - r0;   // rows from the thread's first on
+          const int token = a.by_group.of(first);
+          uint32_t g = (uint32_t)(first - token * a.G);
+          // from row to row: kStep heads on, which is `more` tokens and `on` heads, or one token more and G heads less
+          const int more = a.by_group.of(kStep);
+          const uint32_t on = (uint32_t)(kStep - more * a.G);
+          const uint16_t* src = a.q + (int64_t)(it.s + token) * a.ldq + (int64_t)(p.hk * a.G + (int)g) * D + pc * 8;
+          const int64_t hop = more * a.ldq + (int64_t)on * D, wrap = a.ldq - (int64_t)a.G * D;
+          const uint32_t dst = sm32 + (uint32_t)t * Sh::kTile + (uint32_t)(pc >> 3) * 16384u + (uint32_t)r0 * 128u;
 #pragma unroll 4
           for (int i = 0; i < 128 / kStep; ++i) {
-            const int r = row & 127;
-            const bool on = row < it.rows;
-            const uint16_t* src = on ? a.q + (int64_t)(it.s + (int)token) * a.ldq + (int64_t)(p.hk * a.G + (int)g) * D + pc * 8 : a.q;
-            copy16(sm32 + (uint32_t)t * Sh::kTile + (uint32_t)(pc >> 3) * 16384u + (uint32_t)r * 128u +
-                       (uint32_t)(((pc & 7) ^ (r & 7)) << 4), src, on);
-            row += kStep;
-            token += more, g += left;
-            if (g >= (uint32_t)a.G) g -= (uint32_t)a.G, ++token;
+            const bool live = i * kStep < left;
+            copy16(dst + (uint32_t)(i * kStep) * 128u + (uint32_t)(((pc & 7) ^ ((r0 + i * kStep) & 7)) << 4), live ? src : a.q, live);
+            src += hop, g += on;
+            if (g >= (uint32_t)a.G) g -= (uint32_t)a.G, src += wrap;
           }
-          copies_wait();
+          asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        if (!a.q_boxes && ok) {
+          if (kTiles == 2 && it.rows > 128) {      // the first tile's may be used before the second's are there
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            proxy_fence();
+            mbar_arrive(bar(kQFull));
+          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
           proxy_fence();
-          mbar_arrive(bar(kQFull + t));
+          mbar_arrive(bar(kQFull + (kTiles == 2 && it.rows > 128 ? 1 : 0)));
         }
         if (p.block != block) {
           block = p.block;
@@ -1265,7 +1275,8 @@ struct Layout {
   size_t meta, ml, part, prefix, first, seq, total;
 };
 
-// Two row tiles where a sequence brings more than one on average: each key tile then feeds twice the products.
+// Two row tiles where a sequence brings more than one on average: each key tile then feeds twice the products.  (8192-token
+// prompt 737 us, with one 902; one token over 4096 keys 15.6 us with two, 12.8 with one.)
 Layout layout(int64_t T, int B, int H, int Hkv, int D, int num_sms) {
   Layout y{};
   const int64_t G = H / Hkv;
