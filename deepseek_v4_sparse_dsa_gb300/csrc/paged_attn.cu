@@ -735,11 +735,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         if (whole) {
           const float top = fmaxf(m, sk);
           float inv;
-          if (top == -INFINITY && !(l != l)) {
+          if (top == -INFINITY && !(l != l) && !(sn != sn)) {
             inv = 0.f;
-            l = -INFINITY;                                         // lse
+            l = sn;                                                // lse (a sink near the lowest fp32 has no base-2 form)
           } else {
-            const float g = ex2(m - top), den = l * g + ex2(sk - top);
+            const float g = ex2(m - top), den = l * g + (sk == top ? 1.f : ex2(sk - top));    // (the sink may be infinite)
             inv = g / den;
             l = (sk >= m ? sn : m * kLn2) + logf(den);
           }
@@ -1095,6 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
           }
           asm volatile("cp.async.commit_group;" ::: "memory");
         }
+        if (!a.q_boxes && !ok) asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (!a.q_boxes && ok) {
           if (kTiles == 2 && it.rows > 128) {      // the first tile's may be used before the second's are there
             asm volatile("cp.async.wait_group 1;" ::: "memory");
@@ -1253,13 +1254,13 @@ __global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ At
       }
     }
     const bool none = M == -INFINITY && !(den != den);
-    den += M == -INFINITY ? 0.f : ex2(sk - M);
+    den += M == -INFINITY ? 0.f : sk == M ? 1.f : ex2(sk - M);
     const float inv = none ? 0.f : 1.f / den;
     uint16_t* dst = a.out + (int64_t)(m0.y + token) * a.ldo + (int64_t)head * D + lane * kE;
 #pragma unroll
     for (int e = 0; e < kE; e += 2)
       *reinterpret_cast<__nv_bfloat162*>(dst + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-    if (a.lse != nullptr && lane == 0) a.lse[(int64_t)(m0.y + token) * a.H + head] = none ? -INFINITY : (sk >= M ? sn : M * kLn2) + logf(den);
+    if (a.lse != nullptr && lane == 0) a.lse[(int64_t)(m0.y + token) * a.H + head] = none ? sn : (sk >= M ? sn : M * kLn2) + logf(den);
   }
 }
 

@@ -441,10 +441,10 @@ dsa_status dsa_rope_table(dsa_rope_params params, int rope_dim, int64_t pos0, in
  *           of y with an input, and heads of y do not overlap one another.
  *  positions [T] int32; one outside [0, max_pos) gives zeros in the rotated dims and sets
  *           DSA_DEVERR_INDEX.  cos_sin [max_pos, rope_dim] fp32 as dsa_rope_table writes it.
- * D <= 256 (DSA_ERR_UNSUPPORTED above); rope_dim even, >= 2, rope_off + rope_dim <= D; |hx|,
- * |hy| >= D where H > 1, token strides any.  Any
- * element-aligned pointers and strides work; heads move in units of four elements where D is a
- * multiple of 8, rope_off of 4, rope_dim of 4 (HALF: 8), the strides of 4, and pointers are
+ * D <= 256 (DSA_ERR_UNSUPPORTED above); rope_dim even, >= 2, rope_off + rope_dim <= D; hx and
+ * hy >= D where H > 1, ldx and ldy >= D where T > 1 (heads may lie outside tokens).  Any
+ * element-aligned pointers and such strides work; heads move in units of four elements where D
+ * is a multiple of 8, rope_off of 4, rope_dim of 4 (HALF: 8), the strides of 4, and pointers are
  * aligned to four elements (the table and gains to 16 bytes).
  * fp32 arithmetic, one rounding to `type` at the end.
  */
@@ -498,7 +498,8 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  *  block_table [B, bt_stride] int32; kv the cache (see dsa_kv_cache); block_size any >= 1.
  *           Entries of pages that hold no visible key are not read (with a window the old
  *           pages of a sequence may be gone).
- *  sink     [H] fp32 logits that join the denominators, nullable.  lse [T, H] fp32, nullable.
+ *  sink     [H] fp32 logits that join the denominators, nullable; an entry of -infinity counts for
+ *           nothing, one of +infinity makes its head's rows zeros.  lse [T, H] fp32, nullable.
  *  ws       dsa_paged_attn_workspace_bytes(T, B, H, Hkv, D) bytes, 16-byte aligned; its
  *           contents on entry do not matter.  Calls that may run at the same time need one each.
  * Pointers of q, out and kv are 16-byte aligned, ldq, ldo and kv's strides multiples of 8,

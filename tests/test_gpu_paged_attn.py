@@ -170,6 +170,28 @@ def test_rows_that_see_nothing():
     assert torch.equal(c.lse[10:14], c.sink.expand(4, 8)) and bool((c.out[10:14, :1024] == 0).all())
 
 
+@pytest.mark.parametrize("new, lens", [([1, 4], [20000, 2]), ([200, 3], [9000, 1])])      # cut and whole items, empty rows
+def test_sinks_without_a_finite_form_in_base_2(new, lens):
+    c = Case(new, lens, 4, 2, 128, bs=64)
+    c.check()                                                # no sinks
+    out, lse = (x[c.rows].clone() for x in (c.out, c.lse))
+    low = torch.finfo(torch.float32).min
+    c.sink = torch.tensor([math.inf, -math.inf, low, math.nan], device="cuda")
+    for gone in (False, True):
+        if gone:                                             # every page's entry is bad: all rows see nothing
+            c.table.fill_(-1)
+            out.zero_()
+            lse.fill_(-math.inf)
+        c.run()
+        assert dsa.dsa_device_error() == (dsa.DSA_DEVERR_INDEX if gone else 0)
+        got, l = c.out[c.rows].view(-1, 4, 128), c.lse[c.rows]
+        assert bool((got[:, 0] == 0).all()) and bool((l[:, 0] == math.inf).all())
+        assert bool(got[:, 3].isnan().all()) and bool(l[:, 3].isnan().all())
+        assert torch.equal(got[:, 1:3], out.view(-1, 4, 128)[:, 1:3])          # e^sink is nothing next to any score
+        assert torch.equal(l[:, 1], lse[:, 1])
+        assert torch.equal(l[:, 2], lse[:, 2].clamp(min=low))
+
+
 def test_strides_gaps_and_shared_keys_and_values():
     Case([5, 70], [200, 70], 8, 2, 128, pad=24, gap=3, spare=9, head_major=True, sink=True).check()
     Case([5, 70], [200, 300], 16, 1, 128, shared=True, bs=64, pad=8, gap=1).check()
