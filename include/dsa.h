@@ -512,6 +512,7 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  * statistics; each weight is rounded once to bf16 for its product with v, the denominator sums
  * the unrounded ones: |out - exact| <= (2^-8 + 2 max_j |ds_j|) sum_j p_j |v_j| + 2^-8 |exact| to
  * first order, p_j the exact weights and ds_j the fp32 error of score j; lse is fp32 throughout.
+ * What is below 2^-126 of a row's denominator counts as zero.
  * Long rows are cut where the work of all sequences divides evenly among the SMs, and the parts
  * added in order: results depend on the batch and the device's SM count, but not on timing.
  * Keys and values that a row does not see never touch it, whatever they hold.  An infinity or a
