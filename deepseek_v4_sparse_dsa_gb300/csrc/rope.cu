@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
           }
         }
       } else if constexpr (kHalf) {
-        if (ra) {
+        if (ra && kind < 2) {                      // (values: also a turn by cos 1, sin 0 would spread an infinity)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float x0 = f[e], x1 = g[e];
@@ -311,12 +311,12 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
       } else {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if (ra) {
+          if (ra && kind < 2) {
             const float x0 = f[2 * k], x1 = f[2 * k + 1];
             f[2 * k] = x0 * cs[k] - x1 * sn[k];
             f[2 * k + 1] = x0 * sn[k] + x1 * cs[k];
           }
-          if (rb) {
+          if (rb && kind < 2) {
             const float x0 = g[2 * k], x1 = g[2 * k + 1];
             g[2 * k] = x0 * cs[2 + k] - x1 * sn[2 + k];
             g[2 * k + 1] = x0 * sn[2 + k] + x1 * cs[2 + k];

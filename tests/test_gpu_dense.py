@@ -350,3 +350,25 @@ def test_rope_calls_on_streams_and_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(y, y1) and torch.equal(z, z1)
     assert dsa.dsa_device_error() == 0
+
+
+# ------------------------------------------------------------------ what is copied, and what stays by itself
+@pytest.mark.parametrize("layout", [INTER, HALF])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D, R, off, shift", [(64, 64, 0, 0), (128, 64, 64, 0), (96, 24, 12, 0), (64, 32, 3, 0), (33, 10, 7, 0),
+                                              (64, 64, 0, 1)])
+def test_values_are_copied_whatever_they_hold(D, R, off, shift, dtype, norm, layout):
+    # infinities, NaNs and zeros of both signs, in dims that turn in queries and keys and in dims that do not: nothing of
+    # a value's neighbours reaches it, and every bit but a NaN's payload is the input's (rounded to bf16)
+    c = QK(23, 3, 2, D, R, off, layout, dtype, norm=norm, shift=shift, seed=3)
+    pick = torch.randint(0, 24, c.v.shape, device="cuda", generator=gen(4))
+    for i, x in enumerate((float("inf"), -float("inf"), float("nan"), -0.0, 0.0)):
+        c.v[pick == i] = x
+    wanted = c.v.reshape(23, 2, D).bfloat16()
+    c.run()
+    got = c.vc[c.slot // c.bs, c.slot % c.bs]
+    nan = wanted.isnan()
+    assert torch.equal(got.isnan(), nan)
+    assert torch.equal(got.view(torch.int16)[~nan], wanted.view(torch.int16)[~nan])
+    assert dsa.dsa_device_error() == 0
