@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
       }
     }
     // Behind a norm every element is r (x p + partner q): p and q hold the gains and the rotation, and are found once.
-    // (For dims that do not turn, q and what it multiplies are zero.)
+    // (For dims that do not turn, q and what it multiplies are zero, whatever the other gain is.)
     float pa[4], pb[4], qa[4], qb[4];
     if constexpr (kNorm) {
       float ga[4] = {1.f, 1.f, 1.f, 1.f}, gb[4] = {1.f, 1.f, 1.f, 1.f};
@@ -266,11 +266,11 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
         pa[e] = ga[e] * c0;
         pb[e] = gb[e] * c1;
         if constexpr (kHalf) {
-          qa[e] = -gb[other] * s0;
-          qb[e] = ga[other] * s1;
+          qa[e] = ra ? -gb[other] * s0 : 0.f;
+          qb[e] = rb ? ga[other] * s1 : 0.f;
         } else {
-          qa[e] = (e & 1 ? ga[other] : -ga[other]) * s0;
-          qb[e] = (e & 1 ? gb[other] : -gb[other]) * s1;
+          qa[e] = ra ? (e & 1 ? ga[other] : -ga[other]) * s0 : 0.f;
+          qb[e] = rb ? (e & 1 ? gb[other] : -gb[other]) * s1 : 0.f;
         }
       }
     }

@@ -372,3 +372,22 @@ def test_values_are_copied_whatever_they_hold(D, R, off, shift, dtype, norm, lay
     assert torch.equal(got.isnan(), nan)
     assert torch.equal(got.view(torch.int16)[~nan], wanted.view(torch.int16)[~nan])
     assert dsa.dsa_device_error() == 0
+
+
+@pytest.mark.parametrize("layout", [INTER, HALF])
+@pytest.mark.parametrize("D, R, off", [(128, 64, 64), (128, 64, 0), (96, 24, 12), (128, 0, 0), (40, 10, 7)])
+def test_gains_that_are_no_numbers_stay_in_their_dims(D, R, off, layout):
+    clean, c = (QK(7, 2, 2, D, R, off, layout, torch.float32, seed=5) for _ in range(2))
+    still = [d for d in range(D) if not off <= d < off + R]
+    hit = {still[1]: float("nan"), still[5]: float("inf"), still[-2]: -float("inf")}
+    for d, x in hit.items():
+        c.gq[d] = c.gk[d] = x
+    outs = []
+    for x in (clean, c):
+        x.run(k_out=torch.empty(7, 2 * D, device="cuda"))
+        outs.append((x.qo.view(7, 2, D), x.ko.view(7, 2, D), x.kc[x.slot // x.bs, x.slot % x.bs].float()))
+    rest = [d for d in range(D) if d not in hit]
+    for a, b in zip(*outs):
+        assert torch.equal(a[..., rest], b[..., rest])
+        assert not bool(b[..., list(hit)].isfinite().any())
+    assert dsa.dsa_device_error() == 0
