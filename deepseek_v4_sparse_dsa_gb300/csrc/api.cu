@@ -447,9 +447,9 @@ dsa_status dsa_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int 
   if (ldq >= (int64_t)1 << 39) return DSA_ERR_UNSUPPORTED;                                   // tensor-map strides
   if (!paged_attn_cache_fits(kv, Hkv)) return DSA_ERR_UNSUPPORTED;
   const int sms = device_sm_count();
-  if (ws == nullptr || ws_bytes < paged_attn_ws_bytes(T, B, H, Hkv, D, sms) || !aligned(ws, 16)) return DSA_ERR_WORKSPACE;
+  if (ws == nullptr || ws_bytes < paged_attn_least_ws_bytes(T, B, H, Hkv, D, sms) || !aligned(ws, 16)) return DSA_ERR_WORKSPACE;
   return cuda_status(launch_paged_attn(q, ldq, T, H, Hkv, D, query_start, context_lens, B, block_table, bt_stride, kv,
-                                       softmax_scale, causal != 0, window, sink, out, ldo, lse, ws, sms,
+                                       softmax_scale, causal != 0, window, sink, out, ldo, lse, ws, ws_bytes, sms,
                                        static_cast<cudaStream_t>(stream)));
 }
 

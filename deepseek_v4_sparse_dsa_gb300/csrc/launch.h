@@ -132,10 +132,11 @@ cudaError_t launch_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k
 // ------------------------------------------------------------------ attention over a paged cache (paged_attn.cu)
 bool paged_attn_cache_fits(const dsa_kv_cache& kv, int Hkv);   // strides whose ratios its copies can address
 size_t paged_attn_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms);
+size_t paged_attn_least_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms);   // what a call takes at the least
 cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* start,
                               const int32_t* lens, int B, const int32_t* table, int64_t bt_stride, const dsa_kv_cache& kv,
                               float scale, bool causal, int window, const float* sink, uint16_t* out, int64_t ldo, float* lse,
-                              void* ws, int num_sms, cudaStream_t stream);
+                              void* ws, size_t ws_bytes, int num_sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------ sparse attention (sparse_attn.cu)
 // q [T, 64, 128] bf16 (16-byte aligned), sel [T, k], the paged mxfp4 cache, sink [64],

@@ -1278,10 +1278,12 @@ struct Layout {
 
 // Two row tiles where a sequence brings more than one on average: each key tile then feeds twice the products.  (8192-token
 // prompt 737 us, with one 902; one token over 4096 keys 15.6 us with two, 12.8 with one.)
-Layout layout(int64_t T, int B, int H, int Hkv, int D, int num_sms) {
+int row_tiles(int64_t T, int B, int H, int Hkv) { return T * (H / Hkv) > 128 * (int64_t)B ? 2 : 1; }
+
+Layout layout(int tiles, int64_t T, int B, int H, int Hkv, int D, int num_sms) {
   Layout y{};
   const int64_t G = H / Hkv;
-  y.tiles = T * G > 128 * (int64_t)B ? 2 : 1;
+  y.tiles = tiles;
   y.rows = 128 * y.tiles;
   y.ctas = num_sms;
   const int64_t blocks = T * G / y.rows + (B < T ? B : T);        // at most so many row blocks
@@ -1379,13 +1381,24 @@ bool paged_attn_cache_fits(const dsa_kv_cache& kv, int Hkv) {
          kv.num_blocks * block_rows + Hkv * head_rows + kv.block_size <= INT32_MAX;
 }
 
-size_t paged_attn_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms) { return layout(T, B, H, Hkv, D, num_sms).total; }
+size_t paged_attn_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms) {
+  return layout(row_tiles(T, B, H, Hkv), T, B, H, Hkv, D, num_sms).total;
+}
+
+// One row tile serves any call, with half the room for parts.  So the size of one step is enough for every smaller one (in
+// T and B), whichever takes two: at the same number of tiles the size only grows with T and B, and where the smaller one
+// alone takes one tile, its plan's 12 bytes for each of at most 2 B row blocks are less than the parts save.
+size_t paged_attn_least_ws_bytes(int64_t T, int B, int H, int Hkv, int D, int num_sms) {
+  const size_t one = layout(1, T, B, H, Hkv, D, num_sms).total, own = paged_attn_ws_bytes(T, B, H, Hkv, D, num_sms);
+  return one < own ? one : own;
+}
 
 cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int Hkv, int D, const int32_t* start,
                               const int32_t* lens, int B, const int32_t* table, int64_t bt_stride, const dsa_kv_cache& kv,
                               float scale, bool causal, int window, const float* sink, uint16_t* out, int64_t ldo, float* lse,
-                              void* ws, int num_sms, cudaStream_t stream) {
-  const Layout y = layout(T, B, H, Hkv, D, num_sms);
+                              void* ws, size_t ws_bytes, int num_sms, cudaStream_t stream) {
+  Layout y = layout(row_tiles(T, B, H, Hkv), T, B, H, Hkv, D, num_sms);
+  if (ws_bytes < y.total) y = layout(1, T, B, H, Hkv, D, num_sms);
   uint8_t* w = static_cast<uint8_t*>(ws);
   AttnArgs a{};
   a.q = q, a.ldq = ldq, a.start = start, a.lens = lens, a.table = table, a.bt_stride = bt_stride;

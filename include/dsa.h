@@ -502,6 +502,9 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  *           nothing, one of +infinity makes its head's rows zeros.  lse [T, H] fp32, nullable.
  *  ws       dsa_paged_attn_workspace_bytes(T, B, H, Hkv, D) bytes, 16-byte aligned; its
  *           contents on entry do not matter.  Calls that may run at the same time need one each.
+ *           The size for some T and B is accepted for every smaller T and B too, although it may
+ *           be less than their own: rows then go 128 at a time instead of 256 (a prompt of 8192
+ *           tokens 902 us instead of 737), and results may differ in their last bits.
  * Pointers of q, out and kv are 16-byte aligned, ldq, ldo and kv's strides multiples of 8,
  * num_blocks at least 1.  The pool is addressed as rows row_stride apart: block_stride is a
  * multiple of row_stride, head_stride smaller than it or a multiple of it, and the pool's rows
@@ -514,7 +517,8 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  * first order, p_j the exact weights and ds_j the fp32 error of score j; lse is fp32 throughout.
  * What is below 2^-126 of a row's denominator counts as zero.
  * Long rows are cut where the work of all sequences divides evenly among the SMs, and the parts
- * added in order: results depend on the batch and the device's SM count, but not on timing.
+ * added in order: results depend on the batch, the device's SM count and whether ws has the
+ * call's own size, but not on timing.
  * Keys and values that a row does not see never touch it, whatever they hold.  An infinity or a
  * NaN that it sees gives what the formula gives (at a value: an infinity or NaN in its dim),
  * but a row all of whose scores are -infinity counts as one that sees nothing.

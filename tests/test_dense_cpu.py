@@ -155,3 +155,19 @@ def test_cache_structure_from_tensors():
     for bad in ((k, v[:, :8]), (k, hm.transpose(1, 2)), (k[..., ::2], v[..., ::2])):
         with pytest.raises(ValueError):
             dsa.make_kv_cache(*bad)
+
+
+def test_workspace_sizes_of_larger_steps():
+    # (only refusals are made here: the addresses are not real)
+    ws = dsa.dsa_paged_attn_workspace_bytes
+    one, two = ws(300, 300, 64, 8, 128), ws(300, 1, 64, 8, 128)
+    assert one < two                                         # a size of its own for one and for two row tiles
+    refused(attn, WORKSPACE, T=300, B=1, H=64, Hkv=8, ldq=8192, ldo=8192, row_stride=1024, block_stride=16384,
+            ws_bytes=ws(1, 1, 64, 8, 128) - 1)
+    # at the same number of tiles the size grows with T and B
+    steps = [(t, b) for t in (1, 5, 128, 1000, 20000) for b in (1, 7, 300, 5000)]
+    for T, B in steps:
+        for T2, B2 in steps:
+            same = (T * 8 > 128 * B) == (T2 * 8 > 128 * B2)
+            if T <= T2 and B <= B2 and same:
+                assert ws(T, B, 64, 8, 128) <= ws(T2, B2, 64, 8, 128)

@@ -504,3 +504,44 @@ def test_expired_waits_are_told_and_leave_the_context_usable(case):
     c.lse.fill_(-7)
     c.ws.fill_(255)
     c.check()
+
+
+# ------------------------------------------------------------------ workspaces, ranges that are none, the error as a whole
+@pytest.mark.parametrize("D, heads", [(128, (64, 8)), (64, (8, 1)), (64, (6, 2))])
+def test_a_workspace_of_a_larger_step_fits_every_smaller_one(D, heads):
+    # a decode batch's buffer serves a chunk of one sequence (whose own size, with two row tiles, is larger) and the
+    # other way round, with either form's results
+    H, Hkv = heads
+    big = dsa.dsa_paged_attn_workspace_bytes(300, 300, H, Hkv, D)
+    assert dsa.dsa_paged_attn_workspace_bytes(250, 1, H, Hkv, D) > big
+    for i, (new, lens) in enumerate([([249], [2000]), ([16] * 10, [700] * 10), ([1], [5000]), ([100, 3, 0], [100, 9000, 7]),
+                                     ([280], [280])]):
+        c = Case(new, lens, H, Hkv, D, bs=64, seed=i, sink=bool(i % 2))
+        assert c.T <= 300 and c.B <= 300
+        c.check()
+        c.ws = torch.full((big,), 255, device="cuda", dtype=torch.uint8)
+        c.out.fill_(-7)
+        c.lse.fill_(-7)
+        c.check()
+        again = c.out.clone()
+        c.run()
+        assert torch.equal(c.out, again)
+    with pytest.raises(dsa.DsaError) as e:
+        c.ws = c.ws[:1 << 20]
+        c.run()
+    assert e.value.status == dsa.DSA_ERR_WORKSPACE
+    # a chunk's buffer serves a decode batch
+    big = dsa.dsa_paged_attn_workspace_bytes(4096, 64, H, Hkv, D)
+    c = Case([1] * 60, [90 * b + 1 for b in range(60)], H, Hkv, D, bs=64, seed=9)
+    assert c.ws.numel() <= big
+
+
+def test_a_workspace_of_many_sequences_serves_one_long_chunk():
+    # row blocks of 128 rows, more than a CTA plans by itself
+    c = Case([1100], [1300], 64, 1, 64, seed=1).check()
+    size = dsa.dsa_paged_attn_workspace_bytes(c.T, c.T, 64, 1, 64)
+    assert size < c.ws.numel() and c.T * 64 // 128 > 512
+    c.ws = torch.full((size,), 255, device="cuda", dtype=torch.uint8)
+    c.out.fill_(-7)
+    c.lse.fill_(-7)
+    c.check()
