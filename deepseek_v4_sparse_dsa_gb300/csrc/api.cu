@@ -3,6 +3,7 @@
 #include <cmath>
 #include <atomic>
 #include <cstdint>
+#include <limits>
 #include <mutex>
 
 #include "launch.h"
@@ -323,7 +324,8 @@ dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, co
 
 dsa_status dsa_rope_table(dsa_rope_params p, int rope_dim, int64_t pos0, int64_t n, float* cos_sin, void* stream) {
   if (rope_dim < 2 || rope_dim % 2 != 0 || n < 0 || pos0 < 0) return DSA_ERR_INVALID_ARG;
-  if (!(p.base > 1.0) || !std::isfinite(p.base) || !std::isfinite(p.amplitude)) return DSA_ERR_INVALID_ARG;
+  if (!(p.base > 1.0) || !std::isfinite(p.base)) return DSA_ERR_INVALID_ARG;
+  if (!(std::fabs(p.amplitude) <= (double)std::numeric_limits<float>::max())) return DSA_ERR_INVALID_ARG;   // the table is fp32
   if (p.scaling != DSA_ROPE_PLAIN && p.scaling != DSA_ROPE_LINEAR && p.scaling != DSA_ROPE_YARN) return DSA_ERR_INVALID_ARG;
   if (p.scaling != DSA_ROPE_PLAIN && (!(p.factor >= 1.0) || !std::isfinite(p.factor))) return DSA_ERR_INVALID_ARG;
   if (p.scaling == DSA_ROPE_YARN &&

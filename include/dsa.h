@@ -80,7 +80,7 @@ typedef struct {
   double original_max_pos;   /* YARN: the context the frequencies were trained for       */
   double beta_fast;          /* YARN: turns within it above which a pair is kept         */
   double beta_slow;          /* YARN: turns below which it is slowed by the factor       */
-  double amplitude;          /* multiplies cos and sin (1 for none)                      */
+  double amplitude;          /* multiplies cos and sin (1 for none); within fp32's range  */
 } dsa_rope_params;
 
 /*

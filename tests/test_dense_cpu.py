@@ -171,3 +171,8 @@ def test_workspace_sizes_of_larger_steps():
             same = (T * 8 > 128 * B) == (T2 * 8 > 128 * B2)
             if T <= T2 and B <= B2 and same:
                 assert ws(T, B, 64, 8, 128) <= ws(T2, B2, 64, 8, 128)
+
+
+@pytest.mark.parametrize("amplitude", [1e39, -1e300, 3.5e38])
+def test_table_refuses_an_amplitude_past_fp32(amplitude):
+    refused(table, INVALID, amplitude=amplitude)
