@@ -425,7 +425,8 @@ dsa_status dsa_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, int 
   dsa_status s = check_attn_sizes(T, B, H, Hkv, D);
   if (s != DSA_OK) return s;
   if (T == 0 || B == 0) return DSA_OK;
-  if (window < 0 || bt_stride < 1 || !(softmax_scale > 0.f) || !std::isfinite(softmax_scale)) return DSA_ERR_INVALID_ARG;
+  if (window < 0 || bt_stride < 1 || !(softmax_scale > 0.f)) return DSA_ERR_INVALID_ARG;
+  if (!(softmax_scale * 1.4426950408889634 <= (double)std::numeric_limits<float>::max())) return DSA_ERR_INVALID_ARG;   // in base 2
   if (q == nullptr || query_start == nullptr || context_lens == nullptr || block_table == nullptr || kv.k == nullptr ||
       kv.v == nullptr || out == nullptr)
     return DSA_ERR_INVALID_ARG;

@@ -510,7 +510,8 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  * multiple of row_stride, head_stride smaller than it or a multiple of it, and the pool's rows
  * fewer than 2^31 (DSA_ERR_UNSUPPORTED otherwise).
  * D is 64 or 128 (DSA_ERR_UNSUPPORTED otherwise), Hkv divides H, B <= 65536, T * H < 2^31,
- * softmax_scale > 0.  No output overlaps an input or another output.
+ * softmax_scale > 0, its product with log2(e) within fp32's range.  No output overlaps an input
+ * or another output.
  * Arithmetic: bf16 products summed in fp32 by the tensor cores, softmax in base 2 with fp32
  * statistics; each weight is rounded once to bf16 for its product with v, the denominator sums
  * the unrounded ones: |out - exact| <= (2^-8 + 2 max_j |ds_j|) sum_j p_j |v_j| + 2^-8 |exact| to

@@ -176,3 +176,9 @@ def test_workspace_sizes_of_larger_steps():
 @pytest.mark.parametrize("amplitude", [1e39, -1e300, 3.5e38])
 def test_table_refuses_an_amplitude_past_fp32(amplitude):
     refused(table, INVALID, amplitude=amplitude)
+
+
+@pytest.mark.parametrize("scale", [2.4e38, 3.4e38])
+def test_attn_refuses_a_scale_past_fp32_in_base_2(scale):
+    # the softmax multiplies scores by scale log2(e): with an infinite factor a score of zero would be no number
+    refused(attn, INVALID, scale=scale)
