@@ -432,10 +432,11 @@ dsa_status dsa_rope_table(dsa_rope_params params, int rope_dim, int64_t pos0, in
 
 /*
  * dsa_rope -- rotation of heads.  For every token t and head h, with c and s the cosine and
- * sine of pair i at positions[t] (s negated where inverse is set: the rotation is taken back,
- * which is also its gradient where the table's amplitude is 1), the elements (x0, x1) =
+ * sine of pair i at positions[t] (s negated where inverse is set), the elements (x0, x1) =
  * (rope_off + 2i, rope_off + 2i + 1) (INTERLEAVED) or (rope_off + i, rope_off + rope_dim / 2
  * + i) (HALF), i < rope_dim / 2, become (x0 c - x1 s, x0 s + x1 c); the other dims are copied.
+ * With the same table the inverse is the gradient of the call without it; it takes the rotation
+ * back where the table's amplitude is 1 (otherwise the turned dims come back times its square).
  *  x, y     heads of D elements of `type`: token t, head h at t * ldx + h * hx (t * ldy +
  *           h * hy), in elements.  y may be x where the strides are the same; no other overlap
  *           of y with an input, and heads of y do not overlap one another.

@@ -391,3 +391,27 @@ def test_gains_that_are_no_numbers_stay_in_their_dims(D, R, off, layout):
         assert torch.equal(a[..., rest], b[..., rest])
         assert not bool(b[..., list(hit)].isfinite().any())
     assert dsa.dsa_device_error() == 0
+
+
+@pytest.mark.parametrize("layout", [INTER, HALF])
+def test_rope_inverse_under_an_amplitude(layout):
+    # y = A R x: with the same table the inverse form gives A R^T g, which is the gradient, and A^2 x for y itself
+    T, H, D, R, A = 5, 2, 64, 32, 1.25
+    cs = torch.empty(16, R, device="cuda")
+    dsa.dsa_rope_table(dsa.make_rope_params(amplitude=A), R, 0, 16, cs)
+    pos = torch.tensor([0, 3, 15, 1, 8], device="cuda", dtype=torch.int32)
+    x, g, y, grad, back = (torch.randn(T, H, D, device="cuda", generator=gen(s)) for s in range(5))
+    call = lambda a, b, inv: dsa.dsa_rope(a, H * D, D, pos, cs, 16, R, 16, layout, inv, T, H, D, F32, b, H * D, D)  # noqa: E731
+    call(x, y, False)
+    call(g, grad, True)
+    call(y, back, True)
+    leaf = x.double().requires_grad_(True)
+    (ref.rotate(leaf, cs[pos.long()], R, 16, layout == HALF)[0] * g.double()).sum().backward()
+    _, part = ref.rotate(g.double(), cs[pos.long()], R, 16, layout == HALF, True)
+    ref.close(grad, leaf.grad, part, torch.float32, 3 * 2.0 ** -24)
+    # twice three roundings of parts no larger than A (|x0| + |x1|), and cos^2 + sin^2 of a table within 2^-22 A
+    turned = torch.ones(D, device="cuda", dtype=torch.float64)
+    turned[16:48] = A * A
+    size = 2 * A * A * float(x.abs().max())
+    assert float((back.double() - x.double() * turned).abs().max()) <= (12 * 2.0 ** -24 + 4 * 2.0 ** -22) * size
+    assert dsa.dsa_device_error() == 0
