@@ -545,3 +545,51 @@ def test_a_workspace_of_many_sequences_serves_one_long_chunk():
     c.out.fill_(-7)
     c.lse.fill_(-7)
     c.check()
+
+
+def test_ranges_that_are_none_are_left_out():
+    # each sequence whose rows are no range of the T rows is left out, the others get what they always get, and a row of
+    # no sequence stays as it was
+    q_rows, lens = 8, [100, 90, 60]
+    for starts in ([0, 2, 5, 600], [0, -3, 5, 6], [4, 2, 5, 6], [0, 3, 1, 7], [7, 7, 7, 9], [-1, 2, 2, 8], [0, 8, 0, 8]):
+        c = Case([3, 3, 2], lens, 4, 2, 64, seed=4, spare=0)
+        assert c.T == q_rows
+        c.start = torch.tensor(starts, device="cuda", dtype=torch.int32)
+        c.run()
+        assert dsa.dsa_device_error() == dsa.DSA_DEVERR_INDEX
+        owner = [[b for b in range(3) if starts[b] <= t < starts[b + 1] and 0 <= starts[b] and starts[b + 1] <= q_rows]
+                 for t in range(q_rows)]
+        out, lse = c.out.view(q_rows, 4, 64), c.lse
+        for t in range(q_rows):
+            if not owner[t]:
+                assert bool((out[t] == -7).all()) and bool((lse[t] == -7).all())
+        for b in range(3):
+            s, e = starts[b], starts[b + 1]
+            rows = [t for t in range(max(s, 0), max(e, 0)) if t < q_rows and owner[t] == [b]]
+            if not rows:
+                continue
+            q = c.q[s:e].reshape(e - s, 4, 64)
+            want = ref.attention(q, [c.k_rows[b]], [c.v_rows[b]], [e - s], [lens[b]], c.scale, True, 0, None)
+            at = [t - s for t in rows]
+            assert bool(((out[rows].double() - want[0][at]).abs() <= want[2][at]).all())
+            assert bool(((lse[rows].double() - want[1][at]).abs() <= want[3][at]).all())
+
+
+@pytest.mark.parametrize("new, lens, kw", [
+    ([1] * 8, [4096 * (b + 1) for b in range(8)], dict(H=16, Hkv=2, D=128, bs=64)),
+    ([256], [20000], dict(H=16, Hkv=2, D=128, bs=64)),
+    ([1500, 30], [1500, 9000], dict(H=8, Hkv=2, D=64, bs=16)),
+    ([2] * 6, [9000] * 6, dict(H=64, Hkv=1, D=128, bs=64, window=4096, sink=True)),
+])
+def test_the_norm_of_the_error(new, lens, kw):
+    # Per element the bound of dense_ref is worst case; as a whole the roundings are as often up as down.  A rounding to
+    # bf16 is off by at most 2^-8 of the value, evenly spread: 2^-8 / sqrt(3) in the mean square.  The output has its own;
+    # the weights' adds sum_j p_j d_j v_j, whose mean square, for values v_j of either sign, is d^2 of the output's own
+    # sum_j p_j v_j.  Together at most sqrt(2) 2^-8 / sqrt(3) = 3.19e-3 of the norm.  A value that is lost or taken twice
+    # among n even weights is 1 / sqrt(n) of it.
+    c = Case(new, lens, seed=5, **kw)
+    c.run()
+    assert dsa.dsa_device_error() == 0
+    out = c.want()[0]
+    err = c.out[c.rows, :c.H * c.D].double().reshape(out.shape) - out
+    assert float(err.norm() / out.norm()) <= math.sqrt(2.0 / 3) * 2.0 ** -8
