@@ -31,9 +31,11 @@
 // pages are gathered row by row, four to a copy.  What no row of the item sees is asked for past the tensor's end, which
 // reads as zeros.  Tensor memory: S_t 2 x 2 x 64 columns, O_t 2 x 128.
 //
-// Measured (64 query heads, 8 key heads of 128): a prompt of 8192 tokens 733 us = 1.5 PFLOP/s, bound by the softmax's
-// latency (1250 cycles per half tile and stream, 2800 a key tile; the products need 2560); 64 single tokens over contexts
-// up to 32K 636 us, the rate of a copy; one token over 4096 keys 12.8 us, nearly all of it latency.
+// Measured (64 query heads, 8 key heads of 128), calls in a captured graph: a prompt of 8192 tokens 734 us = 1.5 PFLOP/s in a
+// burst of 24 (741 on another GPU), 789 us on and on at the power limit (1942 MHz).  Four fifths of that are the
+// softmax's latency (1250 cycles per half tile and stream, 2800 a key tile; the products need 2560), the rest passes
+// between items and in their parts; of a 4096-token prompt's 220 us it is two thirds.  64 single tokens over contexts up to
+// 32K 637 us, the rate of a copy; one token over 4096 keys 13.0 us, nearly all of it latency.
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
@@ -52,7 +54,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.0f;                // base-2 headroom before the running maximum moves
 constexpr int kPlanMax = 512;                // row blocks (and sequences) that a CTA plans by itself
-constexpr int kItemCost = 3;                 // an item's fixed cost, in key tiles (8192-token prompt: 2 747, 3 736, 4 744 us)
+constexpr int kItemCost = 3;                 // an item's fixed cost, in key tiles (8192-token prompt: 2 748, 3 741, 4 747 us)
 
 // n / d for 0 <= n < 2^31 as a product and a shift (Granlund and Montgomery: with 2^(s-1) < d <= 2^s and mul =
 // ceil(2^(31+s) / d) the excess mul d - 2^(31+s) < 2^s is too small to reach the next quotient).  Every role finds its
@@ -70,8 +72,7 @@ struct AttnArgs {
   const int32_t* lens;         // [B]
   const int32_t* table;        // [B, bt_stride]
   int64_t bt_stride;
-  const uint16_t* k;
-  const uint16_t* v;
+  const uint16_t* v;           // (keys come by copies alone)
   int64_t num_blocks, block_stride, row_stride, head_stride;
   int block_rows, head_rows;   // block_stride and head_stride in rows of the copies' tensor
   int head_cols;               // and what of head_stride lies within a row, in elements
@@ -1277,7 +1278,7 @@ struct Layout {
 };
 
 // Two row tiles where a sequence brings more than one on average: each key tile then feeds twice the products.  (8192-token
-// prompt 737 us, with one 902; one token over 4096 keys 15.6 us with two, 12.8 with one.)
+// prompt 734 us, with one 908; one token over 4096 keys 15.6 us with two, 12.8 with one.)
 int row_tiles(int64_t T, int B, int H, int Hkv) { return T * (H / Hkv) > 128 * (int64_t)B ? 2 : 1; }
 
 Layout layout(int tiles, int64_t T, int B, int H, int Hkv, int D, int num_sms) {
@@ -1402,7 +1403,7 @@ cudaError_t launch_paged_attn(const uint16_t* q, int64_t ldq, int64_t T, int H, 
   uint8_t* w = static_cast<uint8_t*>(ws);
   AttnArgs a{};
   a.q = q, a.ldq = ldq, a.start = start, a.lens = lens, a.table = table, a.bt_stride = bt_stride;
-  a.k = static_cast<const uint16_t*>(kv.k), a.v = static_cast<const uint16_t*>(kv.v);
+  a.v = static_cast<const uint16_t*>(kv.v);
   a.num_blocks = kv.num_blocks, a.block_stride = kv.block_stride, a.row_stride = kv.row_stride, a.head_stride = kv.head_stride;
   a.block_size = kv.block_size;
   a.cap = bt_stride > INT32_MAX / kv.block_size ? INT32_MAX : bt_stride * kv.block_size;

@@ -8,8 +8,9 @@
 // Sums, norm and rotation are fp32; a result is rounded once, to the rows' type or to the cache's bf16.
 //
 // All of it streams: each element is read once and written once, the table's rows come from L2.  Measured: rotation of
-// 8192 x 64 x 128 in bf16 44 us (91 % of the copy rate); 8192 tokens of 64 query and 8 key and value heads with the norm
-// 61 us (81 %; HBM and issue slots together); a table of 1 M positions x 64 50 us (79 %; instructions); one token 2.7 us.
+// 8192 x 64 x 128 in bf16 44 us (92 % of the copy rate), in fp32 82 (97 %); 8192 tokens of 64 query and 8 key and value
+// heads with the norm 63 us (79 %; HBM and issue slots together), in halves 60, in fp32 98 (96 %), without it 52 (95 %); a
+// table of 1 M positions x 64 51 us (77 %; instructions); one token 3.0 us.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -23,7 +24,7 @@ namespace {
 
 // ------------------------------------------------------------------ table
 // An angle is needed modulo a turn only.  With W_i = f_i / 2 pi turns as a 64-bit binary fraction, the product p W_i
-// modulo 2^64 is the angle's fraction of a turn, exact but for W's own rounding (p 2^-65 turns): far positions lose
+// modulo 2^64 is the angle's fraction of a turn, exact but for W's truncation (p 2^-64 turns): far positions lose
 // nothing and no 64-bit floating point is needed.  The nearest quarter turn is taken off before the conversion to
 // fp32, so that what is left, at most 1/8 turn, keeps 24 significant bits; there the Taylor polynomials of degree 9 and 8
 // are within 2.5e-8 of the sine and the cosine (the terms left out: x^11 / 11!, x^10 / 10! at pi / 4).
@@ -344,7 +345,9 @@ __global__ void __launch_bounds__(256) rope_heads_kernel(const __grid_constant__
 }
 
 // Heads at any alignment, of any size up to 256 and with any part that turns: a warp per head, its values in shared
-// memory between the norm and the rotation (a pair's elements lie in different lanes).
+// memory between the norm and the rotation (a pair's elements lie in different lanes).  For what units do not fit; far from
+// the copy rate with its accesses of single elements: rotation of 8192 x 64 x 128 at an odd offset 364 us in bf16 and 288 in
+// fp32 (floors 40 and 79), 8192 tokens of 64 + 2 x 8 heads with the norm 544 and 440 (50 and 94).
 template <bool F32>
 __global__ void __launch_bounds__(256) rope_heads_any_kernel(const __grid_constant__ HeadArgs a, bool norm, bool halves) {
   __shared__ float row_s[8][256];

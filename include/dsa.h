@@ -411,9 +411,9 @@ dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, co
                          void* stream);
 
 /*
- * The calls of a layer that attends to every cached key (a draft layer, a layer without the
- * selection, a prompt no longer than it).  (The pages have no counterpart.)  The table is made
- * once; dsa_qk_norm_rope turns the projected heads and writes keys and values to the slots of
+ * The calls of a layer that attends to every cached key and keeps them in bf16 (a draft layer, a
+ * layer without the selection).  (The pages have no counterpart.)  The table is made once;
+ * dsa_qk_norm_rope turns the projected heads and writes keys and values to the slots of
  * dsa_assign_slots; dsa_paged_attn reads them through its block table, query_start and
  * context_lens; dsa_rope with inverse set takes the rotation of an output back.
  *
@@ -424,6 +424,8 @@ dsa_status dsa_gemm_e4m3(const uint8_t* a, int64_t lda, const float* a_scale, co
  *   YARN (Peng et al. 2023): f_i (1 - w_i) + f_i / factor w_i, w_i = clamp((i - lo) / (hi -
  *   lo), 0, 1), lo = max(floor(c(beta_fast)), 0), hi = min(ceil(c(beta_slow)), rope_dim - 1),
  *   c(b) = rope_dim ln(original_max_pos / (2 pi b)) / (2 ln base); hi - lo is at least 0.001.
+ *   (The paper's factor on the attention's scale, 0.1 ln(factor) + 1 on queries and keys alike,
+ *   is the caller's to give as the amplitude; nothing is multiplied by itself.)
  *  cos_sin  [n, rope_dim] fp32.  rope_dim even, 2 .. 256; pos0 >= 0, pos0 + n <= 2^31.
  * Each value is within 2^-22 amplitude of the exact one at any position: the angle is reduced
  * by whole turns in 64-bit integers.  params is read on the host.
@@ -472,8 +474,9 @@ dsa_status dsa_rope(const void* x, int64_t ldx, int64_t hx, const int32_t* posit
  *           none; past the pool: none, and DSA_DEVERR_INDEX.  Slots are distinct.
  * No other overlap of outputs with inputs or with one another.  D <= 256, T * (H + 2 Hkv) <
  * 2^31.  Any element-aligned pointers and strides work, faster under the conditions of
- * dsa_rope.  A head's squares must sum to a finite fp32 (past it y is 0), |y| is the formula's
- * within a few fp32 ulps before the last rounding.
+ * dsa_rope.  A head's squares must sum to a finite fp32 (past it y is 0, or NaN where an element
+ * or its product with the gain is infinite), |y| is the formula's within a few fp32 ulps before
+ * the last rounding.
  */
 dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, int64_t ldk, int Hkv, const void* v,
                             int64_t ldv, int64_t T, int D, dsa_real type, const float* gamma_q, const float* gamma_k,
@@ -505,7 +508,7 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, in
  *           contents on entry do not matter.  Calls that may run at the same time need one each.
  *           The size for some T and B is accepted for every smaller T and B too, although it may
  *           be less than their own: rows then go 128 at a time instead of 256 (a prompt of 8192
- *           tokens 902 us instead of 737), and results may differ in their last bits.
+ *           tokens 908 us instead of 734), and results may differ in their last bits.
  * Pointers of q, out and kv are 16-byte aligned, ldq, ldo and kv's strides multiples of 8,
  * num_blocks at least 1.  The pool is addressed as rows row_stride apart: block_stride is a
  * multiple of row_stride, head_stride smaller than it or a multiple of it, and the pool's rows
