@@ -474,9 +474,9 @@ dsa_status dsa_rope(const void* x, int64_t ldx, int64_t hx, const int32_t* posit
  *           none; past the pool: none, and DSA_DEVERR_INDEX.  Slots are distinct.
  * No other overlap of outputs with inputs or with one another.  D <= 256, T * (H + 2 Hkv) <
  * 2^31.  Any element-aligned pointers and strides work, faster under the conditions of
- * dsa_rope.  A head's squares must sum to a finite fp32 (past it y is 0, or NaN where an element
- * or its product with the gain is infinite), |y| is the formula's within a few fp32 ulps before
- * the last rounding.
+ * dsa_rope.  A head's squares must sum to a finite fp32 and its elements' products with the gain
+ * be finite (past that y is 0, infinite or NaN); |y| is the formula's within a few fp32 ulps
+ * before the last rounding.
  */
 dsa_status dsa_qk_norm_rope(const void* q, int64_t ldq, int H, const void* k, int64_t ldk, int Hkv, const void* v,
                             int64_t ldv, int64_t T, int D, dsa_real type, const float* gamma_q, const float* gamma_k,
